@@ -61,7 +61,12 @@ typedef enum {
   GPTQ_OP_W4A16 = 3,
   GPTQ_OP_ABS = 4,
   GPTQ_OP_AWQ_SEARCH = 5,
-  GPTQ_OP_FORWARD = 6
+  GPTQ_OP_FORWARD = 6,
+  /* 7 names no operation and stays GPTQ_EINVAL */
+  GPTQ_OP_LOGPROBS = 8,
+  GPTQ_OP_DISTILL = 9,
+  GPTQ_OP_LORA = 10,
+  GPTQ_OP_W4A16_LORA = 11
 } gptq_op;
 
 /* Quantizer and schedule parameters.
@@ -120,6 +125,9 @@ const char* gptq_status_string(int32_t status);
  *   GPTQ_OP_AWQ_SEARCH: d_out, d_in, n_rows = sample tokens n_s,
  *                     batch = number of candidate alphas.
  *   GPTQ_OP_FORWARD:  d_out, d_in, n_rows = tokens of one call.
+ *   GPTQ_OP_LOGPROBS: d_in = vocab, n_rows, batch = max(k, 1).
+ *   GPTQ_OP_DISTILL:  d_in = vocab, n_rows, batch = k.
+ *   GPTQ_OP_LORA, GPTQ_OP_W4A16_LORA: d_out, d_in, n_rows = M, batch = rank.
  * Unused arguments are ignored (p may be NULL except for GPTQ_OP_QUANTIZE).
  * Writes *bytes_out (host). */
 gptq_status gptq_workspace_size(int32_t op, const gptq_params* p, int64_t d_out, int64_t d_in,
@@ -364,6 +372,115 @@ gptq_status gptq_layer_forward(const void* X, int32_t x_dtype, int64_t n_tok, in
                                const float* Q, int64_t d_out, int64_t ld_q, int32_t act, void* Y, int64_t ld_y,
                                void* workspace, size_t ws_bytes, void* stream);
 
+/* What a model answers: log probabilities of given tokens, with the entropy
+ * and the k best alternatives of every row of logits.  With z = x / T and
+ * lse = log(sum_j e^(z_j)), in nats:
+ *
+ *   logprob[i] = z[targets[i]] - lse        entropy[i] = lse - sum_j p_j z_j
+ *   top: the k largest logits in descending order, ties to the lower index
+ *        (-0 and +0 tie), as ids and log probabilities z - lse.
+ *
+ *   logits    device, n_rows x vocab of x_dtype, row stride ld_x elements;
+ *             only the elements' own alignment is required (rows that start
+ *             anywhere are read with aligned 16-byte loads inside).
+ *   targets   device int32 [n_rows], or NULL with logprob NULL.  A target
+ *             outside [0, vocab) is a row that is not scored: logprob 0.
+ *   temperature  T, in [1e-4, 1e4] (else GPTQ_EINVAL).
+ *   k         0..128 and <= vocab (k > 128: GPTQ_EUNSUPPORTED).
+ *   logprob, lse, entropy  device fp32 [n_rows]; any of them may be NULL.
+ *   top_logprob, top_id    device fp32 / int32 [n_rows][k]; needed when k > 0.
+ *   workspace GPTQ_OP_LOGPROBS bytes (rows split over workgroups when there
+ *             are few of them); may be NULL when that size is 0.
+ * Masked logits may be -inf or the type's lowest value.  A row of -inf alone
+ * has lse and every log probability -inf, entropy 0 and top ids 0..k-1.  A
+ * row that holds a NaN or +inf has NaN for lse, logprob, entropy and every
+ * top_logprob; its top ids order NaN above +inf.  fp32 sums; the outputs do
+ * not depend on timing (no floating-point atomics). */
+gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, int64_t n_rows, int64_t vocab, int64_t ld_x,
+                                const int32_t* targets, float temperature, int32_t k, float* logprob, float* lse,
+                                float* entropy, float* top_logprob, int32_t* top_id, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Distillation from a teacher's top logits: loss of every row and, when grad
+ * is given, the gradient of sum_i weight[i] loss[i] with respect to the
+ * student's logits, in one call.  z = x / T, q = softmax(z); the teacher's
+ * row lists k ids t_i with log probabilities l_i at the same temperature
+ * (gptq_token_logprobs of the teacher's logits), K the set of listed ids.
+ *
+ *   tail = 1: p_i = e^(l_i); all other tokens are one class with p_r =
+ *     max(0, 1 - sum p_i) and q_r = sum of q outside K:
+ *       loss = sum_i p_i (l_i - log q_i) + p_r (log p_r - log q_r)
+ *       dloss/dx_j = (q_j - p_j) / T in K, q_j (1 - p_r / q_r) / T outside.
+ *   tail = 0: p = softmax of the listed l_i (so l may be raw logits / T):
+ *       loss = sum_i p_i (log p_i - log q_i)
+ *       dloss/dx_j = (q_j - p_j) / T, p_j = 0 outside K.
+ *
+ *   logits      device, n_rows x vocab of x_dtype, row stride ld_x.
+ *   top_id      device int32 [n_rows][k], top_logprob device fp32
+ *               [n_rows][k].  An entry whose id is outside [0, vocab) or
+ *               whose l is -inf is absent (padding of a shorter list); an id
+ *               that comes twice counts at its first place.  A row without
+ *               entries has loss 0 and gradient 0.
+ *   k           1..128 (more: GPTQ_EUNSUPPORTED).
+ *   weight      device fp32 [n_rows] or NULL (all 1).  A row of weight 0 has
+ *               gradient 0, whatever it holds (rows that are padding).
+ *   loss        device fp32 [n_rows], not multiplied by weight; may be NULL
+ *               when grad is given.
+ *   grad        device, n_rows x vocab of x_dtype, row stride ld_g, each
+ *               element rounded once to x_dtype (nearest even); NULL = loss
+ *               only.  It may be the logits' own buffer (grad == logits with
+ *               ld_g == ld_x); otherwise it must not overlap them.
+ *   temperature in [1e-4, 1e4].
+ *   workspace   GPTQ_OP_DISTILL bytes; may be NULL when that size is 0.
+ * q_r is summed over the tail alone, with its own maximum, so a student that
+ * puts nearly all its mass on K keeps it exactly.  A student's row that holds a NaN
+ * or +inf, or nothing above -inf, has loss and gradient NaN (weight 0:
+ * gradient 0).  A listed token that the student masks with -inf while p > 0
+ * gives loss +inf and a finite gradient. */
+gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, int64_t n_rows, int64_t vocab, int64_t ld_x,
+                              const int32_t* top_id, const float* top_logprob, int32_t k, float temperature,
+                              int32_t tail, const float* weight, float* loss, void* grad, int64_t ld_g,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *
+ *   Y[m] = base[m] + scale[a] (X[m] A_a^T) B_a^T,   a = adapter[m].
+ *
+ *   X         device, M x d_in of x_dtype (GPTQ_F16 or GPTQ_BF16), row
+ *             stride ld_x; d_in and ld_x may be odd (16-byte loads are used
+ *             where every row is 16-byte aligned).
+ *   A, B      device, [n_adapters][rank][d_in] and [n_adapters][d_out][rank]
+ *             of x_dtype, dense; 1 <= rank <= 128 (more: GPTQ_EUNSUPPORTED).
+ *             Adapters of smaller rank are padded with zeros.
+ *   scale     device fp32 [n_adapters], or NULL (all 1).
+ *   adapter   device int32 [M]; outside [0, n_adapters): no adapter, Y = base.
+ *   base      device, M x d_out of y_dtype, row stride ld_b, or NULL (zero).
+ *             It may be Y itself (base == Y with ld_b == ld_y).
+ *   Y         device, M x d_out of y_dtype (GPTQ_F32, or x_dtype), row
+ *             stride ld_y.
+ *   workspace GPTQ_OP_LORA bytes, 256-byte aligned; calls sharing one
+ *             workspace must be stream-ordered.
+ * fp32 accumulation; X A^T is kept in fp32 and enters the second product as
+ * two 16-bit terms (16 significant bits in bf16, 22 in fp16); Y is rounded
+ * once.  Any mix of adapters is right; rows of one adapter next to each other
+ * (a request's prompt) share its factors.  M = 0 does nothing. */
+gptq_status gptq_lora_add(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x, const void* A,
+                          const void* B, int64_t n_adapters, int32_t rank, const float* scale,
+                          const int32_t* adapter, const void* base, int64_t ld_b, void* Y, int32_t y_dtype,
+                          int64_t d_out, int64_t ld_y, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same beside the packed 4-bit projection, for up to 64 tokens:
+ *   Y[m] = X[m] Q^T + scale[a] (X[m] A_a^T) B_a^T
+ * with Q, its arguments, limits and errors as in gptq_w4a16_matmul and the
+ * adapters' as in gptq_lora_add (A's columns in the input's own order, also
+ * when perm is given).  workspace: GPTQ_OP_W4A16_LORA bytes. */
+gptq_status gptq_w4a16_lora_matmul(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x,
+                                   const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                                   const int32_t* perm, int64_t d_out, int32_t group_size, const void* A,
+                                   const void* B, int64_t n_adapters, int32_t rank, const float* scale,
+                                   const int32_t* adapter, float* Y, int64_t ld_y, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
 /* Reference rates for measurement (not part of the quantization path): the
  * published peaks of a GPU are not what it sustains under a given load, so
  * the benchmark also measures two simple kernels on the same device.  Both
@@ -393,7 +510,8 @@ gptq_status gptq_probe_copy(const void* src, void* dst, size_t bytes, double* gb
  * kernels, 3 = block quantization, 4 = deferred update GEMM, 5 = packing,
  * 6 = working-copy preparation, 7 = reduction of split Hessian partials,
  * 8 / 9 = W4A16 staging / main kernel, 10 = |x| sums, 11 = scale search,
- * 12 = scale application, 13 = layer forward).  gptq_timing_read synchronizes those events
+ * 12 = scale application, 13 = layer forward, 14 = token log probabilities,
+ * 15 = distillation, 16 = low-rank adapters).  gptq_timing_read synchronizes those events
  * and reports the summed duration (ms) and launch count of `kind`; reset
  * drops all records.  Not thread safe; off by default. */
 gptq_status gptq_timing_enable(int32_t on);

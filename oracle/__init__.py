@@ -12,5 +12,7 @@ from .awq import *  # noqa: F401,F403
 from .awq import __all__ as _awq_all
 from .chain import *  # noqa: F401,F403
 from .chain import __all__ as _chain_all
+from .answers import *  # noqa: F401,F403
+from .answers import __all__ as _answers_all
 
-__all__ = list(_gptq_all) + list(_w4a16_all) + list(_awq_all) + list(_chain_all)
+__all__ = list(_gptq_all) + list(_w4a16_all) + list(_awq_all) + list(_chain_all) + list(_answers_all)

@@ -22,11 +22,14 @@ __all__ = [
     "gptq_timing_reset", "gptq_timing_read", "gptq_pack_int4_permuted", "gptq_w4a16_matmul",
     "gptq_abs_accumulate", "gptq_awq_search", "gptq_awq_apply", "gptq_layer_forward",
     "gptq_probe_mfma", "gptq_probe_copy", "gptq_probe_sink_bytes", "gptq_w4a16_matmul_noalloc",
+    "gptq_token_logprobs", "gptq_distill_topk", "gptq_lora_add", "gptq_w4a16_lora_matmul",
     "ACT_NONE", "ACT_RELU", "ACT_SILU",
     "OP_HESSIAN", "OP_PREPARE", "OP_QUANTIZE", "OP_W4A16", "OP_ABS", "OP_AWQ_SEARCH", "OP_FORWARD",
+    "OP_LOGPROBS", "OP_DISTILL", "OP_LORA", "OP_W4A16_LORA",
     "TIME_SYRK", "TIME_DIAG", "TIME_FACTOR", "TIME_BLOCK_QUANT", "TIME_TRAILING",
     "TIME_PACK", "TIME_PREP", "TIME_SYRK_REDUCE", "TIME_W4_STAGE", "TIME_W4_MAIN", "TIME_ABS",
-    "TIME_AWQ_SEARCH", "TIME_AWQ_APPLY", "TIME_FORWARD", "dtype_code", "LIB_PATH",
+    "TIME_AWQ_SEARCH", "TIME_AWQ_APPLY", "TIME_FORWARD", "TIME_LOGPROBS", "TIME_DISTILL", "TIME_LORA",
+    "dtype_code", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
@@ -34,9 +37,11 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so"
 OK, EINVAL, ENOTPD, EHIP, EUNSUPPORTED, ENOMEM = range(6)
 F32, F16, BF16 = 0, 1, 2
 OP_HESSIAN, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_ABS, OP_AWQ_SEARCH, OP_FORWARD = 0, 1, 2, 3, 4, 5, 6
+OP_LOGPROBS, OP_DISTILL, OP_LORA, OP_W4A16_LORA = 8, 9, 10, 11
 ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2
 (TIME_SYRK, TIME_DIAG, TIME_FACTOR, TIME_BLOCK_QUANT, TIME_TRAILING, TIME_PACK, TIME_PREP,
- TIME_SYRK_REDUCE, TIME_W4_STAGE, TIME_W4_MAIN, TIME_ABS, TIME_AWQ_SEARCH, TIME_AWQ_APPLY, TIME_FORWARD) = range(14)
+ TIME_SYRK_REDUCE, TIME_W4_STAGE, TIME_W4_MAIN, TIME_ABS, TIME_AWQ_SEARCH, TIME_AWQ_APPLY, TIME_FORWARD,
+ TIME_LOGPROBS, TIME_DISTILL, TIME_LORA) = range(17)
 
 
 class GptqError(RuntimeError):
@@ -99,6 +104,17 @@ def _load() -> ctypes.CDLL:
     L.gptq_probe_copy.argtypes = [vp, vp, sz, P(ctypes.c_double), P(ctypes.c_double), vp]
     L.gptq_w4a16_matmul_noalloc.restype = i32
     L.gptq_w4a16_matmul_noalloc.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, i32, vp, i64, vp]
+    f32 = ctypes.c_float
+    L.gptq_token_logprobs.restype = i32
+    L.gptq_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.gptq_distill_topk.restype = i32
+    L.gptq_distill_topk.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp, sz, vp]
+    L.gptq_lora_add.restype = i32
+    L.gptq_lora_add.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, vp, vp, i64, vp, i32, i64, i64, vp, sz,
+                                vp]
+    L.gptq_w4a16_lora_matmul.restype = i32
+    L.gptq_w4a16_lora_matmul.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, i32, vp, vp, i64, i32, vp, vp,
+                                         vp, i64, vp, sz, vp]
     L.gptq_timing_enable.restype = i32
     L.gptq_timing_enable.argtypes = [i32]
     L.gptq_timing_reset.restype = i32
@@ -270,6 +286,43 @@ def gptq_layer_forward(X, x_dtype: int, n_tok: int, d_in: int, ld_x: int, Q, d_o
                        ld_y: int, workspace, ws_bytes: int, stream=None) -> None:
     _check(lib.gptq_layer_forward(_ptr(X), x_dtype, n_tok, d_in, ld_x, _ptr(Q), d_out, ld_q, act, _ptr(Y), ld_y,
                                   _ptr(workspace), ws_bytes, _stream(stream)), "gptq_layer_forward")
+
+
+def gptq_token_logprobs(logits, x_dtype: int, n_rows: int, vocab: int, ld_x: int, targets, temperature: float, k: int,
+                        logprob, lse, entropy, top_logprob, top_id, workspace=None, ws_bytes: int = 0,
+                        stream=None) -> None:
+    """Log probabilities of the targets, lse, entropy and the k best alternatives of every row of logits."""
+    _check(lib.gptq_token_logprobs(_ptr(logits), x_dtype, n_rows, vocab, ld_x, _ptr(targets), temperature, k,
+                                   _ptr(logprob), _ptr(lse), _ptr(entropy), _ptr(top_logprob), _ptr(top_id),
+                                   _ptr(workspace), ws_bytes, _stream(stream)), "gptq_token_logprobs")
+
+
+def gptq_distill_topk(logits, x_dtype: int, n_rows: int, vocab: int, ld_x: int, top_id, top_logprob, k: int,
+                      temperature: float, tail: bool, weight, loss, grad, ld_g: int, workspace=None, ws_bytes: int = 0,
+                      stream=None) -> None:
+    """Loss of every row against a teacher's top list and the gradient of sum(weight * loss)."""
+    _check(lib.gptq_distill_topk(_ptr(logits), x_dtype, n_rows, vocab, ld_x, _ptr(top_id), _ptr(top_logprob), k,
+                                 temperature, int(tail), _ptr(weight), _ptr(loss), _ptr(grad), ld_g, _ptr(workspace),
+                                 ws_bytes, _stream(stream)), "gptq_distill_topk")
+
+
+def gptq_lora_add(X, x_dtype: int, M: int, d_in: int, ld_x: int, A, B, n_adapters: int, rank: int, scale, adapter,
+                  base, ld_b: int, Y, y_dtype: int, d_out: int, ld_y: int, workspace, ws_bytes: int,
+                  stream=None) -> None:
+    """Y = base + scale[a] (X A_a^T) B_a^T with a = adapter[m] for every row m."""
+    _check(lib.gptq_lora_add(_ptr(X), x_dtype, M, d_in, ld_x, _ptr(A), _ptr(B), n_adapters, rank, _ptr(scale),
+                             _ptr(adapter), _ptr(base), ld_b, _ptr(Y), y_dtype, d_out, ld_y, _ptr(workspace), ws_bytes,
+                             _stream(stream)), "gptq_lora_add")
+
+
+def gptq_w4a16_lora_matmul(X, x_dtype: int, M: int, d_in: int, ld_x: int, qweight, scales, zeros, perm, d_out: int,
+                           group_size: int, A, B, n_adapters: int, rank: int, scale, adapter, Y, ld_y: int, workspace,
+                           ws_bytes: int, stream=None) -> None:
+    """Y = X Q^T from the packed 4-bit weights plus each row's adapter."""
+    _check(lib.gptq_w4a16_lora_matmul(_ptr(X), x_dtype, M, d_in, ld_x, _ptr(qweight), _ptr(scales), _ptr(zeros),
+                                      _ptr(perm), d_out, group_size, _ptr(A), _ptr(B), n_adapters, rank, _ptr(scale),
+                                      _ptr(adapter), _ptr(Y), ld_y, _ptr(workspace), ws_bytes, _stream(stream)),
+           "gptq_w4a16_lora_matmul")
 
 
 def gptq_timing_enable(on: bool) -> None:

@@ -10,6 +10,10 @@ size_t w4a16_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out);
 size_t abs_workspace_bytes(int64_t d, int64_t n_rows);
 size_t awq_search_workspace_bytes(int64_t d_out, int64_t d_in, int64_t n_s, int64_t n_alpha);
 size_t forward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t d_out);
+size_t logprobs_workspace_bytes(int64_t n_rows, int64_t vocab, int64_t k);
+size_t distill_workspace_bytes(int64_t n_rows, int64_t vocab, int64_t k);
+size_t lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank);
+size_t w4a16_lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank);
 
 // ---------------------------------------------------------------- timing state
 namespace {
@@ -100,6 +104,22 @@ extern "C" gptq_status gptq_workspace_size(int32_t op, const gptq_params* p, int
     case GPTQ_OP_FORWARD:
       GQ_CHECK_ARG(d_out >= 1 && n_rows >= 0);
       *bytes_out = forward_workspace_bytes(n_rows, d_in, d_out);
+      return GPTQ_OK;
+    case GPTQ_OP_LOGPROBS:
+      GQ_CHECK_ARG(n_rows >= 0 && batch <= 128);
+      *bytes_out = logprobs_workspace_bytes(n_rows, d_in, batch);
+      return GPTQ_OK;
+    case GPTQ_OP_DISTILL:
+      GQ_CHECK_ARG(n_rows >= 0 && batch <= 128);
+      *bytes_out = distill_workspace_bytes(n_rows, d_in, batch);
+      return GPTQ_OK;
+    case GPTQ_OP_LORA:
+      GQ_CHECK_ARG(n_rows >= 0 && d_out >= 1 && batch <= 128);
+      *bytes_out = lora_workspace_bytes(n_rows, d_in, d_out, batch);
+      return GPTQ_OK;
+    case GPTQ_OP_W4A16_LORA:
+      GQ_CHECK_ARG(n_rows >= 1 && d_out >= 1 && batch <= 128);
+      *bytes_out = w4a16_lora_workspace_bytes(n_rows, d_in, d_out, batch);
       return GPTQ_OK;
     default:
       return GPTQ_EINVAL;

@@ -57,7 +57,10 @@ enum TimedKind {
   kTimeAwqSearch = 11,
   kTimeAwqApply = 12,
   kTimeForward = 13,
-  kTimeKinds = 14
+  kTimeLogprobs = 14,
+  kTimeDistill = 15,
+  kTimeLora = 16,
+  kTimeKinds = 17
 };
 
 // Records a start event before and a stop event after a launch when timing

@@ -5,15 +5,18 @@ one of the library's entry points.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Dict, Optional, Sequence
 
 import numpy as np
 import torch
 
-from . import (F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_FORWARD, OP_HESSIAN, OP_PREPARE, OP_QUANTIZE, OP_W4A16,
-               ENOTPD, dtype_code, gptq_abs_accumulate, gptq_awq_apply, gptq_awq_search, gptq_hessian_accumulate,
-               gptq_layer_forward, gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv,
-               gptq_quantize_layer, gptq_w4a16_matmul, gptq_workspace_size)
+from . import (F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD, OP_HESSIAN, OP_LOGPROBS, OP_LORA,
+               OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, dtype_code, gptq_abs_accumulate,
+               gptq_awq_apply, gptq_awq_search, gptq_distill_topk, gptq_hessian_accumulate, gptq_layer_forward,
+               gptq_lora_add, gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv,
+               gptq_quantize_layer, gptq_token_logprobs, gptq_w4a16_lora_matmul, gptq_w4a16_matmul,
+               gptq_workspace_size)
 
 
 def to_device(arr: np.ndarray, dtype: str, device="cuda") -> torch.Tensor:
@@ -21,6 +24,13 @@ def to_device(arr: np.ndarray, dtype: str, device="cuda") -> torch.Tensor:
     if dtype == "bf16":
         return torch.from_numpy(np.ascontiguousarray(arr).view(np.int16)).to(device).view(torch.bfloat16)
     return torch.from_numpy(np.ascontiguousarray(arr)).to(device)
+
+
+def _on(stream):
+    """Context in which what torch allocates belongs to the call's stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -187,6 +197,170 @@ def layer_forward(X: torch.Tensor, Q: torch.Tensor, act: int, Y: Optional[torch.
         ws = _ws(need, X.device)
     gptq_layer_forward(X, dtype_code(X.dtype), n, d_in, X.stride(0), Q, d_out, Q.stride(0), act, Y, Y.stride(0),
                        ws, ws.numel(), stream)
+    return Y
+
+
+def _rows(t: torch.Tensor, what: str) -> torch.Tensor:
+    if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{what}: a 2-d tensor with contiguous, disjoint rows is needed")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; a single row may carry any, so its width counts."""
+    return max(t.stride(0), t.shape[1])
+
+
+def _dense(t: Optional[torch.Tensor], dtype, shape, what: str, like: torch.Tensor) -> Optional[torch.Tensor]:
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+                          or t.device != like.device):
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device} is needed")
+    return t
+
+
+def token_logprobs_buffers(logits: torch.Tensor, k: int = 0):
+    """(out, ws) of a token_logprobs call with these sizes, to be kept from call to call."""
+    n, v = logits.shape
+    dev = logits.device
+    out = {name: torch.empty(n, dtype=torch.float32, device=dev) for name in ("logprob", "lse", "entropy")}
+    out["top_logprob"] = torch.empty(n, k, dtype=torch.float32, device=dev)
+    out["top_id"] = torch.empty(n, k, dtype=torch.int32, device=dev)
+    return out, _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), dev)
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, k: int = 0, temperature: float = 1.0,
+                   out: Optional[Dict[str, torch.Tensor]] = None, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> Dict[str, torch.Tensor]:
+    """Log probability of targets[i] (int32; outside the vocabulary: not scored, 0), log-sum-exp, entropy and the k
+    best alternatives (log probabilities and ids, ties to the lower id) of every row of logits at a temperature.
+    Without targets the logprob entry of the result is not written."""
+    n, v = _rows(logits, "logits").shape
+    _dense(targets, torch.int32, (n,), "targets", logits)
+    if out is None:
+        with _on(stream):
+            out = token_logprobs_buffers(logits, k)[0]
+    for name in ("logprob", "lse", "entropy"):
+        _dense(out[name], torch.float32, (n,), name, logits)
+    _dense(out["top_logprob"], torch.float32, (n, k), "top_logprob", logits)
+    _dense(out["top_id"], torch.int32, (n, k), "top_id", logits)
+    if ws is None:
+        with _on(stream):
+            ws = _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), logits.device)
+    gptq_token_logprobs(logits, dtype_code(logits.dtype), n, v, _ld(logits), targets, temperature, k,
+                        out["logprob"] if targets is not None else None, out["lse"], out["entropy"],
+                        out["top_logprob"], out["top_id"], ws, ws.numel(), stream)
+    return out
+
+
+def distill_topk_buffers(logits: torch.Tensor, k: int, want_grad: bool = True):
+    """(out, ws) of a distill_topk call with these sizes, to be kept from call to call."""
+    n, v = logits.shape
+    out = {"loss": torch.empty(n, dtype=torch.float32, device=logits.device)}
+    if want_grad:
+        out["grad"] = torch.empty(n, v, dtype=logits.dtype, device=logits.device)
+    return out, _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device)
+
+
+def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.Tensor, temperature: float = 1.0,
+                 tail: bool = True, weight: Optional[torch.Tensor] = None, want_grad: bool = True,
+                 out: Optional[Dict[str, torch.Tensor]] = None, ws: Optional[torch.Tensor] = None,
+                 stream=None) -> Dict[str, torch.Tensor]:
+    """Loss of every row of the student's logits against the teacher's top list (int32 ids, fp32 log probabilities
+    at the same temperature) and, with want_grad, the gradient of sum(weight * loss) in the logits' type.  out may
+    hold the logits themselves as "grad": the gradient then replaces them."""
+    n, v = _rows(logits, "logits").shape
+    k = top_id.shape[-1]
+    _dense(top_id, torch.int32, (n, k), "top_id", logits)
+    _dense(top_logprob, torch.float32, (n, k), "top_logprob", logits)
+    _dense(weight, torch.float32, (n,), "weight", logits)
+    if out is None:
+        with _on(stream):
+            out = distill_topk_buffers(logits, k, want_grad)[0]
+    _dense(out["loss"], torch.float32, (n,), "loss", logits)
+    grad = None
+    if want_grad:
+        grad = _rows(out["grad"], "grad")
+        if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.device != logits.device:
+            raise ValueError("grad: the logits' type, shape and device are needed")
+    if ws is None:
+        with _on(stream):
+            ws = _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device)
+    gptq_distill_topk(logits, dtype_code(logits.dtype), n, v, _ld(logits), top_id, top_logprob, k, temperature, tail,
+                      weight, out["loss"], grad, _ld(grad) if grad is not None else v, ws, ws.numel(), stream)
+    return out
+
+
+def _adapters(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, scale):
+    n, r, d_in = A.shape
+    M = _rows(X, "X").shape[0]
+    _dense(A, X.dtype, (n, r, X.shape[1]), "A", X)
+    _dense(B, X.dtype, (n, B.shape[1], r), "B", X)
+    _dense(adapter, torch.int32, (M,), "adapter", X)
+    _dense(scale, torch.float32, (n,), "scale", X)
+    return M, n, r, d_in, B.shape[1]
+
+
+def _rows_like(t: torch.Tensor, dtype, shape, what: str, like: torch.Tensor) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != like.device:
+        raise ValueError(f"{what}: a {dtype} tensor of shape {tuple(shape)} on {like.device} is needed")
+    return _rows(t, what)
+
+
+def lora_buffers(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, y_dtype=torch.float32):
+    """(Y, ws) of a lora_add call with these sizes, to be kept from call to call."""
+    M, d_in = X.shape
+    d_out, r = B.shape[1], B.shape[2]
+    return (torch.empty(M, d_out, dtype=y_dtype, device=X.device),
+            _ws(gptq_workspace_size(OP_LORA, None, d_out, d_in, M, r), X.device))
+
+
+def lora_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor,
+             scale: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+             Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[m] = base[m] + scale[a] (X[m] A_a^T) B_a^T, a = adapter[m] (int32; outside the adapters: none).  A is
+    (n, rank, d_in), B (n, d_out, rank) in X's type; Y fp32 or X's type, base in Y's type; Y may be base itself."""
+    M, n, r, d_in, d_out = _adapters(X, A, B, adapter, scale)
+    if Y is None:
+        with _on(stream):
+            Y = torch.empty(M, d_out, dtype=base.dtype if base is not None else torch.float32, device=X.device)
+    _rows_like(Y, Y.dtype, (M, d_out), "Y", X)
+    if base is not None:
+        _rows_like(base, Y.dtype, (M, d_out), "base", X)
+    if ws is None:
+        with _on(stream):
+            ws = _ws(gptq_workspace_size(OP_LORA, None, d_out, d_in, M, r), X.device)
+    gptq_lora_add(X, dtype_code(X.dtype), M, d_in, _ld(X), A, B, n, r, scale, adapter, base,
+                  _ld(base) if base is not None else d_out, Y, dtype_code(Y.dtype), d_out, _ld(Y), ws, ws.numel(),
+                  stream)
+    return Y
+
+
+def w4a16_lora_buffers(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor):
+    """(Y, ws) of a w4a16_lora_matmul call with these sizes, to be kept from call to call."""
+    M, d_in = X.shape
+    d_out, r = B.shape[1], B.shape[2]
+    return (torch.empty(M, d_out, dtype=torch.float32, device=X.device),
+            _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, M, r), X.device))
+
+
+def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                      group_size: int, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor,
+                      scale: Optional[torch.Tensor] = None, perm: Optional[torch.Tensor] = None,
+                      Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """w4a16_matmul (up to 64 tokens) plus every token's adapter, as lora_add adds it."""
+    M, n, r, d_in, d_out = _adapters(X, A, B, adapter, scale)
+    if qweight.shape[0] != d_out or qweight.shape[1] * 2 != d_in:
+        raise ValueError("qweight: its rows and columns must match B and X")
+    if Y is None:
+        with _on(stream):
+            Y = torch.empty(M, d_out, dtype=torch.float32, device=X.device)
+    _rows_like(Y, torch.float32, (M, d_out), "Y", X)
+    if ws is None:
+        with _on(stream):
+            ws = _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, M, r), X.device)
+    gptq_w4a16_lora_matmul(X, dtype_code(X.dtype), M, d_in, _ld(X), qweight, scales, zeros, perm, d_out, group_size,
+                           A, B, n, r, scale, adapter, Y, _ld(Y), ws, ws.numel(), stream)
     return Y
 
 

@@ -1,0 +1,248 @@
+"""Low-rank adapters beside a projection on the GPU against the float64
+oracle, element by element within the bound of tests/answer_data.py."""
+import numpy as np
+import pytest
+
+import oracle as O
+import synth
+from tests import answer_data as D
+from tests.gpu_run import log
+from tests.parity import w4a16_error_bound
+
+pytestmark = pytest.mark.gpu
+
+
+def _assign(M, n, how, r):
+    if how == "runs":
+        cut = np.sort(r.integers(0, M + 1, 2 * n))
+        a = np.searchsorted(cut, np.arange(M), side="right") % (n + 1)
+        return np.where(a == n, -1, a).astype(np.int32)
+    if how == "none":
+        return np.full(M, -1, np.int32)
+    if how == "one":
+        return np.full(M, n - 1, np.int32)
+    a = r.integers(-1, n + 1, M)                          # -1 and n: no adapter
+    return a.astype(np.int32)
+
+
+def _place(t, ld, offset, fill):
+    import torch
+    M, w = t.shape
+    buf = torch.full((offset + M * ld,), fill, dtype=t.dtype, device="cuda")
+    view = buf.as_strided((M, w), (ld, 1), offset)
+    view.copy_(t)
+    return buf, view
+
+
+def _check(M, d_in, d_out, rank, n, xdt, ydt, how, base="given", scaled=True, pad=0, off=0, seed=1):
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+
+    r = np.random.default_rng([98, M, d_in, d_out, rank, seed])
+    Xs, As, Bs, s = D.adapters(M, d_in, d_out, rank, n, xdt, seed)
+    a = _assign(M, n, how, r)
+    bs = D.store(r.standard_normal((M, d_out)), ydt)
+    scale = s if scaled else None
+    _, X = _place(D.to_torch(Xs, xdt), d_in + pad, off, 9.0)
+    A, B = D.to_torch(As, xdt), D.to_torch(Bs, xdt)
+    sd = torch.from_numpy(s).cuda() if scaled else None
+    ybuf, Y = _place(D.to_torch(bs, ydt), d_out + pad, off, 77.0)
+    bd = None if base == "none" else Y if base == "inplace" else _place(Y, d_out + pad + 1, 0, 5.0)[1]
+    if base != "inplace":
+        Y.fill_(float("nan"))
+    P.lora_add(X, A, B, torch.from_numpy(a).cuda(), sd, base=bd, Y=Y)
+    torch.cuda.synchronize()
+    keep = torch.ones(ybuf.numel(), dtype=torch.bool, device="cuda")
+    keep.as_strided((M, d_out), Y.stride(), Y.storage_offset()).fill_(False)
+    assert bool(((ybuf == 77.0) | ~keep).all())
+    got = Y.float().cpu().numpy().astype(np.float64)
+    Xf, Af, Bf = D.exact(Xs, xdt), D.exact(As, xdt), D.exact(Bs, xdt)
+    want = O.lora(Xf, Af, Bf, a, scale, None if base == "none" else D.exact(bs, ydt))
+    tol = D.lora_bound(Xf, Af, Bf, a, scale, want, xdt, ydt)
+    if base == "none":
+        off_rows = (a < 0) | (a >= n)
+        assert np.all(got[off_rows] == 0.0)
+    err = np.abs(got - want)
+    worst = float(np.max(err / np.maximum(tol, 1e-300)))
+    log(f"[gpu] lora {M}x{d_in}->{d_out} r={rank} n={n} {xdt}/{ydt} {how}: worst error / bound {worst:.3f}")
+    assert np.all(err <= tol), worst
+
+
+# (M, d_in, d_out, rank, adapters, X type, Y type, assignment)
+CASES = [
+    (1, 128, 64, 8, 1, "f16", "f32", "one"),
+    (1, 1, 1, 1, 1, "bf16", "f32", "one"),
+    (1, 4096, 1000, 16, 3, "bf16", "bf16", "one"),
+    (2, 96, 33, 3, 2, "f16", "f16", "mixed"),
+    (7, 513, 130, 5, 4, "bf16", "f32", "mixed"),
+    (16, 1000, 257, 16, 16, "f16", "f32", "mixed"),
+    (17, 1024, 1024, 32, 5, "bf16", "f32", "mixed"),
+    (48, 2048, 700, 64, 48, "bf16", "f32", "mixed"),
+    (64, 1024, 513, 128, 3, "f16", "f32", "runs"),
+    (64, 1024, 512, 16, 2, "bf16", "bf16", "none"),
+    (65, 264, 1000, 24, 4, "f16", "f16", "runs"),
+    (130, 3333, 641, 8, 6, "bf16", "f32", "runs"),
+    (300, 1024, 2000, 32, 4, "bf16", "bf16", "runs"),
+    (300, 1024, 96, 32, 40, "f16", "f32", "mixed"),
+    (1000, 520, 1031, 64, 8, "f16", "f32", "runs"),
+    (1000, 136, 264, 100, 3, "bf16", "bf16", "one"),
+    (2049, 256, 384, 16, 9, "bf16", "f32", "runs"),
+]
+
+
+@pytest.mark.parametrize("M,d_in,d_out,rank,n,xdt,ydt,how", CASES)
+def test_lora_matches_the_oracle(M, d_in, d_out, rank, n, xdt, ydt, how):
+    _check(M, d_in, d_out, rank, n, xdt, ydt, how)
+
+
+@pytest.mark.parametrize("base", ["none", "inplace", "given"])
+@pytest.mark.parametrize("pad,off", [(0, 0), (8, 0), (3, 1), (0, 5)])
+def test_lora_bases_strides_and_starts(base, pad, off):
+    for M, xdt, ydt in ((5, "bf16", "f32"), (90, "f16", "f16")):
+        _check(M, 640, 328, 16, 4, xdt, ydt, "mixed", base=base, pad=pad, off=off)
+        _check(M, 640, 328, 16, 4, xdt, ydt, "runs", base=base, pad=pad, off=off, scaled=False)
+
+
+def test_lora_factors_that_start_anywhere():
+    """A and B at addresses that are only their elements' own multiples."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    for M in (3, 100):
+        Xs, As, Bs, s = D.adapters(M, 256, 192, 16, 3, "bf16", 5)
+        a = (np.arange(M) % 3).astype(np.int32)
+        X, A, B = (D.to_torch(t, "bf16") for t in (Xs, As, Bs))
+        ad, sd = torch.from_numpy(a).cuda(), torch.from_numpy(s).cuda()
+
+        def shifted(t):
+            buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+            buf[1:].copy_(t.flatten())
+            return buf[1:].view(t.shape)
+        Xf, Af, Bf = D.exact(Xs, "bf16"), D.exact(As, "bf16"), D.exact(Bs, "bf16")
+        want = O.lora(Xf, Af, Bf, a, s)
+        tol = D.lora_bound(Xf, Af, Bf, a, s, want, "bf16", "f32")
+        for args in ((X, shifted(A), B), (X, A, shifted(B)), (X, shifted(A), shifted(B))):
+            got = P.lora_add(*args, ad, sd).double().cpu().numpy()
+            assert np.all(np.abs(got - want) <= tol)
+
+
+def test_rows_without_an_adapter_ignore_what_they_hold():
+    """NaN in a row without an adapter, or in an adapter nobody uses, reaches no other output."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    for M in (6, 80):
+        Xs, As, Bs, s = D.adapters(M, 256, 160, 8, 4, "bf16", 6)
+        X, A, B = (D.to_torch(t, "bf16") for t in (Xs, As, Bs))
+        a = np.where(np.arange(M) % 3 == 1, -1, np.arange(M) % 3).astype(np.int32)
+        ad, sd = torch.from_numpy(a).cuda(), torch.from_numpy(s).cuda()
+        clean = P.lora_add(X, A, B, ad, sd)
+        X2, A2, B2 = X.clone(), A.clone(), B.clone()
+        X2[1::3] = float("nan")
+        A2[3], B2[3] = float("nan"), float("inf")
+        A2[1], B2[1] = float("inf"), float("nan")
+        got = P.lora_add(X2, A2, B2, ad, sd)
+        assert torch.equal(clean, got)
+        X2[0] = float("inf")                              # a broken row of an adapter its neighbours share
+        got = P.lora_add(X2, A, B, ad, sd)
+        assert torch.equal(clean[1:], got[1:]) and not torch.isfinite(got[0]).all()
+
+
+def test_lora_past_4_gib():
+    """Rows of X and Y beyond 2^32 bytes and 2^31 elements."""
+    import torch
+    _check(5, 256, 200, 16, 3, "bf16", "f32", "mixed", base="inplace", pad=(1 << 29) + 7)
+    torch.cuda.empty_cache()
+    _check(70, 256, 200, 16, 3, "f16", "f16", "runs", base="inplace", pad=(1 << 25) + 8)
+    torch.cuda.empty_cache()
+
+
+# (d_out, d_in, M, g, type, act-order, rank, adapters)
+W4_CASES = [
+    (64, 1024, 1, 128, "f16", False, 8, 1),
+    (1, 128, 1, 128, "bf16", False, 1, 1),
+    (1000, 2048, 3, 128, "bf16", True, 16, 5),
+    (300, 1024, 17, 256, "f16", False, 32, 9),
+    (70, 384, 33, 128, "bf16", False, 5, 40),
+    (515, 4096, 48, 128, "bf16", True, 64, 6),
+    (2000, 1024, 64, 1024, "f16", True, 16, 64),
+    (130, 512, 64, 128, "bf16", False, 128, 2),
+]
+
+
+@pytest.mark.parametrize("d_out,d_in,m,g,xdt,act_order,rank,n", W4_CASES)
+def test_w4a16_lora_matches_the_oracle(d_out, d_in, m, g, xdt, act_order, rank, n):
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+
+    i = W4_CASES.index((d_out, d_in, m, g, xdt, act_order, rank, n))
+    cfg = synth.CONFIGS["up_proj_70b"].scaled(f"w4lora:{i}", 500 + i, d_out=d_out, d_in=d_in, group_size=g, x_dtype=xdt)
+    codes, scales, zeros, perm, g_idx = synth.w4_layer(cfg, act_order, 0)
+    Xs, As, Bs, s = D.adapters(m, d_in, d_out, rank, n, xdt, 7)
+    a = _assign(m, n, "mixed", np.random.default_rng([99, i]))
+    X, A, B = (D.to_torch(t, xdt) for t in (Xs, As, Bs))
+    cd = torch.from_numpy(codes).cuda()
+    pd = torch.from_numpy(perm).cuda() if perm is not None else None
+    qw = P.pack_int4_permuted(cd, pd) if pd is not None else P.pack(cd, 4)
+    sc, zd = torch.from_numpy(scales.view(np.int16)).cuda(), torch.from_numpy(zeros).cuda()
+    args = (X, qw, sc, zd, g, A, B, torch.from_numpy(a).cuda(), torch.from_numpy(s).cuda())
+    Y = P.w4a16_lora_matmul(*args, perm=pd)
+    again = P.w4a16_lora_matmul(*args, perm=pd)
+    assert torch.equal(Y, again)
+    Xf, Af, Bf = D.exact(Xs, xdt), D.exact(As, xdt), D.exact(Bs, xdt)
+    s32 = scales.view(np.float16).astype(np.float32)
+    base = O.w4a16_matmul(Xf, O.pack_int4(codes), s32, zeros, g_idx)
+    want = O.lora(Xf, Af, Bf, a, s, base)
+    tol = (w4a16_error_bound(Xf, codes, s32, zeros, g_idx, bias=128.0 if xdt == "bf16" else 0.0)
+           + D.lora_bound(Xf, Af, Bf, a, s, want, xdt, "f32"))
+    err = np.abs(Y.double().cpu().numpy() - want)
+    log(f"[gpu] w4a16 lora {d_out}x{d_in} M={m} r={rank} n={n} {xdt}: worst error / bound {np.max(err / tol):.3f}")
+    assert np.all(err <= tol)
+    # the projection's own part is w4a16_matmul's, bit for bit, where no adapter acts
+    plain = P.w4a16_matmul(X, qw, sc, zd, g, perm=pd)
+    none = torch.from_numpy((a < 0) | (a >= n)).cuda()
+    assert torch.equal(plain[none], Y[none])
+
+
+def test_lora_in_a_graph_and_on_another_stream():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    for M in (5, 200):
+        Xs, As, Bs, s = D.adapters(M, 512, 300, 16, 4, "bf16", 8)
+        X, A, B = (D.to_torch(t, "bf16") for t in (Xs, As, Bs))
+        ad = torch.from_numpy((np.arange(M) // 7 % 5 - 1).astype(np.int32)).cuda()
+        sd = torch.from_numpy(s).cuda()
+        base = torch.randn(M, 300, device="cuda")
+        a = P.lora_add(X, A, B, ad, sd, base=base)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        b = P.lora_add(X, A, B, ad, sd, base=base, stream=side)
+        side.synchronize()
+        assert torch.equal(a, b)
+        Y, ws = P.lora_buffers(X, A, B)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            P.lora_add(X, A, B, ad, sd, base=base, Y=Y, ws=ws)
+        for r in range(4):
+            Y.fill_(5)
+            ws.fill_(255 if r % 2 else 0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(a, Y), r
+
+
+def test_lora_wrappers_refuse_wrong_tensors():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    X = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    A = torch.zeros(2, 8, 256, dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros(2, 96, 8, dtype=torch.bfloat16, device="cuda")
+    ad = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in ((X.half(), A, B, ad), (X, A[:, :, :128], B, ad), (X, A, B[:, :, :4], ad), (X, A, B, ad.long()),
+                (X, A, B, ad[:3].contiguous()), (X, A, B, ad.cpu())):
+        with pytest.raises(ValueError):
+            P.lora_add(*bad)
+    with pytest.raises(ValueError):
+        P.lora_add(X, A, B, ad, base=torch.zeros(4, 96, device="cuda"), Y=torch.zeros(4, 96, device="cuda").bfloat16())
+    with pytest.raises(P.GptqError):
+        P.lora_add(X, A, B, ad, Y=torch.zeros(4, 96, device="cuda").half())
+    with pytest.raises(P.GptqError):
+        P.lora_add(X, A, B, ad, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
