@@ -381,6 +381,7 @@ gptq_status gptq_layer_forward(const void* X, int32_t x_dtype, int64_t n_tok, in
  *        (-0 and +0 tie), as ids and log probabilities z - lse.
  *
  *   logits    device, n_rows x vocab of x_dtype, row stride ld_x elements;
+ *             vocab <= 2^21 (more: GPTQ_EUNSUPPORTED);
  *             only the elements' own alignment is required (rows that start
  *             anywhere are read with aligned 16-byte loads inside).
  *   targets   device int32 [n_rows], or NULL with logprob NULL.  A target
@@ -389,8 +390,8 @@ gptq_status gptq_layer_forward(const void* X, int32_t x_dtype, int64_t n_tok, in
  *   k         0..128 and <= vocab (k > 128: GPTQ_EUNSUPPORTED).
  *   logprob, lse, entropy  device fp32 [n_rows]; any of them may be NULL.
  *   top_logprob, top_id    device fp32 / int32 [n_rows][k]; needed when k > 0.
- *   workspace GPTQ_OP_LOGPROBS bytes (rows split over workgroups when there
- *             are few of them); may be NULL when that size is 0.
+ *   workspace GPTQ_OP_LOGPROBS bytes, 256-byte aligned (rows split over
+ *             workgroups when there are few); may be NULL when that size is 0.
  * Masked logits may be -inf or the type's lowest value.  A row of -inf alone
  * has lse and every log probability -inf, entropy 0 and top ids 0..k-1.  A
  * row that holds a NaN or +inf has NaN for lse, logprob, entropy and every

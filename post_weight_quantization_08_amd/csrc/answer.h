@@ -43,4 +43,90 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
 
 __device__ __forceinline__ uint32_t index_of(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
 
+// ---------------------------------------------------------------- rows in blocks
+// A row is walked in 16-byte blocks on 16-byte addresses, wherever it starts:
+// block b holds elements b E - h .. b E - h + E - 1, E elements of a block, h
+// the elements between the boundary below the row's start and that start.
+// Blocks that stick out of the row (at most the first and the last) are read
+// element by element, so nothing outside the row is touched.
+template <int kDt>
+struct Blocks {
+  static constexpr int E = kDt == GPTQ_F32 ? 4 : 8;
+  const char* p0;   // address of block 0 (at most 15 bytes before the row)
+  int h, vocab, n;  // elements before the row, elements, blocks
+
+  __device__ __forceinline__ Blocks(const void* x, int64_t row, int64_t ld, int v) {
+    constexpr int es = 16 / E;
+    const char* p = static_cast<const char*>(x) + row * ld * es;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    p0 = p - off;
+    h = off / es;
+    vocab = v;
+    n = (h + v + E - 1) / E;
+  }
+  // blocks [first_whole(), end_whole()) lie inside the row
+  __device__ __forceinline__ int first_whole() const { return h > 0 ? 1 : 0; }
+  __device__ __forceinline__ int end_whole() const { return (h + vocab) / E; }
+  __device__ __forceinline__ int element(int b, int e) const { return b * E - h + e; }
+
+  __device__ __forceinline__ u32x4 load(int b) const {
+    return *reinterpret_cast<const u32x4*>(p0 + (int64_t)b * 16);
+  }
+  static __device__ __forceinline__ void unpack(u32x4 w, float (&v)[E]) {
+    if constexpr (kDt == GPTQ_F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (kDt == GPTQ_BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = f16_bits_to_f32(w[i] & 0xFFFFu);
+        v[2 * i + 1] = f16_bits_to_f32(w[i] >> 16);
+      }
+    }
+  }
+  // any block; elements outside the row (and whole blocks outside) come as -inf
+  __device__ __forceinline__ void fetch(int b, float (&v)[E]) const {
+    if (b >= first_whole() && b < end_whole()) {
+      unpack(load(b), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int j = element(b, e);
+        v[e] = j >= 0 && j < vocab ? load_el<kDt>(p0, (int64_t)b * E + e) : -INFINITY;
+      }
+    }
+  }
+};
+
+// 2^x by the hardware's instruction (one unit in the last place; results below
+// the normal range are zero).
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <class T, class F>
+__device__ __forceinline__ T wave_reduce(T v, F f) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = f(v, __shfl_xor(v, d));
+  return v;
+}
+
+// ---------------------------------------------------------------- running sums
+// S = sum 2^((x - r) c) and U = sum 2^((x - r) c) (x - r) c over what was seen,
+// r some reference near the maximum.  c = log2(e) / T.
+struct Sums {
+  float r, s, u;
+};
+
+// The sums moved to the reference `to` (>= r up to rounding).
+__device__ __forceinline__ Sums moved(Sums a, float to, float c) {
+  const float d = fmaxf((a.r - to) * c, -1e30f);   // finite, so that 0 * d is 0
+  const float f = exp2_hw(d);
+  return Sums{to, a.s * f, f * fmaf(d, a.s, a.u)};
+}
+
 }  // namespace gq
