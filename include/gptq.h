@@ -416,7 +416,8 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, int64_t n_r
  *       loss = sum_i p_i (log p_i - log q_i)
  *       dloss/dx_j = (q_j - p_j) / T, p_j = 0 outside K.
  *
- *   logits      device, n_rows x vocab of x_dtype, row stride ld_x.
+ *   logits      device, n_rows x vocab of x_dtype, row stride ld_x; vocab
+ *               <= 2^21 (more: GPTQ_EUNSUPPORTED).
  *   top_id      device int32 [n_rows][k], top_logprob device fp32
  *               [n_rows][k].  An entry whose id is outside [0, vocab) or
  *               whose l is -inf is absent (padding of a shorter list); an id
@@ -432,7 +433,8 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, int64_t n_r
  *               only.  It may be the logits' own buffer (grad == logits with
  *               ld_g == ld_x); otherwise it must not overlap them.
  *   temperature in [1e-4, 1e4].
- *   workspace   GPTQ_OP_DISTILL bytes; may be NULL when that size is 0.
+ *   workspace   GPTQ_OP_DISTILL bytes, 256-byte aligned; may be NULL when that
+ *               size is 0.
  * q_r is summed over the tail alone, with its own maximum, so a student that
  * puts nearly all its mass on K keeps it exactly.  A student's row that holds a NaN
  * or +inf, or nothing above -inf, has loss and gradient NaN (weight 0:

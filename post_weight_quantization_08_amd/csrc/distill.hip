@@ -1,7 +1,36 @@
 // Distillation from a teacher's top logits: loss and gradient of rows.
+//
+// The listed tokens K and the rest of the vocabulary are kept apart.  For the
+// rest one pass keeps a reference r and s = sum 2^((x - r) c), c = log2(e) / T;
+// the listed ones (at most 128) give their own maximum and sum.  Joined, with
+// m the larger reference and S = s 2^((r - m) c) + s_K 2^((m_K - m) c):
+//   log q_k = (x_k - m) / T - ln S,   log q_r = (r - m) / T + ln s - ln S,
+// so the tail's mass is never the difference of nearly equal sums, and
+//   gradient in the rest = w / T 2^((x - r) c) (2^((r - m) c) / S - p_r / s)
+//   gradient in K        = w / T (2^((x - m) c) / S - p_k).
+//
+// Row kernel: one workgroup holds a whole row in registers (16-byte blocks as
+// loaded), so a logit is read once and its gradient written once: the same
+// traffic as a copy.  Workgroups stay and take row after row; a block's
+// registers are refilled with the next row's as soon as its gradient is
+// stored, so the loads of one row run under the stores of the one before.
+// Part kernels: few rows are split over workgroups (and rows too long for the
+// registers of one): sums per part, then each part joins them and writes its
+// own gradients.
+//
+// The lanes that own listed tokens find them through lists in LDS: entry i
+// hangs itself on its owner's list, the owner turns its list into one bit per
+// held logit.  An id that comes twice meets itself in one list.
 #include "answer.h"
 
 namespace gq {
+
+constexpr int kDsMaxK = 128;
+
+// References as in the log probabilities: none below the floor (a power of
+// two), a new one when a term would exceed 2^8, another way when r c is so
+// large that its rounding matters.
+constexpr float kDsFloor = -1048576.f, kDsFast = 268435456.f, kDsLag = 8.f;
 
 struct DsArgs {
   const void* x;
@@ -11,114 +40,686 @@ struct DsArgs {
   const float* weight;
   float* loss;
   void* grad;
-  int64_t ld_g;
+  int64_t ld_g, n_rows;
   float c, inv_t;
   int vocab, k, tail;
+  int wide;                // gradient rows start on their 16 bytes where the logits' do
+  int parts, slots;        // part kernels: parts of a row, blocks a lane holds of one
+  float* ws_sums;          // [rows][parts][2]: r, s
+  float* ws_list;          // [rows][8]: the listed tokens' sums
 };
 
-template <class F>
-__device__ float block_reduce_f(float v, float* lds, F f) {
-  __syncthreads();
-  lds[threadIdx.x] = v;
-  for (int s = 128; s > 0; s >>= 1) {
-    __syncthreads();
-    if (threadIdx.x < s) lds[threadIdx.x] = f(lds[threadIdx.x], lds[threadIdx.x + s]);
+// What the listed tokens of a row give.
+struct DsList {
+  float m, s;              // maximum of x, sum of 2^((x - m) c)
+  float mass, norm;        // sum of p before (tail) / 1 after normalization; p = e^(l - norm)
+  float l1, l2;            // sum p log p, sum p (x - m) / T
+  float count;
+};
+
+// A row as `head` single logits, `blocks` 16-byte blocks on 16-byte addresses
+// and `rest` single logits.
+template <int kDt>
+struct Span {
+  static constexpr int E = kDt == GPTQ_F32 ? 4 : 8;
+  static constexpr int kSize = 16 / E;
+  const char* p;           // first element
+  int head, blocks, rest;
+  __device__ __forceinline__ Span(const void* x, int64_t row, int64_t ld, int vocab) {
+    p = static_cast<const char*>(x) + row * ld * kSize;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
+    head = min(vocab, off ? E - off : 0);
+    blocks = (vocab - head) / E;
+    rest = vocab - head - blocks * E;
   }
-  __syncthreads();
-  return lds[0];
+  // block first + lane, `first` the same in every lane
+  __device__ __forceinline__ u32x4 load(int first, int lane) const {
+    return *reinterpret_cast<const u32x4*>(p + head * kSize + (int64_t)first * 16 + (uint32_t)lane * 16u);
+  }
+  // the single logit of thread t (threads 0..7 the head's, 8..15 the rest's), or -1
+  __device__ __forceinline__ int edge(int t) const {
+    if (t < 8) return t < head ? t : -1;
+    return t < 16 && t - 8 < rest ? head + blocks * E + t - 8 : -1;
+  }
+};
+
+template <int kDt>
+__device__ __forceinline__ u32x4 masked_block() {
+  const uint32_t w = kDt == GPTQ_F32 ? 0xFF800000u : kDt == GPTQ_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  return u32x4{w, w, w, w};
 }
 
-// One workgroup of 256 per row.  The tail's maximum and sum are taken over
-// the tokens outside the teacher's list, the listed ones join afterwards.
 template <int kDt>
-__global__ __launch_bounds__(256) void distill_kernel(DsArgs a) {
-  __shared__ float lds[256];
-  __shared__ int ids[128];
-  __shared__ float lps[128], xs[128];
-  const int64_t row = blockIdx.x;
-  const int t = threadIdx.x;
-  const char* x = static_cast<const char*>(a.x) + row * a.ld * (kDt == GPTQ_F32 ? 4 : 2);
-  if (t < a.k) {
-    const int id = a.id[row * a.k + t];
-    const float lp = a.lp[row * a.k + t];
-    bool ok = id >= 0 && id < a.vocab && !(lp == -INFINITY);
-    if (ok)
-      for (int i = 0; i < t; ++i) ok = ok && !(a.id[row * a.k + i] == id && !(a.lp[row * a.k + i] == -INFINITY));
-    ids[t] = ok ? id : -1;
-    lps[t] = lp;
-    xs[t] = ok ? load_el<kDt>(x, id) : -INFINITY;
+__device__ __forceinline__ u32x4 pack_block(const float (&g)[Span<kDt>::E]) {
+  u32x4 w;
+  if constexpr (kDt == GPTQ_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(g[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kDt == GPTQ_BF16) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 h = {(__bf16)g[2 * i], (__bf16)g[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, h);
+      } else {
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        const f16x2 h = {(_Float16)g[2 * i], (_Float16)g[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, h);
+      }
+    }
   }
-  __syncthreads();
-  auto listed = [&](int j) {
-    int at = -1;
-    for (int i = 0; i < a.k; ++i) at = ids[i] == j ? i : at;
-    return at;
-  };
+  return w;
+}
+
+constexpr int kDsEnd = 255;   // end of a list
+
+// LDS of a workgroup of T threads.  The list's entries are held twice, for
+// this row and the next one.
+template <int T>
+struct DsShared {
+  int id[2][kDsMaxK];
+  float lp[2][kDsMaxK], x[2][kDsMaxK];
+  int next[2][kDsMaxK];
+  int head[T];
+  float red[T / 64][2];
+  DsList list;
+};
+
+// Reference and sum joined over the workgroup; every thread gets them.
+template <int T>
+__device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T>& sh) {
   auto fmax2 = [](float p, float q) { return fmaxf(p, q); };
   auto add2 = [](float p, float q) { return p + q; };
-  float mr = -INFINITY;
-  for (int j = t; j < a.vocab; j += 256)
-    if (listed(j) < 0) mr = fmaxf(mr, load_el<kDt>(x, j));
-  mr = block_reduce_f(mr, lds, fmax2);
-  float sr = 0.f;
-  if (mr > -INFINITY)
-    for (int j = t; j < a.vocab; j += 256) {
-      const float v = load_el<kDt>(x, j);
-      if (listed(j) < 0) sr += exp2f((v - mr) * a.c);
-      else if (v != v) sr += v;
-    }
-  else
-    for (int j = t; j < a.vocab; j += 256) {
-      const float v = load_el<kDt>(x, j);
-      if (v != v) sr += v;
-    }
-  sr = block_reduce_f(sr, lds, add2);
-  // the listed tokens
-  const bool has = t < a.k && ids[t < a.k ? t : 0] >= 0;
-  const float lp = has ? lps[t] : -INFINITY, xk = has ? xs[t] : -INFINITY;
-  const float m = block_reduce_f(fmaxf(xk, mr), lds, fmax2);
-  const float lm = block_reduce_f(lp, lds, fmax2);
-  const int count = (int)block_reduce_f(has ? 1.f : 0.f, lds, add2);
-  float p = has ? expf(a.tail ? lp : lp - lm) : 0.f;
-  const float mass = block_reduce_f(p, lds, add2);
-  float l = lp;
-  if (!a.tail) {
-    p /= mass;
-    l = lp - lm - logf(mass);
+  const float rw = wave_reduce(r, fmax2);
+  s = wave_reduce(s * exp2_hw((r - rw) * c), add2);
+  if ((threadIdx.x & 63) == 0) {
+    sh.red[threadIdx.x >> 6][0] = rw;
+    sh.red[threadIdx.x >> 6][1] = s;
   }
-  const float s = block_reduce_f(has ? exp2f((xk - m) * a.c) : 0.f, lds, add2) +
-                  (sr != 0.f ? sr * exp2f((mr - m) * a.c) : 0.f);
-  const float log2s = log2f(s);
-  float term = 0.f;
-  if (has && p > 0.f) term = p * (l - ((xk - m) * a.inv_t - kLn2 * log2s));
-  float loss = block_reduce_f(term, lds, add2);
-  const float pr = a.tail ? fmaxf(1.f - mass, 0.f) : 0.f;
-  const float lqr = sr != 0.f ? (mr - m) * a.inv_t + kLn2 * (log2f(sr) - log2s) : -INFINITY;
-  if (pr > 0.f) loss += pr * (logf(pr) - lqr);
-  const bool bad = !(m > -INFINITY) || s != s || m == INFINITY;
-  if (count == 0) loss = 0.f;
-  else if (bad) loss = NAN;
-  if (t == 0 && a.loss) a.loss[row] = loss;
-  if (!a.grad) return;
-  char* g = static_cast<char*>(a.grad) + row * a.ld_g * (kDt == GPTQ_F32 ? 4 : 2);
-  const float w = (a.weight ? a.weight[row] : 1.f) * a.inv_t;
-  const float inv_s = 1.f / s;
-  for (int j = t; j < a.vocab; j += 256) {
-    float d = 0.f;
-    if (w != 0.f && count > 0) {
-      const float v = load_el<kDt>(x, j);
-      const int at = listed(j);
-      const float q = exp2f((v - m) * a.c) * inv_s;
-      if (at >= 0) d = q - (a.tail ? expf(lps[at]) : expf(lps[at] - lm) / mass);
-      else if (a.tail) d = sr > 0.f ? q - pr * exp2f((v - mr) * a.c) / sr : 0.f;
-      else d = q;
-      d = bad ? NAN : d * w;
+  __syncthreads();
+  r = sh.red[0][0];
+#pragma unroll
+  for (int w = 1; w < T / 64; ++w) r = fmaxf(r, sh.red[w][0]);
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) s += sh.red[w][1] * exp2_hw((sh.red[w][0] - r) * c);
+}
+
+// A thread's list entry of a row as read from memory.
+struct DsEntry {
+  int id;
+  float lp, x;
+};
+
+template <int kDt, int T, int NB>
+struct DsRow {
+  static constexpr int E = Span<kDt>::E;
+  static constexpr int kMaskWords = (NB * E + 31) / 32;
+  DsShared<T>& sh;
+  const DsArgs& a;
+  uint32_t mask[kMaskWords];   // listed logits among the held ones
+  bool edge_listed;
+  int mine;                    // this lane's list
+  int buf;                     // which of the two lists
+
+  __device__ __forceinline__ DsRow(DsShared<T>& s, const DsArgs& args) : sh(s), a(args) {}
+
+  // Thread and slot that hold token j of a row; slot -1: the lane's single logit.
+  static __device__ __forceinline__ void owner(const Span<kDt>& sp, int j, int& thread, int& slot, int& e) {
+    if (j < sp.head) {
+      thread = j;
+      slot = -1;
+      e = 0;
+    } else if (j >= sp.head + sp.blocks * E) {
+      thread = 8 + j - sp.head - sp.blocks * E;
+      slot = -1;
+      e = 0;
+    } else {
+      const int b = (j - sp.head) / E;
+      thread = b % T;
+      slot = b / T;
+      e = (j - sp.head) % E;
     }
-    store_el<kDt>(g, j, d);
+  }
+
+  __device__ __forceinline__ DsEntry read_entry(int64_t row) const {
+    DsEntry n{-1, -INFINITY, -INFINITY};
+    if ((int)threadIdx.x < a.k) {
+      n.id = a.id[row * a.k + threadIdx.x];
+      n.lp = a.lp[row * a.k + threadIdx.x];
+      if (n.id < 0 || n.id >= a.vocab || n.lp == -INFINITY) n.id = -1;
+    }
+    return n;
+  }
+  __device__ __forceinline__ void read_logit(DsEntry& n, const Span<kDt>& sp) const {
+    if (n.id >= 0) n.x = load_el<kDt>(sp.p, n.id);
+  }
+
+  // The row's list into LDS and this lane's bits out of it.  Slots
+  // [slot0, slot0 + NB) are the held ones; `edges`: the single logits, too.
+  // Two barriers.
+  __device__ __forceinline__ void take_list(const Span<kDt>& sp, const DsEntry& n, int which, int slot0, bool edges) {
+    buf = which;
+    const int t = threadIdx.x;
+    if (t < a.k) {
+      sh.id[buf][t] = n.id;
+      sh.lp[buf][t] = n.lp;
+      sh.x[buf][t] = n.x;
+      if (n.id >= 0) {
+        int thread, slot, e;
+        owner(sp, n.id, thread, slot, e);
+        sh.next[buf][t] = atomicExch(&sh.head[thread], t);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMaskWords; ++i) mask[i] = 0;
+    edge_listed = false;
+    mine = sh.head[t];
+    sh.head[t] = kDsEnd;
+    for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
+      const int id = sh.id[buf][i];
+      // only the first of several places of an id counts
+      for (int o = mine; o != kDsEnd; o = sh.next[buf][o])
+        if (o < i && sh.id[buf][o] == id) sh.lp[buf][i] = -INFINITY;
+      int thread, slot, e;
+      owner(sp, id, thread, slot, e);
+      if (slot < 0) {
+        edge_listed = edges;
+      } else if (slot >= slot0 && slot < slot0 + NB) {
+        const int bit = (slot - slot0) * E + e;
+#pragma unroll
+        for (int w = 0; w < kMaskWords; ++w)
+          if (w == bit / 32) mask[w] |= 1u << (bit % 32);
+      }
+    }
+    __syncthreads();
+  }
+
+  // Listed bits of held block i (i known to the compiler, or any).
+  __device__ __forceinline__ uint32_t bits(int i) const {
+    return mask[i * E / 32] >> (i * E % 32) & ((1u << E) - 1u);
+  }
+  __device__ __forceinline__ uint32_t bits_any(int i) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < kMaskWords; ++w) m = w == i * E / 32 ? mask[w] : m;
+    return m >> (i * E % 32) & ((1u << E) - 1u);
+  }
+
+  // The listed tokens' sums, by one wave.
+  __device__ __forceinline__ DsList list_sums() const {
+    auto fmax2 = [](float p, float q) { return fmaxf(p, q); };
+    auto add2 = [](float p, float q) { return p + q; };
+    const int lane = threadIdx.x & 63;
+    float l[2], x[2], p[2];
+    bool has[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = lane + 64 * i;
+      has[i] = at < a.k && sh.id[buf][at < a.k ? at : 0] >= 0;
+      l[i] = has[i] ? sh.lp[buf][at] : -INFINITY;
+      has[i] = has[i] && l[i] != -INFINITY;
+      x[i] = has[i] ? sh.x[buf][at] : -INFINITY;
+    }
+    DsList d;
+    d.count = wave_reduce((float)((int)has[0] + (int)has[1]), add2);
+    d.m = wave_reduce(fmaxf(x[0], x[1]), fmax2);
+    const float lm = a.tail ? 0.f : wave_reduce(fmaxf(l[0], l[1]), fmax2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p[i] = has[i] ? expf(l[i] - lm) : 0.f;
+    d.mass = wave_reduce(p[0] + p[1], add2);
+    d.norm = 0.f;
+    if (!a.tail) {
+      d.norm = lm + logf(d.mass);
+      p[0] /= d.mass;
+      p[1] /= d.mass;
+      d.mass = 1.f;
+    }
+    float s = 0.f, l1 = 0.f, l2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float far = x[i] == -INFINITY ? -INFINITY : x[i] - d.m;
+      if (has[i]) s += exp2f(far * a.c);
+      if (p[i] > 0.f) {
+        l1 = fmaf(p[i], l[i] - d.norm, l1);
+        l2 = fmaf(p[i], far * a.inv_t, l2);
+      }
+    }
+    d.s = wave_reduce(s, add2);
+    d.l1 = wave_reduce(l1, add2);
+    d.l2 = wave_reduce(l2, add2);
+    return d;
+  }
+};
+
+// What the gradient of a row is made of.
+struct DsFinal {
+  float m, inv_s;          // listed: w (2^((x - m) c) inv_s - p)
+  float r, rest;           // rest: rest * 2^((x - r) c)
+  float w, norm;
+  float loss;
+  bool zero, nan;
+};
+
+__device__ __forceinline__ DsFinal ds_final(const DsArgs& a, int64_t row, const DsList& l, float r, float s) {
+  DsFinal f;
+  f.m = fmaxf(l.m, s > 0.f ? r : -INFINITY);
+  const float up = s > 0.f ? exp2f((r - f.m) * a.c) : 0.f;
+  const float total = (l.s > 0.f || l.s != l.s ? l.s * exp2f((l.m - f.m) * a.c) : 0.f) + (s != s ? s : s * up);
+  const bool bad = !(total > 0.f && total < INFINITY);
+  const float log_s = kLn2 * log2f(total);
+  float loss = l.l1 - l.l2;
+  if (l.mass > 0.f) loss -= l.mass * ((l.m - f.m) * a.inv_t - log_s);
+  const float pr = a.tail ? fmaxf(1.f - l.mass, 0.f) : 0.f;
+  if (pr > 0.f) loss += s > 0.f ? pr * (logf(pr) - ((r - f.m) * a.inv_t + kLn2 * log2f(s) - log_s)) : INFINITY;
+  if (bad) loss = NAN;
+  if (l.count == 0.f) loss = 0.f;
+  f.loss = loss;
+  f.w = (a.weight ? a.weight[row] : 1.f) * a.inv_t;
+  f.zero = f.w == 0.f || l.count == 0.f;
+  f.nan = bad && !f.zero;
+  f.inv_s = 1.f / total;
+  f.r = r;
+  f.norm = l.norm;
+  f.rest = s > 0.f ? f.w * (up * f.inv_s - pr / s) : 0.f;
+  if (f.zero) f.rest = 0.f;
+  return f;
+}
+
+// The rest's sum over what a lane holds.
+template <int kDt, int T, int NB>
+__device__ __forceinline__ void ds_add_block(float& r, float& rc, float& s, const float (&v)[Span<kDt>::E], float c) {
+  constexpr int E = Span<kDt>::E;
+  float vm = fmaxf(v[0], v[1]);
+#pragma unroll
+  for (int e = 2; e < E; ++e) vm = fmaxf(vm, v[e]);
+  if (fmaf(vm, c, -rc) > kDsLag) {
+    // s stands at rc, not at r c: both roundings go into the move
+    const float skew = fmaf(vm, c, -(vm * c)) - fmaf(r, c, -rc);
+    s *= exp2_hw(fmaxf((r - vm) * c, -1e30f) + skew);
+    r = vm;
+    rc = vm * c;
+  }
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    s0 += exp2_hw(fmaf(v[e], c, -rc));
+    s1 += exp2_hw(fmaf(v[e + 1], c, -rc));
+  }
+  s += s0 + s1;
+}
+
+// The block's logits.  The empty asm makes every use of a held block a value
+// of its own: without it the compiler keeps the unpacked logits of the sums
+// for the gradients, eight registers for every four held.
+template <int kDt>
+__device__ __forceinline__ void unpack_held(u32x4 w, float (&v)[Span<kDt>::E]) {
+  asm volatile("" : "+v"(w));
+  Blocks<kDt>::unpack(w, v);
+}
+
+template <int kDt, int NB>
+__device__ __forceinline__ void hide(float (&v)[Span<kDt>::E], uint32_t listed) {
+  if (listed) {
+#pragma unroll
+    for (int e = 0; e < Span<kDt>::E; ++e) v[e] = listed >> e & 1u ? -INFINITY : v[e];
   }
 }
 
-size_t distill_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+// r, s of the rest among the workgroup's blocks, the slow way: around the true
+// maximum, differences taken before they are scaled.  Reads the row again, so
+// that the common way needs no registers for this.
+template <int kDt, int T, int NB>
+__device__ __forceinline__ void ds_exact_sums(const DsRow<kDt, T, NB>& d, const Span<kDt>& sp, int slot0, int slots,
+                                              float xe, float& r, float& s, DsShared<T>& sh) {
+  constexpr int E = Span<kDt>::E;
+  const bool nan = s != s;
+  auto get = [&](int i, float (&v)[E]) {
+    const int first = (slot0 + i) * T, t = threadIdx.x;
+    Blocks<kDt>::unpack(t < sp.blocks - first ? sp.load(first, t) : masked_block<kDt>(), v);
+    hide<kDt, NB>(v, d.bits_any(i));
+  };
+  float m = xe;
+#pragma unroll 1
+  for (int i = 0; i < slots; ++i) {
+    float v[E];
+    get(i, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
+  }
+  m = wave_reduce(m, [](float p, float q) { return fmaxf(p, q); });
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh.red[threadIdx.x >> 6][0] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) m = fmaxf(m, sh.red[i][0]);
+  __syncthreads();
+  r = -3.4028235e38f;
+  s = 0.f;
+  if (m == -INFINITY) {
+    s = nan ? NAN : 0.f;
+    return;
+  }
+  r = m;
+  if (m == INFINITY) {
+    s = NAN;
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < slots; ++i) {
+    float v[E];
+    get(i, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += exp2_hw((v[e] - m) * d.a.c);
+  }
+  s += exp2_hw((xe - m) * d.a.c);
+  ds_join<T>(r, s, d.a.c, sh);
+}
+
+// Gradients of one held block: v the logits, listed their bits; kFast: r c
+// rounded is rc, and the row is none of zeros or NaN.
+template <int kDt, int T, int NB, bool kFast>
+__device__ __forceinline__ void ds_gradient(const DsRow<kDt, T, NB>& d, const Span<kDt>& sp, const DsFinal& f, float rest,
+                                            float rc, const float* v, float* g, int n, uint32_t listed, int slot) {
+  const float c = d.a.c;
+#pragma unroll
+  for (int e = 0; e < n; ++e) g[e] = rest * exp2_hw(kFast ? fmaf(v[e], c, -rc) : (v[e] - f.r) * c);
+  if (listed) {
+    for (int i = d.mine; i != kDsEnd; i = d.sh.next[d.buf][i]) {
+      const float l = d.sh.lp[d.buf][i];
+      int thread, at, e;
+      DsRow<kDt, T, NB>::owner(sp, d.sh.id[d.buf][i], thread, at, e);
+      if (at != slot || l == -INFINITY) continue;
+      const float p = expf(l - f.norm);
+#pragma unroll
+      for (int q = 0; q < n; ++q)
+        if (q == e) g[q] = f.w * (exp2f((v[q] - f.m) * c) * f.inv_s - p);
+    }
+  }
+  if (!kFast && (f.zero || f.nan)) {
+#pragma unroll
+    for (int e = 0; e < n; ++e) g[e] = f.nan ? NAN : 0.f;
+  }
+}
+
+template <int kDt>
+__device__ __forceinline__ void ds_store(const DsArgs& a, const Span<kDt>& sp, int64_t row, int first, int lane,
+                                         const float (&g)[Span<kDt>::E]) {
+  constexpr int E = Span<kDt>::E;
+  char* p = static_cast<char*>(a.grad) + (row * a.ld_g + sp.head) * Span<kDt>::kSize + (int64_t)first * 16 +
+            (uint32_t)lane * 16u;
+  if (a.wide) {
+    *reinterpret_cast<u32x4*>(p) = pack_block<kDt>(g);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_el<kDt>(p, e, g[e]);
+  }
+}
+
+// Row kernel: T threads hold a row of at most T NB blocks.
+template <int kDt, int T, int NB, bool kGrad>
+__global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
+  __shared__ DsShared<T> sh;
+  constexpr int E = Span<kDt>::E;
+  const int t = threadIdx.x;
+  int64_t row = blockIdx.x;
+  if (row >= a.n_rows) return;
+  DsRow<kDt, T, NB> d(sh, a);
+  sh.head[t] = kDsEnd;
+  u32x4 w[NB];
+  Span<kDt> sp(a.x, row, a.ld, a.vocab);
+  auto refill = [&](const Span<kDt>& s, int blocks, int i) {
+    w[i] = masked_block<kDt>();
+    if (t < blocks - i * T) w[i] = s.load(i * T, t);
+  };
+#pragma unroll
+  for (int i = 0; i < NB; ++i) refill(sp, sp.blocks, i);
+  float xe = sp.edge(t) >= 0 ? load_el<kDt>(sp.p, sp.edge(t)) : -INFINITY;
+  DsEntry n = d.read_entry(row);
+  d.read_logit(n, sp);
+  __syncthreads();
+  for (int which = 0;; which ^= 1) {
+    const int64_t next_row = row + gridDim.x;
+    const bool more = next_row < a.n_rows;
+    const Span<kDt> next(a.x, more ? next_row : row, a.ld, a.vocab);
+    const int next_blocks = more ? next.blocks : 0;
+    d.take_list(sp, n, which, 0, true);
+    DsEntry ahead{-1, -INFINITY, -INFINITY};
+    if (more) ahead = d.read_entry(next_row);
+    if (t < 64) {
+      const DsList l = d.list_sums();
+      if (t == 0) sh.list = l;
+    }
+    float r = kDsFloor, rc = kDsFloor * a.c, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      float v[E];
+      unpack_held<kDt>(w[i], v);
+      hide<kDt, NB>(v, d.bits(i));
+      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const float xr = d.edge_listed ? -INFINITY : xe;
+    {
+      float v[E];
+      v[0] = xr;
+#pragma unroll
+      for (int e = 1; e < E; ++e) v[e] = -INFINITY;
+      if (t < 64) ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+    }
+    s *= exp2_hw(-fmaf(r, a.c, -rc));
+    ds_join<T>(r, s, a.c, sh);
+    const DsList list = sh.list;
+    // a rest of -inf alone, or out of the fast way's range
+    const bool exact = !(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast);
+    if (exact) ds_exact_sums<kDt, T, NB>(d, sp, 0, NB, xr, r, s, sh);
+    const DsFinal f = ds_final(a, row, list, r, s);
+    if (t == 0 && a.loss) a.loss[row] = f.loss;
+    if (more) d.read_logit(ahead, next);
+    float xe_next = -INFINITY;
+    if (more && next.edge(t) >= 0) xe_next = load_el<kDt>(next.p, next.edge(t));
+    if constexpr (kGrad) {
+      const float frc = r * a.c;
+      const float rest = exact ? f.rest : f.rest * exp2_hw(-fmaf(r, a.c, -frc));
+      if (sp.edge(t) >= 0) {
+        float g[1];
+        ds_gradient<kDt, T, NB, false>(d, sp, f, f.rest, 0.f, &xe, g, 1, d.edge_listed, -1);
+        store_el<kDt>(static_cast<char*>(a.grad) + row * a.ld_g * Span<kDt>::kSize, sp.edge(t), g[0]);
+      }
+      if (!(exact || f.zero || f.nan)) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          float v[E], g[E];
+          unpack_held<kDt>(w[i], v);
+          ds_gradient<kDt, T, NB, true>(d, sp, f, rest, frc, v, g, E, d.bits(i), i);
+          if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
+          refill(next, next_blocks, i);
+          __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < NB; ++i) {
+          if (t >= sp.blocks - i * T) break;
+          float v[E], g[E];
+          Blocks<kDt>::unpack(sp.load(i * T, t), v);
+          ds_gradient<kDt, T, NB, false>(d, sp, f, rest, frc, v, g, E, d.bits_any(i), i);
+          ds_store<kDt>(a, sp, row, i * T, t, g);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) refill(next, next_blocks, i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) refill(next, next_blocks, i);
+    }
+    if (!more) break;
+    row = next_row;
+    sp = next;
+    n = ahead;
+    xe = xe_next;
+  }
+}
+
+constexpr int kDsPartThreads = 256;
+constexpr int kDsPartBlocks = 16;   // blocks a lane holds of a part, at most
+
+// Part kernels.  kSums: r, s of a part's rest (and from part 0 the listed
+// tokens' sums) into the workspace.  Otherwise: the parts joined, the loss
+// (part 0), the part's gradients.
+template <int kDt, int NB, bool kSums>
+__global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) {
+  constexpr int T = kDsPartThreads;
+  constexpr int E = Span<kDt>::E;
+  __shared__ DsShared<T> sh;
+  const int t = threadIdx.x;
+  const int per_row = kSums || a.grad ? a.parts : 1;
+  const int64_t row = blockIdx.x / per_row;
+  const int part = blockIdx.x % per_row;
+  const Span<kDt> sp(a.x, row, a.ld, a.vocab);
+  DsRow<kDt, T, NB> d(sh, a);
+  sh.head[t] = kDsEnd;
+  u32x4 w[NB];
+  const bool edges = part == 0;
+  const int slot0 = part * a.slots;
+  float xe = -INFINITY;
+  if (kSums || a.grad) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int first = (slot0 + i) * T;
+      w[i] = masked_block<kDt>();
+      if (i < a.slots && t < sp.blocks - first) w[i] = sp.load(first, t);
+    }
+    if (edges && sp.edge(t) >= 0) xe = load_el<kDt>(sp.p, sp.edge(t));
+  }
+  DsEntry n = d.read_entry(row);
+  if (kSums && part == 0) d.read_logit(n, sp);
+  __syncthreads();
+  d.take_list(sp, n, 0, slot0, edges);
+  if constexpr (kSums) {
+    if (part == 0 && t < 64) {
+      const DsList l = d.list_sums();
+      if (t == 0) {
+        float* o = a.ws_list + row * 8;
+        o[0] = l.m;
+        o[1] = l.s;
+        o[2] = l.mass;
+        o[3] = l.norm;
+        o[4] = l.l1;
+        o[5] = l.l2;
+        o[6] = l.count;
+      }
+    }
+    float r = kDsFloor, rc = kDsFloor * a.c, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      float v[E];
+      unpack_held<kDt>(w[i], v);
+      hide<kDt, NB>(v, d.bits(i));
+      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const float xr = d.edge_listed ? -INFINITY : xe;
+    if (edges && t < 64) {
+      float v[E];
+      v[0] = xr;
+#pragma unroll
+      for (int e = 1; e < E; ++e) v[e] = -INFINITY;
+      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+    }
+    s *= exp2_hw(-fmaf(r, a.c, -rc));
+    ds_join<T>(r, s, a.c, sh);
+    if (!(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast)) ds_exact_sums<kDt, T, NB>(d, sp, slot0, a.slots, xr, r, s, sh);
+    if (t == 0) {
+      float* o = a.ws_sums + (row * a.parts + part) * 2;
+      o[0] = r;
+      o[1] = s;
+    }
+  } else {
+    float r = -3.4028235e38f, s = 0.f;
+    for (int p = t; p < a.parts; p += T) {
+      const float* o = a.ws_sums + (row * a.parts + p) * 2;
+      const float to = fmaxf(r, o[0]);
+      s = (s == 0.f ? 0.f : s * exp2_hw((r - to) * a.c)) + (o[1] == 0.f ? 0.f : o[1] * exp2_hw((o[0] - to) * a.c));
+      r = to;
+    }
+    ds_join<T>(r, s, a.c, sh);
+    const float* o = a.ws_list + row * 8;
+    const DsList list{o[0], o[1], o[2], o[3], o[4], o[5], o[6]};
+    const DsFinal f = ds_final(a, row, list, r, s);
+    if (part == 0 && t == 0 && a.loss) a.loss[row] = f.loss;
+    if (!a.grad) return;
+    if (edges && sp.edge(t) >= 0) {
+      float g[1];
+      ds_gradient<kDt, T, NB, false>(d, sp, f, f.rest, 0.f, &xe, g, 1, d.edge_listed, -1);
+      store_el<kDt>(static_cast<char*>(a.grad) + row * a.ld_g * Span<kDt>::kSize, sp.edge(t), g[0]);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int first = (slot0 + i) * T;
+      if (i >= a.slots || t >= sp.blocks - first) continue;
+      float v[E], g[E];
+      unpack_held<kDt>(w[i], v);
+      ds_gradient<kDt, T, NB, false>(d, sp, f, f.rest, 0.f, v, g, E, d.bits(i), slot0 + i);
+      ds_store<kDt>(a, sp, row, first, t, g);
+    }
+  }
+}
+
+struct DsPlan {
+  int threads, held;       // row kernel: threads and blocks a lane holds; threads 0: part kernels
+  int parts, slots;
+  size_t off_list, total;
+};
+
+static DsPlan ds_plan(int64_t n_rows, int64_t vocab, int es) {
+  DsPlan p{};
+  const int64_t blocks = vocab * es / 16;
+  const int64_t row_max = 1024 * 20;
+  if (blocks <= 1024 || (n_rows > 128 && blocks <= row_max)) {
+    p.threads = blocks <= 256 * 16 ? 256 : blocks <= 512 * 16 ? 512 : 1024;
+    p.held = blocks <= 256 * 4 ? 4 : blocks <= 1024 * 16 ? 16 : 20;
+    return p;
+  }
+  // parts: enough for four workgroups per CU, of one block a lane or more
+  int64_t slots = kDsPartBlocks;
+  while (slots > 1 && n_rows * cdiv(blocks, slots * kDsPartThreads) < 1024) slots /= 2;
+  p.slots = (int)slots;
+  p.parts = (int)cdiv(blocks, slots * kDsPartThreads);
+  p.off_list = align_up((size_t)n_rows * p.parts * 8, 256);
+  p.total = p.off_list + (size_t)n_rows * 32;
+  return p;
+}
+
+size_t distill_workspace_bytes(int64_t n_rows, int64_t vocab, int64_t) {
+  return std::max(ds_plan(n_rows, vocab, 2).total, ds_plan(n_rows, vocab, 4).total);
+}
+
+template <int kDt, int T, int NB>
+static void ds_launch_rows(const DsArgs& a, int per_cu, hipStream_t st) {
+  const dim3 grid((unsigned)std::min<int64_t>(a.n_rows, 256 * per_cu));
+  if (a.grad) hipLaunchKernelGGL((distill_row_kernel<kDt, T, NB, true>), grid, dim3(T), 0, st, a);
+  else hipLaunchKernelGGL((distill_row_kernel<kDt, T, NB, false>), grid, dim3(T), 0, st, a);
+}
+
+template <int kDt, int NB>
+static void ds_launch_parts(const DsArgs& a, hipStream_t st) {
+  const dim3 all((unsigned)(a.n_rows * a.parts)), rows((unsigned)a.n_rows);
+  hipLaunchKernelGGL((distill_part_kernel<kDt, NB, true>), all, dim3(kDsPartThreads), 0, st, a);
+  hipLaunchKernelGGL((distill_part_kernel<kDt, NB, false>), a.grad ? all : rows, dim3(kDsPartThreads), 0, st, a);
+}
+
+template <int kDt>
+static void ds_dispatch(const DsArgs& a, const DsPlan& p, hipStream_t st) {
+  if (p.threads == 256 && p.held == 4) ds_launch_rows<kDt, 256, 4>(a, 8, st);
+  else if (p.threads == 256) ds_launch_rows<kDt, 256, 16>(a, 4, st);
+  else if (p.threads == 512) ds_launch_rows<kDt, 512, 16>(a, 2, st);
+  else if (p.threads == 1024 && p.held == 16) ds_launch_rows<kDt, 1024, 16>(a, 1, st);
+  else if (p.threads == 1024) ds_launch_rows<kDt, 1024, 20>(a, 1, st);
+  else if (p.slots <= 4) ds_launch_parts<kDt, 4>(a, st);
+  else ds_launch_parts<kDt, kDsPartBlocks>(a, st);
+}
 
 }  // namespace gq
 
@@ -129,28 +730,48 @@ extern "C" gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, in
                                          float temperature, int32_t tail, const float* weight, float* loss, void* grad,
                                          int64_t ld_g, void* workspace, size_t ws_bytes, void* stream) {
   GQ_CHECK_ARG(x_dtype == GPTQ_F32 || x_dtype == GPTQ_F16 || x_dtype == GPTQ_BF16);
-  GQ_CHECK_ARG(n_rows >= 0 && n_rows <= ((int64_t)1 << 24) && vocab >= 1 && vocab <= ((int64_t)1 << 30));
-  GQ_CHECK_ARG(ld_x >= vocab && ld_x <= ((int64_t)1 << 40));
+  GQ_CHECK_ARG(n_rows >= 0 && n_rows <= ((int64_t)1 << 22) && vocab >= 1 && vocab <= ((int64_t)1 << 30));
+  GQ_CHECK_ARG(ld_x >= vocab && ld_x <= ((int64_t)1 << 36));
   GQ_CHECK_ARG(temperature >= 1e-4f && temperature <= 1e4f);
   GQ_CHECK_ARG(k >= 1 && (tail == 0 || tail == 1));
   GQ_CHECK_ARG(loss || grad);
-  GQ_CHECK_ARG(grad == nullptr || (ld_g >= vocab && ld_g <= ((int64_t)1 << 40)));
+  GQ_CHECK_ARG(grad == nullptr || (ld_g >= vocab && ld_g <= ((int64_t)1 << 36)));
   GQ_CHECK_ARG(grad == nullptr || grad != logits || ld_g == ld_x);
-  if (k > 128) return GPTQ_EUNSUPPORTED;
+  if (k > kDsMaxK || vocab > ((int64_t)1 << 21)) return GPTQ_EUNSUPPORTED;
   if (n_rows == 0) return GPTQ_OK;
-  const size_t es = x_dtype == GPTQ_F32 ? 4 : 2;
+  const int es = x_dtype == GPTQ_F32 ? 4 : 2;
   GQ_CHECK_ARG(logits && top_id && top_logprob && reinterpret_cast<uintptr_t>(logits) % es == 0 &&
                reinterpret_cast<uintptr_t>(grad) % es == 0);
   const size_t need = distill_workspace_bytes(n_rows, vocab, k);
   if (need > 0 && (workspace == nullptr || ws_bytes < need)) return GPTQ_ENOMEM;
-  DsArgs a{logits, ld_x, top_id, top_logprob, weight, loss, grad, ld_g, (float)(1.4426950408889634074 / temperature),
-           (float)(1.0 / temperature), (int)vocab, k, tail};
+  const DsPlan pl = ds_plan(n_rows, vocab, es);
+  GQ_CHECK_ARG(pl.threads != 0 || reinterpret_cast<uintptr_t>(workspace) % 256 == 0);
+  DsArgs a{};
+  a.x = logits;
+  a.ld = ld_x;
+  a.id = top_id;
+  a.lp = top_logprob;
+  a.weight = weight;
+  a.loss = loss;
+  a.grad = grad;
+  a.ld_g = ld_g;
+  a.n_rows = n_rows;
+  a.c = (float)(1.4426950408889634074 / temperature);
+  a.inv_t = (float)(1.0 / temperature);
+  a.vocab = (int)vocab;
+  a.k = k;
+  a.tail = tail;
+  a.wide = (reinterpret_cast<uintptr_t>(grad) - reinterpret_cast<uintptr_t>(logits)) % 16 == 0 &&
+           (n_rows == 1 || (ld_g - ld_x) * es % 16 == 0);
+  a.parts = pl.parts;
+  a.slots = pl.slots;
+  a.ws_sums = static_cast<float*>(workspace);
+  a.ws_list = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_list);
   hipStream_t st = static_cast<hipStream_t>(stream);
   TimedScope ts(kTimeDistill, st);
-  const dim3 grid((unsigned)n_rows);
-  if (x_dtype == GPTQ_F32) hipLaunchKernelGGL(distill_kernel<GPTQ_F32>, grid, dim3(256), 0, st, a);
-  else if (x_dtype == GPTQ_F16) hipLaunchKernelGGL(distill_kernel<GPTQ_F16>, grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(distill_kernel<GPTQ_BF16>, grid, dim3(256), 0, st, a);
+  if (x_dtype == GPTQ_F32) ds_dispatch<GPTQ_F32>(a, pl, st);
+  else if (x_dtype == GPTQ_F16) ds_dispatch<GPTQ_F16>(a, pl, st);
+  else ds_dispatch<GPTQ_BF16>(a, pl, st);
   GQ_LAUNCHED();
   return GPTQ_OK;
 }
