@@ -42,6 +42,7 @@ struct DsArgs {
   void* grad;
   int64_t ld_g, n_rows;
   float c, inv_t;
+  double inv_td;           // 1 / T
   int vocab, k, tail;
   int wide;                // gradient rows start on their 16 bytes where the logits' do
   int parts, slots;        // part kernels: parts of a row, blocks a lane holds of one
@@ -49,11 +50,16 @@ struct DsArgs {
   float* ws_list;          // [rows][8]: the listed tokens' sums
 };
 
+// A value that is the same in every lane, kept in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // What the listed tokens of a row give.
 struct DsList {
   float m, s;              // maximum of x, sum of 2^((x - m) c)
   float mass, norm;        // sum of p before (tail) / 1 after normalization; p = e^(l - norm)
-  float l1, l2;            // sum p log p, sum p (x - m) / T
+  double gap;              // sum p (log p - (x - m) / T)
   float count;
 };
 
@@ -144,6 +150,8 @@ __device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T>
   s = 0.f;
 #pragma unroll
   for (int w = 0; w < T / 64; ++w) s += sh.red[w][1] * exp2_hw((sh.red[w][0] - r) * c);
+  r = uniform(r);
+  s = uniform(s);
 }
 
 // A thread's list entry of a row as read from memory.
@@ -213,17 +221,25 @@ struct DsRow {
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMaskWords; ++i) mask[i] = 0;
-    edge_listed = false;
     mine = sh.head[t];
     sh.head[t] = kDsEnd;
     for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
-      const int id = sh.id[buf][i];
       // only the first of several places of an id counts
+      const int id = sh.id[buf][i];
       for (int o = mine; o != kDsEnd; o = sh.next[buf][o])
         if (o < i && sh.id[buf][o] == id) sh.lp[buf][i] = -INFINITY;
+    }
+    set_bits(sp, slot0, edges);
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ void set_bits(const Span<kDt>& sp, int slot0, bool edges) {
+#pragma unroll
+    for (int i = 0; i < kMaskWords; ++i) mask[i] = 0;
+    edge_listed = false;
+    for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
       int thread, slot, e;
+      const int id = sh.id[buf][i];
       owner(sp, id, thread, slot, e);
       if (slot < 0) {
         edge_listed = edges;
@@ -234,7 +250,6 @@ struct DsRow {
           if (w == bit / 32) mask[w] |= 1u << (bit % 32);
       }
     }
-    __syncthreads();
   }
 
   // Listed bits of held block i (i known to the compiler, or any).
@@ -268,7 +283,7 @@ struct DsRow {
     d.m = wave_reduce(fmaxf(x[0], x[1]), fmax2);
     const float lm = a.tail ? 0.f : wave_reduce(fmaxf(l[0], l[1]), fmax2);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) p[i] = has[i] ? expf(l[i] - lm) : 0.f;
+    for (int i = 0; i < 2; ++i) p[i] = has[i] ? exp2_hw((l[i] - lm) * kLog2e) : 0.f;
     d.mass = wave_reduce(p[0] + p[1], add2);
     d.norm = 0.f;
     if (!a.tail) {
@@ -277,19 +292,16 @@ struct DsRow {
       p[1] /= d.mass;
       d.mass = 1.f;
     }
-    float s = 0.f, l1 = 0.f, l2 = 0.f;
+    float s = 0.f;
+    double gap = 0.0;   // the loss is what is left of sums larger than it: 64 bits for these few
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float far = x[i] == -INFINITY ? -INFINITY : x[i] - d.m;
-      if (has[i]) s += exp2f(far * a.c);
-      if (p[i] > 0.f) {
-        l1 = fmaf(p[i], l[i] - d.norm, l1);
-        l2 = fmaf(p[i], far * a.inv_t, l2);
-      }
+      if (has[i]) s += exp2_hw(far * a.c);
+      if (p[i] > 0.f) gap += (double)p[i] * ((double)l[i] - d.norm - (double)far * a.inv_td);
     }
     d.s = wave_reduce(s, add2);
-    d.l1 = wave_reduce(l1, add2);
-    d.l2 = wave_reduce(l2, add2);
+    d.gap = wave_reduce(gap, [](double q, double w) { return q + w; });
     return d;
   }
 };
@@ -306,25 +318,29 @@ struct DsFinal {
 __device__ __forceinline__ DsFinal ds_final(const DsArgs& a, int64_t row, const DsList& l, float r, float s) {
   DsFinal f;
   f.m = fmaxf(l.m, s > 0.f ? r : -INFINITY);
-  const float up = s > 0.f ? exp2f((r - f.m) * a.c) : 0.f;
-  const float total = (l.s > 0.f || l.s != l.s ? l.s * exp2f((l.m - f.m) * a.c) : 0.f) + (s != s ? s : s * up);
+  const float up = s > 0.f ? exp2_hw((r - f.m) * a.c) : 0.f;
+  const float total = (l.s > 0.f || l.s != l.s ? l.s * exp2_hw((l.m - f.m) * a.c) : 0.f) + (s != s ? s : s * up);
   const bool bad = !(total > 0.f && total < INFINITY);
   const float log_s = kLn2 * log2f(total);
-  float loss = l.l1 - l.l2;
-  if (l.mass > 0.f) loss -= l.mass * ((l.m - f.m) * a.inv_t - log_s);
+  double loss = l.gap;
+  if (l.mass > 0.f) loss -= (double)l.mass * ((double)(l.m - f.m) * a.inv_td - log_s);
   const float pr = a.tail ? fmaxf(1.f - l.mass, 0.f) : 0.f;
-  if (pr > 0.f) loss += s > 0.f ? pr * (logf(pr) - ((r - f.m) * a.inv_t + kLn2 * log2f(s) - log_s)) : INFINITY;
+  if (pr > 0.f) loss += s > 0.f ? (double)pr * (logf(pr) - ((double)(r - f.m) * a.inv_td + kLn2 * log2f(s) - log_s)) : INFINITY;
   if (bad) loss = NAN;
   if (l.count == 0.f) loss = 0.f;
-  f.loss = loss;
+  f.loss = (float)loss;
   f.w = (a.weight ? a.weight[row] : 1.f) * a.inv_t;
   f.zero = f.w == 0.f || l.count == 0.f;
   f.nan = bad && !f.zero;
   f.inv_s = 1.f / total;
   f.r = r;
   f.norm = l.norm;
-  f.rest = s > 0.f ? f.w * (up * f.inv_s - pr / s) : 0.f;
-  if (f.zero) f.rest = 0.f;
+  f.rest = s > 0.f && !f.zero ? f.w * (up * f.inv_s - pr / s) : 0.f;
+  f.m = uniform(f.m);
+  f.inv_s = uniform(f.inv_s);
+  f.rest = uniform(f.rest);
+  f.w = uniform(f.w);
+  f.norm = uniform(f.norm);
   return f;
 }
 
@@ -372,10 +388,11 @@ __device__ __forceinline__ void hide(float (&v)[Span<kDt>::E], uint32_t listed) 
 // maximum, differences taken before they are scaled.  Reads the row again, so
 // that the common way needs no registers for this.
 template <int kDt, int T, int NB>
-__device__ __forceinline__ void ds_exact_sums(const DsRow<kDt, T, NB>& d, const Span<kDt>& sp, int slot0, int slots,
-                                              float xe, float& r, float& s, DsShared<T>& sh) {
+__device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<kDt>& sp, int slot0, int slots, float xe,
+                                              float& r, float& s, DsShared<T>& sh) {
   constexpr int E = Span<kDt>::E;
   const bool nan = s != s;
+  d.set_bits(sp, slot0, false);
   auto get = [&](int i, float (&v)[E]) {
     const int first = (slot0 + i) * T, t = threadIdx.x;
     Blocks<kDt>::unpack(t < sp.blocks - first ? sp.load(first, t) : masked_block<kDt>(), v);
@@ -418,29 +435,32 @@ __device__ __forceinline__ void ds_exact_sums(const DsRow<kDt, T, NB>& d, const 
   ds_join<T>(r, s, d.a.c, sh);
 }
 
-// Gradients of one held block: v the logits, listed their bits; kFast: r c
-// rounded is rc, and the row is none of zeros or NaN.
-template <int kDt, int T, int NB, bool kFast>
-__device__ __forceinline__ void ds_gradient(const DsRow<kDt, T, NB>& d, const Span<kDt>& sp, const DsFinal& f, float rest,
-                                            float rc, const float* v, float* g, int n, uint32_t listed, int slot) {
-  const float c = d.a.c;
+// Gradients of n logits of the rest.  kFast: rc is r c rounded, `rest` made
+// for that, and the row none of zeros or NaN.
+template <bool kFast>
+__device__ __forceinline__ void ds_gradient(const DsFinal& f, float rest, float rc, float c, const float* v, float* g,
+                                            int n) {
 #pragma unroll
-  for (int e = 0; e < n; ++e) g[e] = rest * exp2_hw(kFast ? fmaf(v[e], c, -rc) : (v[e] - f.r) * c);
-  if (listed) {
-    for (int i = d.mine; i != kDsEnd; i = d.sh.next[d.buf][i]) {
-      const float l = d.sh.lp[d.buf][i];
-      int thread, at, e;
-      DsRow<kDt, T, NB>::owner(sp, d.sh.id[d.buf][i], thread, at, e);
-      if (at != slot || l == -INFINITY) continue;
-      const float p = expf(l - f.norm);
-#pragma unroll
-      for (int q = 0; q < n; ++q)
-        if (q == e) g[q] = f.w * (exp2f((v[q] - f.m) * c) * f.inv_s - p);
-    }
+  for (int e = 0; e < n; ++e) {
+    g[e] = rest * exp2_hw(kFast ? fmaf(v[e], c, -rc) : (v[e] - f.r) * c);
+    if (!kFast && (f.zero || f.nan)) g[e] = f.nan ? NAN : 0.f;
   }
-  if (!kFast && (f.zero || f.nan)) {
-#pragma unroll
-    for (int e = 0; e < n; ++e) g[e] = f.nan ? NAN : 0.f;
+}
+
+// The gradients of the listed tokens that this lane owns, over what its own
+// stores just left there.
+template <int kDt, int T, int NB>
+__device__ __forceinline__ void ds_fix_listed(const DsRow<kDt, T, NB>& d, const Span<kDt>& sp, int64_t row,
+                                              const DsFinal& f, int slot0, int slots, bool edges) {
+  if (f.zero || f.nan) return;
+  for (int i = d.mine; i != kDsEnd; i = d.sh.next[d.buf][i]) {
+    const float l = d.sh.lp[d.buf][i];
+    const int id = d.sh.id[d.buf][i];
+    int thread, slot, e;
+    DsRow<kDt, T, NB>::owner(sp, id, thread, slot, e);
+    if (l == -INFINITY || !(slot < 0 ? edges : slot >= slot0 && slot < slot0 + slots)) continue;
+    const float g = f.w * (exp2_hw((d.sh.x[d.buf][i] - f.m) * d.a.c) * f.inv_s - exp2_hw((l - f.norm) * kLog2e));
+    store_el<kDt>(d.a.grad, row * d.a.ld_g + id, g);
   }
 }
 
@@ -525,7 +545,7 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
       const float rest = exact ? f.rest : f.rest * exp2_hw(-fmaf(r, a.c, -frc));
       if (sp.edge(t) >= 0) {
         float g[1];
-        ds_gradient<kDt, T, NB, false>(d, sp, f, f.rest, 0.f, &xe, g, 1, d.edge_listed, -1);
+        ds_gradient<false>(f, f.rest, 0.f, a.c, &xe, g, 1);
         store_el<kDt>(static_cast<char*>(a.grad) + row * a.ld_g * Span<kDt>::kSize, sp.edge(t), g[0]);
       }
       if (!(exact || f.zero || f.nan)) {
@@ -533,7 +553,7 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
         for (int i = 0; i < NB; ++i) {
           float v[E], g[E];
           unpack_held<kDt>(w[i], v);
-          ds_gradient<kDt, T, NB, true>(d, sp, f, rest, frc, v, g, E, d.bits(i), i);
+          ds_gradient<true>(f, rest, frc, a.c, v, g, E);
           if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
           refill(next, next_blocks, i);
           __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
@@ -544,12 +564,13 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
           if (t >= sp.blocks - i * T) break;
           float v[E], g[E];
           Blocks<kDt>::unpack(sp.load(i * T, t), v);
-          ds_gradient<kDt, T, NB, false>(d, sp, f, rest, frc, v, g, E, d.bits_any(i), i);
+          ds_gradient<false>(f, f.rest, 0.f, a.c, v, g, E);
           ds_store<kDt>(a, sp, row, i * T, t, g);
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) refill(next, next_blocks, i);
       }
+      ds_fix_listed<kDt, T, NB>(d, sp, row, f, 0, NB, true);
     } else {
 #pragma unroll
       for (int i = 0; i < NB; ++i) refill(next, next_blocks, i);
@@ -594,7 +615,14 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     if (edges && sp.edge(t) >= 0) xe = load_el<kDt>(sp.p, sp.edge(t));
   }
   DsEntry n = d.read_entry(row);
-  if (kSums && part == 0) d.read_logit(n, sp);
+  if (kSums) {
+    if (part == 0) d.read_logit(n, sp);
+  } else if (n.id >= 0) {
+    // only what this part holds: in place, other parts are being overwritten
+    int thread, slot, e;
+    DsRow<kDt, T, NB>::owner(sp, n.id, thread, slot, e);
+    if (slot < 0 ? edges : slot >= slot0 && slot < slot0 + a.slots) d.read_logit(n, sp);
+  }
   __syncthreads();
   d.take_list(sp, n, 0, slot0, edges);
   if constexpr (kSums) {
@@ -606,9 +634,8 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
         o[1] = l.s;
         o[2] = l.mass;
         o[3] = l.norm;
-        o[4] = l.l1;
-        o[5] = l.l2;
-        o[6] = l.count;
+        o[4] = l.count;
+        *reinterpret_cast<double*>(o + 6) = l.gap;
       }
     }
     float r = kDsFloor, rc = kDsFloor * a.c, s = 0.f;
@@ -646,13 +673,13 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     }
     ds_join<T>(r, s, a.c, sh);
     const float* o = a.ws_list + row * 8;
-    const DsList list{o[0], o[1], o[2], o[3], o[4], o[5], o[6]};
+    const DsList list{o[0], o[1], o[2], o[3], *reinterpret_cast<const double*>(o + 6), o[4]};
     const DsFinal f = ds_final(a, row, list, r, s);
     if (part == 0 && t == 0 && a.loss) a.loss[row] = f.loss;
     if (!a.grad) return;
     if (edges && sp.edge(t) >= 0) {
       float g[1];
-      ds_gradient<kDt, T, NB, false>(d, sp, f, f.rest, 0.f, &xe, g, 1, d.edge_listed, -1);
+      ds_gradient<false>(f, f.rest, 0.f, a.c, &xe, g, 1);
       store_el<kDt>(static_cast<char*>(a.grad) + row * a.ld_g * Span<kDt>::kSize, sp.edge(t), g[0]);
     }
 #pragma unroll
@@ -661,9 +688,10 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       if (i >= a.slots || t >= sp.blocks - first) continue;
       float v[E], g[E];
       unpack_held<kDt>(w[i], v);
-      ds_gradient<kDt, T, NB, false>(d, sp, f, f.rest, 0.f, v, g, E, d.bits(i), slot0 + i);
+      ds_gradient<false>(f, f.rest, 0.f, a.c, v, g, E);
       ds_store<kDt>(a, sp, row, first, t, g);
     }
+    ds_fix_listed<kDt, T, NB>(d, sp, row, f, slot0, a.slots, edges);
   }
 }
 
@@ -758,6 +786,7 @@ extern "C" gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, in
   a.n_rows = n_rows;
   a.c = (float)(1.4426950408889634074 / temperature);
   a.inv_t = (float)(1.0 / temperature);
+  a.inv_td = 1.0 / temperature;
   a.vocab = (int)vocab;
   a.k = k;
   a.tail = tail;
