@@ -108,11 +108,55 @@ struct Blocks {
 // the normal range are zero).
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A barrier that waits for LDS only: loads and stores of global memory stay in
+// flight across it.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A value that is the same in every lane, kept in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
+}
+template <int kCtrl>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __uint_as_float(dpp_move<kCtrl>(__float_as_uint(v)));
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp_move(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t m = (uint64_t)dpp_move<kCtrl>((uint32_t)(b >> 32)) << 32 | dpp_move<kCtrl>((uint32_t)b);
+  return __builtin_bit_cast(double, m);
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t m = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  return __builtin_bit_cast(double, m);
+}
+
+// f over each 16 lanes, in all of them: exchanges within quads, then mirrored
+// eights and sixteens (data-parallel moves, no LDS).  All lanes are active.
+template <class T, class F>
+__device__ __forceinline__ T row_reduce(T v, F f) {
+  v = f(v, dpp_move<0xB1>(v));    // lanes 1 0 3 2
+  v = f(v, dpp_move<0x4E>(v));    // lanes 2 3 0 1
+  v = f(v, dpp_move<0x141>(v));   // eights mirrored
+  return f(v, dpp_move<0x140>(v));   // sixteens mirrored
+}
+
+// f over the wave, the same value in every lane.
 template <class T, class F>
 __device__ __forceinline__ T wave_reduce(T v, F f) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = f(v, __shfl_xor(v, d));
-  return v;
+  v = row_reduce(v, f);
+  return f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
 }
 
 // ---------------------------------------------------------------- running sums

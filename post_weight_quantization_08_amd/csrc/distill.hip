@@ -50,11 +50,6 @@ struct DsArgs {
   float* ws_list;          // [rows][8]: the listed tokens' sums
 };
 
-// A value that is the same in every lane, kept in a scalar register.
-__device__ __forceinline__ float uniform(float x) {
-  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
-}
-
 // What the listed tokens of a row give.
 struct DsList {
   float m, s;              // maximum of x, sum of 2^((x - m) c)
@@ -143,15 +138,14 @@ __device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T>
     sh.red[threadIdx.x >> 6][0] = rw;
     sh.red[threadIdx.x >> 6][1] = s;
   }
-  __syncthreads();
-  r = sh.red[0][0];
-#pragma unroll
-  for (int w = 1; w < T / 64; ++w) r = fmaxf(r, sh.red[w][0]);
-  s = 0.f;
-#pragma unroll
-  for (int w = 0; w < T / 64; ++w) s += sh.red[w][1] * exp2_hw((sh.red[w][0] - r) * c);
-  r = uniform(r);
-  s = uniform(s);
+  lds_barrier();
+  static_assert(T / 64 <= 16, "a wave's partial per lane of sixteen");
+  const int w = threadIdx.x & (T / 64 - 1) & 15;
+  const float rl = sh.red[w][0], sl = sh.red[w][1];
+  r = uniform(row_reduce(rl, fmax2));
+  // every wave's partial stands 16 / (T / 64) times in a row of sixteen lanes
+  const float mine = (threadIdx.x & 15) < T / 64 ? sl * exp2_hw((rl - r) * c) : 0.f;
+  s = uniform(row_reduce(mine, add2));
 }
 
 // A thread's list entry of a row as read from memory.
@@ -220,7 +214,7 @@ struct DsRow {
         sh.next[buf][t] = atomicExch(&sh.head[thread], t);
       }
     }
-    __syncthreads();
+    lds_barrier();
     mine = sh.head[t];
     sh.head[t] = kDsEnd;
     for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
@@ -230,7 +224,7 @@ struct DsRow {
         if (o < i && sh.id[buf][o] == id) sh.lp[buf][i] = -INFINITY;
     }
     set_bits(sp, slot0, edges);
-    __syncthreads();
+    lds_barrier();
   }
 
   __device__ __forceinline__ void set_bits(const Span<kDt>& sp, int slot0, bool edges) {
@@ -279,7 +273,7 @@ struct DsRow {
       x[i] = has[i] ? sh.x[buf][at] : -INFINITY;
     }
     DsList d;
-    d.count = wave_reduce((float)((int)has[0] + (int)has[1]), add2);
+    d.count = (float)(__popcll(__ballot(has[0])) + __popcll(__ballot(has[1])));
     d.m = wave_reduce(fmaxf(x[0], x[1]), fmax2);
     const float lm = a.tail ? 0.f : wave_reduce(fmaxf(l[0], l[1]), fmax2);
 #pragma unroll
@@ -311,9 +305,32 @@ struct DsFinal {
   float m, inv_s;          // listed: w (2^((x - m) c) inv_s - p)
   float r, rest;           // rest: rest * 2^((x - r) c)
   float w, norm;
-  float loss;
-  bool zero, nan;
+  float total, tail_q, pr; // S, q_r (0 also where it is below 2^-126) and p_r, for the loss
+  bool zero, nan, bad;
 };
+
+// ln x in 64 bits of a 32-bit x: the exponent apart, so that the logarithm of
+// a large sum keeps the digits that the loss is made of.
+__device__ __forceinline__ double ln_wide(float x) {
+  int e;
+  const float m = frexpf(x, &e);
+  return (double)e * 0.69314718055994530942 + (double)logf(m);
+}
+
+// loss of a row: sum p (log p - log q) over the list, p_r (log p_r - log q_r).
+__device__ __forceinline__ float ds_loss(const DsArgs& a, const DsList& l, const DsFinal& f, float r, float s) {
+  if (l.count == 0.f) return 0.f;
+  if (f.bad) return NAN;
+  const double log_s = ln_wide(f.total);
+  double loss = l.gap;
+  if (l.mass > 0.f) loss -= (double)l.mass * ((double)(l.m - f.m) * a.inv_td - log_s);
+  if (f.pr > 0.f) {
+    if (!(s > 0.f)) return INFINITY;
+    const double lq = f.tail_q > 0.f ? ln_wide(f.tail_q) : (double)(r - f.m) * a.inv_td + ln_wide(s) - log_s;
+    loss += (double)f.pr * (ln_wide(f.pr) - lq);
+  }
+  return (float)loss;
+}
 
 __device__ __forceinline__ DsFinal ds_final(const DsArgs& a, int64_t row, const DsList& l, float r, float s) {
   DsFinal f;
@@ -321,14 +338,11 @@ __device__ __forceinline__ DsFinal ds_final(const DsArgs& a, int64_t row, const 
   const float up = s > 0.f ? exp2_hw((r - f.m) * a.c) : 0.f;
   const float total = (l.s > 0.f || l.s != l.s ? l.s * exp2_hw((l.m - f.m) * a.c) : 0.f) + (s != s ? s : s * up);
   const bool bad = !(total > 0.f && total < INFINITY);
-  const float log_s = kLn2 * log2f(total);
-  double loss = l.gap;
-  if (l.mass > 0.f) loss -= (double)l.mass * ((double)(l.m - f.m) * a.inv_td - log_s);
   const float pr = a.tail ? fmaxf(1.f - l.mass, 0.f) : 0.f;
-  if (pr > 0.f) loss += s > 0.f ? (double)pr * (logf(pr) - ((double)(r - f.m) * a.inv_td + kLn2 * log2f(s) - log_s)) : INFINITY;
-  if (bad) loss = NAN;
-  if (l.count == 0.f) loss = 0.f;
-  f.loss = (float)loss;
+  f.total = total;
+  f.tail_q = s * up / total;
+  f.pr = pr;
+  f.bad = bad;
   f.w = (a.weight ? a.weight[row] : 1.f) * a.inv_t;
   f.zero = f.w == 0.f || l.count == 0.f;
   f.nan = bad && !f.zero;
@@ -407,12 +421,12 @@ __device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<k
     for (int e = 0; e < E; ++e) m = fmaxf(m, v[e]);
   }
   m = wave_reduce(m, [](float p, float q) { return fmaxf(p, q); });
-  __syncthreads();
+  lds_barrier();
   if ((threadIdx.x & 63) == 0) sh.red[threadIdx.x >> 6][0] = m;
-  __syncthreads();
+  lds_barrier();
 #pragma unroll
   for (int i = 0; i < T / 64; ++i) m = fmaxf(m, sh.red[i][0]);
-  __syncthreads();
+  lds_barrier();
   r = -3.4028235e38f;
   s = 0.f;
   if (m == -INFINITY) {
@@ -499,7 +513,7 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
   float xe = sp.edge(t) >= 0 ? load_el<kDt>(sp.p, sp.edge(t)) : -INFINITY;
   DsEntry n = d.read_entry(row);
   d.read_logit(n, sp);
-  __syncthreads();
+  lds_barrier();
   for (int which = 0;; which ^= 1) {
     const int64_t next_row = row + gridDim.x;
     const bool more = next_row < a.n_rows;
@@ -536,7 +550,7 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
     const bool exact = !(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast);
     if (exact) ds_exact_sums<kDt, T, NB>(d, sp, 0, NB, xr, r, s, sh);
     const DsFinal f = ds_final(a, row, list, r, s);
-    if (t == 0 && a.loss) a.loss[row] = f.loss;
+    if (t == 0 && a.loss) a.loss[row] = ds_loss(a, list, f, r, s);
     if (more) d.read_logit(ahead, next);
     float xe_next = -INFINITY;
     if (more && next.edge(t) >= 0) xe_next = load_el<kDt>(next.p, next.edge(t));
@@ -623,7 +637,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     DsRow<kDt, T, NB>::owner(sp, n.id, thread, slot, e);
     if (slot < 0 ? edges : slot >= slot0 && slot < slot0 + a.slots) d.read_logit(n, sp);
   }
-  __syncthreads();
+  lds_barrier();
   d.take_list(sp, n, 0, slot0, edges);
   if constexpr (kSums) {
     if (part == 0 && t < 64) {
@@ -675,7 +689,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     const float* o = a.ws_list + row * 8;
     const DsList list{o[0], o[1], o[2], o[3], *reinterpret_cast<const double*>(o + 6), o[4]};
     const DsFinal f = ds_final(a, row, list, r, s);
-    if (part == 0 && t == 0 && a.loss) a.loss[row] = f.loss;
+    if (part == 0 && t == 0 && a.loss) a.loss[row] = ds_loss(a, list, f, r, s);
     if (!a.grad) return;
     if (edges && sp.edge(t) >= 0) {
       float g[1];

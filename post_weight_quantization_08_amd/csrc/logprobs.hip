@@ -284,9 +284,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
         sh.gmax[b - b0] = vm;
       } else {
         // 16 lanes hold 16 blocks in a row
-        float g = vm;
-#pragma unroll
-        for (int d = 1; d < kGs; d <<= 1) g = fmaxf(g, __shfl_xor(g, d));
+        const float g = row_reduce(vm, [](float p, float q) { return fmaxf(p, q); });
         if ((tid & (kGs - 1)) == 0) sh.gmax[(b - b0) / kGs] = g;
       }
     }
