@@ -44,7 +44,6 @@ struct DsArgs {
   float c, inv_t;
   double inv_td;           // 1 / T
   int vocab, k, tail;
-  int wide;                // gradient rows start on their 16 bytes where the logits' do
   int parts, slots;        // part kernels: parts of a row, blocks a lane holds of one
   float* ws_sums;          // [rows][parts][2]: r, s
   float* ws_list;          // [rows][8]: the listed tokens' sums
@@ -56,6 +55,15 @@ struct DsList {
   float mass, norm;        // sum of p before (tail) / 1 after normalization; p = e^(l - norm)
   double gap;              // sum p (log p - (x - m) / T)
   float count;
+};
+
+// What the gradient of a row is made of.
+struct DsFinal {
+  float m, inv_s;          // listed: w (2^((x - m) c) inv_s - p)
+  float r, rest;           // rest: rest * 2^((x - r) c)
+  float w, norm;
+  float total, tail_q, pr; // S, q_r (0 also where it is below 2^-126) and p_r, for the loss
+  int zero, nan, bad;
 };
 
 // A row as `head` single logits, `blocks` 16-byte blocks on 16-byte addresses
@@ -100,9 +108,9 @@ __device__ __forceinline__ u32x4 pack_block(const float (&g)[Span<kDt>::E]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (kDt == GPTQ_BF16) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        const bf16x2 h = {(__bf16)g[2 * i], (__bf16)g[2 * i + 1]};
-        w[i] = __builtin_bit_cast(uint32_t, h);
+        uint32_t h;   // two roundings to nearest even in one instruction
+        asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(h) : "v"(g[2 * i]), "v"(g[2 * i + 1]));
+        w[i] = h;
       } else {
         typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
         const f16x2 h = {(_Float16)g[2 * i], (_Float16)g[2 * i + 1]};
@@ -115,6 +123,29 @@ __device__ __forceinline__ u32x4 pack_block(const float (&g)[Span<kDt>::E]) {
 
 constexpr int kDsEnd = 255;   // end of a list
 
+// Where a lane reads that has no block to read: every load is made, so that
+// the compiler can count the ones behind it and wait for one block at a time.
+static __device__ u32x4 ds_pad[1];
+
+// Blocks of a span as a lane reads them: block first + lane, or the last one
+// in its place (or the pad, if there is none).
+template <int kDt>
+struct DsSource {
+  const char* base;
+  uint32_t last, lane;     // byte offsets: of the last block, of the lane's first
+  __device__ __forceinline__ DsSource(const Span<kDt>& sp, bool real) {
+    const bool any = real && sp.blocks > 0;
+    base = any ? sp.p + sp.head * Span<kDt>::kSize : reinterpret_cast<const char*>(ds_pad);
+    last = any ? (uint32_t)(sp.blocks - 1) * 16u : 0u;
+    lane = threadIdx.x * 16u;
+    asm volatile("" : "+v"(lane));   // a row's own value: offsets of all slots are not kept from row to row
+  }
+  __device__ __forceinline__ u32x4 load(int first) const {
+    const uint32_t at = (uint32_t)first * 16u + lane;
+    return *reinterpret_cast<const u32x4*>(base + (at < last ? at : last));
+  }
+};
+
 // LDS of a workgroup of T threads.  The list's entries are held twice, for
 // this row and the next one.
 template <int T>
@@ -124,7 +155,7 @@ struct DsShared {
   int next[2][kDsMaxK];
   int head[T];
   float red[T / 64][2];
-  DsList list;
+  DsFinal fin;
 };
 
 // Reference and sum joined over the workgroup; every thread gets them.
@@ -148,10 +179,25 @@ __device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T>
   s = uniform(row_reduce(mine, add2));
 }
 
+// A logit's bits as loaded, and its value.  What is read ahead stays in this
+// form: looking at it would wait for it, and for everything loaded before.
+template <int kDt>
+__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t i) {
+  if constexpr (kDt == GPTQ_F32) return static_cast<const uint32_t*>(p)[i];
+  else return static_cast<const uint16_t*>(p)[i];
+}
+template <int kDt>
+__device__ __forceinline__ float bits_value(uint32_t b) {
+  if constexpr (kDt == GPTQ_F32) return __uint_as_float(b);
+  else if constexpr (kDt == GPTQ_BF16) return bf16_bits_to_f32(b);
+  else return f16_bits_to_f32(b);
+}
+
 // A thread's list entry of a row as read from memory.
 struct DsEntry {
   int id;
-  float lp, x;
+  float lp;
+  uint32_t x;
 };
 
 template <int kDt, int T, int NB>
@@ -160,7 +206,7 @@ struct DsRow {
   static constexpr int kMaskWords = (NB * E + 31) / 32;
   DsShared<T>& sh;
   const DsArgs& a;
-  uint32_t mask[kMaskWords];   // listed logits among the held ones
+  uint32_t mask[kMaskWords];   // held logits that are not the rest's: listed, or behind the row's end
   bool edge_listed;
   int mine;                    // this lane's list
   int buf;                     // which of the two lists
@@ -185,30 +231,39 @@ struct DsRow {
     }
   }
 
+  // Every lane reads (lanes without an entry the last one's), so that the
+  // compiler can count these loads, too.
   __device__ __forceinline__ DsEntry read_entry(int64_t row) const {
-    DsEntry n{-1, -INFINITY, -INFINITY};
-    if ((int)threadIdx.x < a.k) {
-      n.id = a.id[row * a.k + threadIdx.x];
-      n.lp = a.lp[row * a.k + threadIdx.x];
-      if (n.id < 0 || n.id >= a.vocab || n.lp == -INFINITY) n.id = -1;
-    }
-    return n;
+    const int64_t at = row * a.k + min((int)threadIdx.x, a.k - 1);
+    return DsEntry{a.id[at], a.lp[at], 0};
+  }
+  __device__ __forceinline__ bool present(const DsEntry& n) const {
+    return (int)threadIdx.x < a.k && n.id >= 0 && n.id < a.vocab && n.lp != -INFINITY;
   }
   __device__ __forceinline__ void read_logit(DsEntry& n, const Span<kDt>& sp) const {
-    if (n.id >= 0) n.x = load_el<kDt>(sp.p, n.id);
+    n.x = load_bits<kDt>(sp.p, min(max(n.id, 0), a.vocab - 1));
+  }
+  __device__ __forceinline__ uint32_t read_edge(const Span<kDt>& sp) const {
+    return load_bits<kDt>(sp.p, max(sp.edge(threadIdx.x), 0));
   }
 
-  // The row's list into LDS and this lane's bits out of it.  Slots
-  // [slot0, slot0 + NB) are the held ones; `edges`: the single logits, too.
+  // The entries' logits into LDS.
+  __device__ __forceinline__ void put_logits(const DsEntry& n) const {
+    if (present(n)) sh.x[buf][threadIdx.x] = bits_value<kDt>(n.x);
+  }
+
+  // The row's list (without its logits) into LDS and this lane's bits out of it.  Slots
+  // [slot0, slot0 + slots) are the held ones; `edges`: the single logits, too.
   // Two barriers.
-  __device__ __forceinline__ void take_list(const Span<kDt>& sp, const DsEntry& n, int which, int slot0, bool edges) {
+  __device__ __forceinline__ void take_list(const Span<kDt>& sp, const DsEntry& n, int which, int slot0, int slots,
+                                            bool edges) {
     buf = which;
     const int t = threadIdx.x;
     if (t < a.k) {
-      sh.id[buf][t] = n.id;
+      const bool there = present(n);
+      sh.id[buf][t] = there ? n.id : -1;
       sh.lp[buf][t] = n.lp;
-      sh.x[buf][t] = n.x;
-      if (n.id >= 0) {
+      if (there) {
         int thread, slot, e;
         owner(sp, n.id, thread, slot, e);
         sh.next[buf][t] = atomicExch(&sh.head[thread], t);
@@ -223,13 +278,18 @@ struct DsRow {
       for (int o = mine; o != kDsEnd; o = sh.next[buf][o])
         if (o < i && sh.id[buf][o] == id) sh.lp[buf][i] = -INFINITY;
     }
-    set_bits(sp, slot0, edges);
+    set_bits(sp, slot0, slots, edges);
     lds_barrier();
   }
 
-  __device__ __forceinline__ void set_bits(const Span<kDt>& sp, int slot0, bool edges) {
+  // The bits of listed logits, of blocks behind the span's end and of slots not held.
+  __device__ __forceinline__ void set_bits(const Span<kDt>& sp, int slot0, int slots, bool edges) {
+    // this lane's first slot without a block, as a bit number
+    const int end = sp.blocks - slot0 * T - (int)threadIdx.x;
+    const int bits = min(max(end + T - 1, 0) / T, slots) * E;
 #pragma unroll
-    for (int i = 0; i < kMaskWords; ++i) mask[i] = 0;
+    for (int i = 0; i < kMaskWords; ++i)
+      mask[i] = bits <= 32 * i ? ~0u : bits >= 32 * i + 32 ? 0u : ~0u << (bits - 32 * i);
     edge_listed = false;
     for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
       int thread, slot, e;
@@ -237,7 +297,7 @@ struct DsRow {
       owner(sp, id, thread, slot, e);
       if (slot < 0) {
         edge_listed = edges;
-      } else if (slot >= slot0 && slot < slot0 + NB) {
+      } else if (slot >= slot0 && slot < slot0 + slots) {
         const int bit = (slot - slot0) * E + e;
 #pragma unroll
         for (int w = 0; w < kMaskWords; ++w)
@@ -300,15 +360,6 @@ struct DsRow {
   }
 };
 
-// What the gradient of a row is made of.
-struct DsFinal {
-  float m, inv_s;          // listed: w (2^((x - m) c) inv_s - p)
-  float r, rest;           // rest: rest * 2^((x - r) c)
-  float w, norm;
-  float total, tail_q, pr; // S, q_r (0 also where it is below 2^-126) and p_r, for the loss
-  bool zero, nan, bad;
-};
-
 // ln x in 64 bits of a 32-bit x: the exponent apart, so that the logarithm of
 // a large sum keeps the digits that the loss is made of.
 __device__ __forceinline__ double ln_wide(float x) {
@@ -332,7 +383,7 @@ __device__ __forceinline__ float ds_loss(const DsArgs& a, const DsList& l, const
   return (float)loss;
 }
 
-__device__ __forceinline__ DsFinal ds_final(const DsArgs& a, int64_t row, const DsList& l, float r, float s) {
+__device__ __forceinline__ DsFinal ds_final(const DsArgs& a, float weight, const DsList& l, float r, float s) {
   DsFinal f;
   f.m = fmaxf(l.m, s > 0.f ? r : -INFINITY);
   const float up = s > 0.f ? exp2_hw((r - f.m) * a.c) : 0.f;
@@ -343,18 +394,27 @@ __device__ __forceinline__ DsFinal ds_final(const DsArgs& a, int64_t row, const 
   f.tail_q = s * up / total;
   f.pr = pr;
   f.bad = bad;
-  f.w = (a.weight ? a.weight[row] : 1.f) * a.inv_t;
+  f.w = weight * a.inv_t;
   f.zero = f.w == 0.f || l.count == 0.f;
   f.nan = bad && !f.zero;
   f.inv_s = 1.f / total;
   f.r = r;
   f.norm = l.norm;
   f.rest = s > 0.f && !f.zero ? f.w * (up * f.inv_s - pr / s) : 0.f;
-  f.m = uniform(f.m);
-  f.inv_s = uniform(f.inv_s);
-  f.rest = uniform(f.rest);
-  f.w = uniform(f.w);
-  f.norm = uniform(f.norm);
+  return f;
+}
+
+// What every wave needs of it, from LDS into scalar registers.
+__device__ __forceinline__ DsFinal ds_fetch(const DsFinal& g, float r) {
+  DsFinal f;
+  f.m = uniform(g.m);
+  f.inv_s = uniform(g.inv_s);
+  f.rest = uniform(g.rest);
+  f.w = uniform(g.w);
+  f.norm = uniform(g.norm);
+  f.zero = __builtin_amdgcn_readfirstlane(g.zero);
+  f.nan = __builtin_amdgcn_readfirstlane(g.nan);
+  f.r = r;
   return f;
 }
 
@@ -406,7 +466,7 @@ __device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<k
                                               float& r, float& s, DsShared<T>& sh) {
   constexpr int E = Span<kDt>::E;
   const bool nan = s != s;
-  d.set_bits(sp, slot0, false);
+  d.set_bits(sp, slot0, slots, false);
   auto get = [&](int i, float (&v)[E]) {
     const int first = (slot0 + i) * T, t = threadIdx.x;
     Blocks<kDt>::unpack(t < sp.blocks - first ? sp.load(first, t) : masked_block<kDt>(), v);
@@ -478,23 +538,28 @@ __device__ __forceinline__ void ds_fix_listed(const DsRow<kDt, T, NB>& d, const 
   }
 }
 
+// A block's gradients, 16 bytes in one store wherever they start (the gradient's
+// rows need not start on their 16 bytes where the logits' do).
 template <int kDt>
 __device__ __forceinline__ void ds_store(const DsArgs& a, const Span<kDt>& sp, int64_t row, int first, int lane,
                                          const float (&g)[Span<kDt>::E]) {
-  constexpr int E = Span<kDt>::E;
   char* p = static_cast<char*>(a.grad) + (row * a.ld_g + sp.head) * Span<kDt>::kSize + (int64_t)first * 16 +
             (uint32_t)lane * 16u;
-  if (a.wide) {
-    *reinterpret_cast<u32x4*>(p) = pack_block<kDt>(g);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) store_el<kDt>(p, e, g[e]);
-  }
+  const u32x4 w = pack_block<kDt>(g);
+  if constexpr (kDt == GPTQ_F32) __builtin_memcpy(__builtin_assume_aligned(p, 4), &w, 16);
+  else __builtin_memcpy(__builtin_assume_aligned(p, 2), &w, 16);
 }
 
 // Row kernel: T threads hold a row of at most T NB blocks.
+//
+// What is read ahead is waited for only where nothing younger is in flight:
+// the memory operations of a wave complete in order, so a wait for one is a
+// wait for all before it, and the compiler counts none of the conditional ones
+// after it.  So the next row's ids are looked at after this row's blocks are
+// used up, its blocks and listed logits are asked for after that, and the
+// listed logits are looked at after its blocks.
 template <int kDt, int T, int NB, bool kGrad>
-__global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
+__global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void distill_row_kernel(DsArgs a) {
   __shared__ DsShared<T> sh;
   constexpr int E = Span<kDt>::E;
   const int t = threadIdx.x;
@@ -504,28 +569,24 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
   sh.head[t] = kDsEnd;
   u32x4 w[NB];
   Span<kDt> sp(a.x, row, a.ld, a.vocab);
-  auto refill = [&](const Span<kDt>& s, int blocks, int i) {
-    w[i] = masked_block<kDt>();
-    if (t < blocks - i * T) w[i] = s.load(i * T, t);
-  };
-#pragma unroll
-  for (int i = 0; i < NB; ++i) refill(sp, sp.blocks, i);
-  float xe = sp.edge(t) >= 0 ? load_el<kDt>(sp.p, sp.edge(t)) : -INFINITY;
   DsEntry n = d.read_entry(row);
   d.read_logit(n, sp);
+  uint32_t edge_bits = d.read_edge(sp);
+  {
+    const DsSource<kDt> src(sp, true);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
+  }
   lds_barrier();
   for (int which = 0;; which ^= 1) {
     const int64_t next_row = row + gridDim.x;
     const bool more = next_row < a.n_rows;
     const Span<kDt> next(a.x, more ? next_row : row, a.ld, a.vocab);
-    const int next_blocks = more ? next.blocks : 0;
-    d.take_list(sp, n, which, 0, true);
-    DsEntry ahead{-1, -INFINITY, -INFINITY};
-    if (more) ahead = d.read_entry(next_row);
-    if (t < 64) {
-      const DsList l = d.list_sums();
-      if (t == 0) sh.list = l;
-    }
+    const DsSource<kDt> src(next, more);
+    d.take_list(sp, n, which, 0, NB, true);
+    DsEntry ahead = d.read_entry(more ? next_row : row);
+    const float* weights = a.weight ? a.weight + row : a.lp;
+    float weight = *weights;
     float r = kDsFloor, rc = kDsFloor * a.c, s = 0.f;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -535,41 +596,49 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
       ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
       __builtin_amdgcn_sched_barrier(0);
     }
+    const float xe = sp.edge(t) >= 0 ? bits_value<kDt>(edge_bits) : -INFINITY;
     const float xr = d.edge_listed ? -INFINITY : xe;
-    {
+    if (t < 64) {
       float v[E];
       v[0] = xr;
 #pragma unroll
       for (int e = 1; e < E; ++e) v[e] = -INFINITY;
-      if (t < 64) ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
     }
     s *= exp2_hw(-fmaf(r, a.c, -rc));
+    d.put_logits(n);
+    asm volatile("" : "+v"(ahead.id), "+v"(ahead.lp), "+v"(weight));   // waited for here
+    d.read_logit(ahead, next);
+    const uint32_t edge_ahead = d.read_edge(next);
     ds_join<T>(r, s, a.c, sh);
-    const DsList list = sh.list;
     // a rest of -inf alone, or out of the fast way's range
     const bool exact = !(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast);
     if (exact) ds_exact_sums<kDt, T, NB>(d, sp, 0, NB, xr, r, s, sh);
-    const DsFinal f = ds_final(a, row, list, r, s);
-    if (t == 0 && a.loss) a.loss[row] = ds_loss(a, list, f, r, s);
-    if (more) d.read_logit(ahead, next);
-    float xe_next = -INFINITY;
-    if (more && next.edge(t) >= 0) xe_next = load_el<kDt>(next.p, next.edge(t));
+    if (t < 64) {
+      const DsList l = d.list_sums();
+      if (t == 0) {
+        sh.fin = ds_final(a, a.weight ? weight : 1.f, l, r, s);
+        if (a.loss) a.loss[row] = ds_loss(a, l, sh.fin, r, s);
+      }
+    }
+    lds_barrier();
     if constexpr (kGrad) {
-      const float frc = r * a.c;
-      const float rest = exact ? f.rest : f.rest * exp2_hw(-fmaf(r, a.c, -frc));
+      const DsFinal f = ds_fetch(sh.fin, r);
       if (sp.edge(t) >= 0) {
         float g[1];
         ds_gradient<false>(f, f.rest, 0.f, a.c, &xe, g, 1);
         store_el<kDt>(static_cast<char*>(a.grad) + row * a.ld_g * Span<kDt>::kSize, sp.edge(t), g[0]);
       }
       if (!(exact || f.zero || f.nan)) {
+        const float frc = r * a.c;
+        const float rest = f.rest * exp2_hw(-fmaf(r, a.c, -frc));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           float v[E], g[E];
           unpack_held<kDt>(w[i], v);
           ds_gradient<true>(f, rest, frc, a.c, v, g, E);
           if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
-          refill(next, next_blocks, i);
+          w[i] = src.load(i * T);
           __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
         }
       } else {
@@ -582,18 +651,18 @@ __global__ __launch_bounds__(T) void distill_row_kernel(DsArgs a) {
           ds_store<kDt>(a, sp, row, i * T, t, g);
         }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) refill(next, next_blocks, i);
+        for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
       }
       ds_fix_listed<kDt, T, NB>(d, sp, row, f, 0, NB, true);
     } else {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) refill(next, next_blocks, i);
+      for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
     }
     if (!more) break;
     row = next_row;
     sp = next;
     n = ahead;
-    xe = xe_next;
+    edge_bits = edge_ahead;
   }
 }
 
@@ -620,25 +689,24 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
   const int slot0 = part * a.slots;
   float xe = -INFINITY;
   if (kSums || a.grad) {
+    const DsSource<kDt> src(sp, true);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int first = (slot0 + i) * T;
-      w[i] = masked_block<kDt>();
-      if (i < a.slots && t < sp.blocks - first) w[i] = sp.load(first, t);
-    }
+    for (int i = 0; i < NB; ++i) w[i] = src.load((slot0 + min(i, a.slots - 1)) * T);
     if (edges && sp.edge(t) >= 0) xe = load_el<kDt>(sp.p, sp.edge(t));
   }
   DsEntry n = d.read_entry(row);
   if (kSums) {
     if (part == 0) d.read_logit(n, sp);
-  } else if (n.id >= 0) {
+  } else if (d.present(n)) {
     // only what this part holds: in place, other parts are being overwritten
     int thread, slot, e;
     DsRow<kDt, T, NB>::owner(sp, n.id, thread, slot, e);
     if (slot < 0 ? edges : slot >= slot0 && slot < slot0 + a.slots) d.read_logit(n, sp);
   }
   lds_barrier();
-  d.take_list(sp, n, 0, slot0, edges);
+  d.take_list(sp, n, 0, slot0, a.slots, edges);
+  d.put_logits(n);
+  lds_barrier();
   if constexpr (kSums) {
     if (part == 0 && t < 64) {
       const DsList l = d.list_sums();
@@ -688,7 +756,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     ds_join<T>(r, s, a.c, sh);
     const float* o = a.ws_list + row * 8;
     const DsList list{o[0], o[1], o[2], o[3], *reinterpret_cast<const double*>(o + 6), o[4]};
-    const DsFinal f = ds_final(a, row, list, r, s);
+    const DsFinal f = ds_final(a, a.weight ? a.weight[row] : 1.f, list, r, s);
     if (part == 0 && t == 0 && a.loss) a.loss[row] = ds_loss(a, list, f, r, s);
     if (!a.grad) return;
     if (edges && sp.edge(t) >= 0) {
@@ -754,7 +822,7 @@ static void ds_launch_parts(const DsArgs& a, hipStream_t st) {
 
 template <int kDt>
 static void ds_dispatch(const DsArgs& a, const DsPlan& p, hipStream_t st) {
-  if (p.threads == 256 && p.held == 4) ds_launch_rows<kDt, 256, 4>(a, 8, st);
+  if (p.threads == 256 && p.held == 4) ds_launch_rows<kDt, 256, 4>(a, 6, st);
   else if (p.threads == 256) ds_launch_rows<kDt, 256, 16>(a, 4, st);
   else if (p.threads == 512) ds_launch_rows<kDt, 512, 16>(a, 2, st);
   else if (p.threads == 1024 && p.held == 16) ds_launch_rows<kDt, 1024, 16>(a, 1, st);
@@ -804,8 +872,6 @@ extern "C" gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, in
   a.vocab = (int)vocab;
   a.k = k;
   a.tail = tail;
-  a.wide = (reinterpret_cast<uintptr_t>(grad) - reinterpret_cast<uintptr_t>(logits)) % 16 == 0 &&
-           (n_rows == 1 || (ld_g - ld_x) * es % 16 == 0);
   a.parts = pl.parts;
   a.slots = pl.slots;
   a.ws_sums = static_cast<float*>(workspace);
