@@ -594,6 +594,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
       unpack_held<kDt>(w[i], v);
       hide<kDt, NB>(v, d.bits(i));
       ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      if constexpr (!kGrad) w[i] = src.load(i * T);
       __builtin_amdgcn_sched_barrier(0);
     }
     const float xe = sp.edge(t) >= 0 ? bits_value<kDt>(edge_bits) : -INFINITY;
@@ -629,7 +630,16 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
         ds_gradient<false>(f, f.rest, 0.f, a.c, &xe, g, 1);
         store_el<kDt>(static_cast<char*>(a.grad) + row * a.ld_g * Span<kDt>::kSize, sp.edge(t), g[0]);
       }
-      if (!(exact || f.zero || f.nan)) {
+      if (f.zero || f.nan) {
+        float g[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = f.nan ? NAN : 0.f;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
+          w[i] = src.load(i * T);
+        }
+      } else if (!exact) {
         const float frc = r * a.c;
         const float rest = f.rest * exp2_hw(-fmaf(r, a.c, -frc));
 #pragma unroll
@@ -654,9 +664,6 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
         for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
       }
       ds_fix_listed<kDt, T, NB>(d, sp, row, f, 0, NB, true);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
     }
     if (!more) break;
     row = next_row;
