@@ -18,9 +18,10 @@
 // registers of one): sums per part, then each part joins them and writes its
 // own gradients.
 //
-// The lanes that own listed tokens find them through lists in LDS: entry i
-// hangs itself on its owner's list, the owner turns its list into one bit per
-// held logit.  An id that comes twice meets itself in one list.
+// Listed tokens are kept out of the rest by one bit per held logit, which the
+// list's entries set in LDS for the lanes that own them.  Their gradients are
+// made by the entries and stored over the rest's once those are known to be
+// written: a row later, after a wait that the row kernel makes anyway.
 #include "answer.h"
 
 namespace gq {
@@ -121,8 +122,6 @@ __device__ __forceinline__ u32x4 pack_block(const float (&g)[Span<kDt>::E]) {
   return w;
 }
 
-constexpr int kDsEnd = 255;   // end of a list
-
 // Where a lane reads that has no block to read: every load is made, so that
 // the compiler can count the ones behind it and wait for one block at a time.
 static __device__ u32x4 ds_pad[1];
@@ -146,21 +145,21 @@ struct DsSource {
   }
 };
 
-// LDS of a workgroup of T threads.  The list's entries are held twice, for
-// this row and the next one.
-template <int T>
+// LDS of a workgroup of T threads with W words of bits per lane.
+template <int T, int W>
 struct DsShared {
-  int id[2][kDsMaxK];
-  float lp[2][kDsMaxK], x[2][kDsMaxK];
-  int next[2][kDsMaxK];
-  int head[T];
+  __align__(16) int id[kDsMaxK];   // -1: absent
+  float lp[kDsMaxK];       // -inf: absent, or not the id's first place
+  float x[kDsMaxK];
+  uint32_t listed[W][T];   // a bit per held logit
+  uint32_t edge[16];       // the single logits' bits
   float red[T / 64][2];
   DsFinal fin;
 };
 
 // Reference and sum joined over the workgroup; every thread gets them.
-template <int T>
-__device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T>& sh) {
+template <int T, int W>
+__device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T, W>& sh) {
   auto fmax2 = [](float p, float q) { return fmaxf(p, q); };
   auto add2 = [](float p, float q) { return p + q; };
   const float rw = wave_reduce(r, fmax2);
@@ -204,14 +203,19 @@ template <int kDt, int T, int NB>
 struct DsRow {
   static constexpr int E = Span<kDt>::E;
   static constexpr int kMaskWords = (NB * E + 31) / 32;
-  DsShared<T>& sh;
+  using Shared = DsShared<T, kMaskWords>;
+  Shared& sh;
   const DsArgs& a;
   uint32_t mask[kMaskWords];   // held logits that are not the rest's: listed, or behind the row's end
   bool edge_listed;
-  int mine;                    // this lane's list
-  int buf;                     // which of the two lists
 
-  __device__ __forceinline__ DsRow(DsShared<T>& s, const DsArgs& args) : sh(s), a(args) {}
+  __device__ __forceinline__ DsRow(Shared& s, const DsArgs& args) : sh(s), a(args) {}
+
+  __device__ __forceinline__ void clear_bits() const {
+#pragma unroll
+    for (int i = 0; i < kMaskWords; ++i) sh.listed[i][threadIdx.x] = 0;
+    if (threadIdx.x < 16) sh.edge[threadIdx.x] = 0;
+  }
 
   // Thread and slot that hold token j of a row; slot -1: the lane's single logit.
   static __device__ __forceinline__ void owner(const Span<kDt>& sp, int j, int& thread, int& slot, int& e) {
@@ -249,61 +253,56 @@ struct DsRow {
 
   // The entries' logits into LDS.
   __device__ __forceinline__ void put_logits(const DsEntry& n) const {
-    if (present(n)) sh.x[buf][threadIdx.x] = bits_value<kDt>(n.x);
+    if (present(n)) sh.x[threadIdx.x] = bits_value<kDt>(n.x);
   }
 
-  // The row's list (without its logits) into LDS and this lane's bits out of it.  Slots
-  // [slot0, slot0 + slots) are the held ones; `edges`: the single logits, too.
-  // Two barriers.
-  __device__ __forceinline__ void take_list(const Span<kDt>& sp, const DsEntry& n, int which, int slot0, int slots,
-                                            bool edges) {
-    buf = which;
+  // The row's list (without its logits) into LDS and this lane's bits out of it.
+  // Slots [slot0, slot0 + slots) are the held ones; `edges`: the single logits,
+  // too.  The bits in LDS are clear before, and stay until clear_bits().  One
+  // barrier; absent and repeated entries are marked only after another one.
+  __device__ __forceinline__ void take_list(const Span<kDt>& sp, const DsEntry& n, int slot0, int slots, bool edges) {
     const int t = threadIdx.x;
     if (t < a.k) {
       const bool there = present(n);
-      sh.id[buf][t] = there ? n.id : -1;
-      sh.lp[buf][t] = n.lp;
-      if (there) {
-        int thread, slot, e;
-        owner(sp, n.id, thread, slot, e);
-        sh.next[buf][t] = atomicExch(&sh.head[thread], t);
+      sh.id[t] = there ? n.id : -1;
+      sh.lp[t] = n.lp;
+      int thread, slot, e;
+      owner(sp, n.id, thread, slot, e);
+      if (there && slot < 0) {
+        if (edges) sh.edge[thread] = 1;
+      } else if (there && slot >= slot0 && slot < slot0 + slots) {
+        const int bit = (slot - slot0) * E + e;
+        atomicOr(&sh.listed[bit / 32][thread], 1u << (bit % 32));
       }
     }
     lds_barrier();
-    mine = sh.head[t];
-    sh.head[t] = kDsEnd;
-    for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
-      // only the first of several places of an id counts
-      const int id = sh.id[buf][i];
-      for (int o = mine; o != kDsEnd; o = sh.next[buf][o])
-        if (o < i && sh.id[buf][o] == id) sh.lp[buf][i] = -INFINITY;
+    read_bits(sp, slot0, slots);
+    edge_listed = t < 16 && sh.edge[t & 15] != 0;
+    // an id counts at its first place: every entry against a share of the
+    // entries before it
+    const int i = t % kDsMaxK, share = t / kDsMaxK;
+    if (i < a.k) {
+      const int id = sh.id[i];
+      constexpr int kPer = kDsMaxK / (T / kDsMaxK);
+      bool again = false;
+      const int end = min((share + 1) * kPer, i);
+      for (int o = share * kPer; o < end; o += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(sh.id + o);
+        again = again || (v.x == id) || (v.y == id && o + 1 < i) || (v.z == id && o + 2 < i) || (v.w == id && o + 3 < i);
+      }
+      if (again) sh.lp[i] = -INFINITY;
     }
-    set_bits(sp, slot0, slots, edges);
-    lds_barrier();
   }
 
   // The bits of listed logits, of blocks behind the span's end and of slots not held.
-  __device__ __forceinline__ void set_bits(const Span<kDt>& sp, int slot0, int slots, bool edges) {
+  __device__ __forceinline__ void read_bits(const Span<kDt>& sp, int slot0, int slots) {
     // this lane's first slot without a block, as a bit number
     const int end = sp.blocks - slot0 * T - (int)threadIdx.x;
     const int bits = min(max(end + T - 1, 0) / T, slots) * E;
 #pragma unroll
     for (int i = 0; i < kMaskWords; ++i)
-      mask[i] = bits <= 32 * i ? ~0u : bits >= 32 * i + 32 ? 0u : ~0u << (bits - 32 * i);
-    edge_listed = false;
-    for (int i = mine; i != kDsEnd; i = sh.next[buf][i]) {
-      int thread, slot, e;
-      const int id = sh.id[buf][i];
-      owner(sp, id, thread, slot, e);
-      if (slot < 0) {
-        edge_listed = edges;
-      } else if (slot >= slot0 && slot < slot0 + slots) {
-        const int bit = (slot - slot0) * E + e;
-#pragma unroll
-        for (int w = 0; w < kMaskWords; ++w)
-          if (w == bit / 32) mask[w] |= 1u << (bit % 32);
-      }
-    }
+      mask[i] = sh.listed[i][threadIdx.x] |
+                (bits <= 32 * i ? ~0u : bits >= 32 * i + 32 ? 0u : ~0u << (bits - 32 * i));
   }
 
   // Listed bits of held block i (i known to the compiler, or any).
@@ -327,10 +326,10 @@ struct DsRow {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = lane + 64 * i;
-      has[i] = at < a.k && sh.id[buf][at < a.k ? at : 0] >= 0;
-      l[i] = has[i] ? sh.lp[buf][at] : -INFINITY;
+      has[i] = at < a.k && sh.id[at < a.k ? at : 0] >= 0;
+      l[i] = has[i] ? sh.lp[at] : -INFINITY;
       has[i] = has[i] && l[i] != -INFINITY;
-      x[i] = has[i] ? sh.x[buf][at] : -INFINITY;
+      x[i] = has[i] ? sh.x[at] : -INFINITY;
     }
     DsList d;
     d.count = (float)(__popcll(__ballot(has[0])) + __popcll(__ballot(has[1])));
@@ -463,10 +462,10 @@ __device__ __forceinline__ void hide(float (&v)[Span<kDt>::E], uint32_t listed) 
 // that the common way needs no registers for this.
 template <int kDt, int T, int NB>
 __device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<kDt>& sp, int slot0, int slots, float xe,
-                                              float& r, float& s, DsShared<T>& sh) {
+                                              float& r, float& s, typename DsRow<kDt, T, NB>::Shared& sh) {
   constexpr int E = Span<kDt>::E;
   const bool nan = s != s;
-  d.set_bits(sp, slot0, slots, false);
+  d.read_bits(sp, slot0, slots);
   auto get = [&](int i, float (&v)[E]) {
     const int first = (slot0 + i) * T, t = threadIdx.x;
     Blocks<kDt>::unpack(t < sp.blocks - first ? sp.load(first, t) : masked_block<kDt>(), v);
@@ -506,7 +505,7 @@ __device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<k
     for (int e = 0; e < E; ++e) s += exp2_hw((v[e] - m) * d.a.c);
   }
   s += exp2_hw((xe - m) * d.a.c);
-  ds_join<T>(r, s, d.a.c, sh);
+  ds_join(r, s, d.a.c, sh);
 }
 
 // Gradients of n logits of the rest.  kFast: rc is r c rounded, `rest` made
@@ -521,22 +520,29 @@ __device__ __forceinline__ void ds_gradient(const DsFinal& f, float rest, float 
   }
 }
 
-// The gradients of the listed tokens that this lane owns, over what its own
-// stores just left there.
+// The gradient of a list's entry: id -1 where there is nothing to store.
+struct DsFix {
+  int id;
+  float g;
+};
 template <int kDt, int T, int NB>
-__device__ __forceinline__ void ds_fix_listed(const DsRow<kDt, T, NB>& d, const Span<kDt>& sp, int64_t row,
-                                              const DsFinal& f, int slot0, int slots, bool edges) {
-  if (f.zero || f.nan) return;
-  for (int i = d.mine; i != kDsEnd; i = d.sh.next[d.buf][i]) {
-    const float l = d.sh.lp[d.buf][i];
-    const int id = d.sh.id[d.buf][i];
-    int thread, slot, e;
-    DsRow<kDt, T, NB>::owner(sp, id, thread, slot, e);
-    if (l == -INFINITY || !(slot < 0 ? edges : slot >= slot0 && slot < slot0 + slots)) continue;
-    const float g = f.w * (exp2_hw((d.sh.x[d.buf][i] - f.m) * d.a.c) * f.inv_s - exp2_hw((l - f.norm) * kLog2e));
-    store_el<kDt>(d.a.grad, row * d.a.ld_g + id, g);
+__device__ __forceinline__ DsFix ds_fix(const DsRow<kDt, T, NB>& d, const DsFinal& f) {
+  DsFix x{-1, 0.f};
+  const int t = threadIdx.x;
+  if (t < d.a.k && !(f.zero || f.nan)) {
+    const float l = d.sh.lp[t];
+    if (l != -INFINITY) x.id = d.sh.id[t];
+    x.g = f.w * (exp2_hw((d.sh.x[t] - f.m) * d.a.c) * f.inv_s - exp2_hw((l - f.norm) * kLog2e));
   }
+  return x;
 }
+template <int kDt>
+__device__ __forceinline__ void ds_store_fix(const DsArgs& a, int64_t row, const DsFix& x) {
+  if (x.id >= 0) store_el<kDt>(a.grad, row * a.ld_g + x.id, x.g);
+}
+
+// Every memory operation of this wave is done.
+__device__ __forceinline__ void memory_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // A block's gradients, 16 bytes in one store wherever they start (the gradient's
 // rows need not start on their 16 bytes where the logits' do).
@@ -560,13 +566,13 @@ __device__ __forceinline__ void ds_store(const DsArgs& a, const Span<kDt>& sp, i
 // listed logits are looked at after its blocks.
 template <int kDt, int T, int NB, bool kGrad>
 __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void distill_row_kernel(DsArgs a) {
-  __shared__ DsShared<T> sh;
+  __shared__ typename DsRow<kDt, T, NB>::Shared sh;
   constexpr int E = Span<kDt>::E;
   const int t = threadIdx.x;
   int64_t row = blockIdx.x;
   if (row >= a.n_rows) return;
   DsRow<kDt, T, NB> d(sh, a);
-  sh.head[t] = kDsEnd;
+  d.clear_bits();
   u32x4 w[NB];
   Span<kDt> sp(a.x, row, a.ld, a.vocab);
   DsEntry n = d.read_entry(row);
@@ -578,12 +584,14 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
     for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
   }
   lds_barrier();
-  for (int which = 0;; which ^= 1) {
+  DsFix fix{-1, 0.f};
+  int64_t fix_row = row;
+  for (;;) {
     const int64_t next_row = row + gridDim.x;
     const bool more = next_row < a.n_rows;
     const Span<kDt> next(a.x, more ? next_row : row, a.ld, a.vocab);
     const DsSource<kDt> src(next, more);
-    d.take_list(sp, n, which, 0, NB, true);
+    d.take_list(sp, n, 0, NB, true);
     DsEntry ahead = d.read_entry(more ? next_row : row);
     const float* weights = a.weight ? a.weight + row : a.lp;
     float weight = *weights;
@@ -608,10 +616,13 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
     }
     s *= exp2_hw(-fmaf(r, a.c, -rc));
     d.put_logits(n);
-    asm volatile("" : "+v"(ahead.id), "+v"(ahead.lp), "+v"(weight));   // waited for here
+    // the ids read ahead, and the last row's gradients in memory
+    if constexpr (kGrad) memory_done();
+    asm volatile("" : "+v"(ahead.id), "+v"(ahead.lp), "+v"(weight));
     d.read_logit(ahead, next);
     const uint32_t edge_ahead = d.read_edge(next);
-    ds_join<T>(r, s, a.c, sh);
+    ds_join(r, s, a.c, sh);
+    if constexpr (kGrad) ds_store_fix<kDt>(a, fix_row, fix);
     // a rest of -inf alone, or out of the fast way's range
     const bool exact = !(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast);
     if (exact) ds_exact_sums<kDt, T, NB>(d, sp, 0, NB, xr, r, s, sh);
@@ -622,9 +633,12 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
         if (a.loss) a.loss[row] = ds_loss(a, l, sh.fin, r, s);
       }
     }
+    d.clear_bits();
     lds_barrier();
     if constexpr (kGrad) {
       const DsFinal f = ds_fetch(sh.fin, r);
+      fix = ds_fix<kDt, T, NB>(d, f);
+      fix_row = row;
       if (sp.edge(t) >= 0) {
         float g[1];
         ds_gradient<false>(f, f.rest, 0.f, a.c, &xe, g, 1);
@@ -663,13 +677,17 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
 #pragma unroll
         for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
       }
-      ds_fix_listed<kDt, T, NB>(d, sp, row, f, 0, NB, true);
     }
     if (!more) break;
     row = next_row;
     sp = next;
     n = ahead;
     edge_bits = edge_ahead;
+  }
+  if constexpr (kGrad) {
+    memory_done();
+    lds_barrier();
+    ds_store_fix<kDt>(a, fix_row, fix);
   }
 }
 
@@ -683,14 +701,14 @@ template <int kDt, int NB, bool kSums>
 __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) {
   constexpr int T = kDsPartThreads;
   constexpr int E = Span<kDt>::E;
-  __shared__ DsShared<T> sh;
+  __shared__ typename DsRow<kDt, T, NB>::Shared sh;
   const int t = threadIdx.x;
   const int per_row = kSums || a.grad ? a.parts : 1;
   const int64_t row = blockIdx.x / per_row;
   const int part = blockIdx.x % per_row;
   const Span<kDt> sp(a.x, row, a.ld, a.vocab);
   DsRow<kDt, T, NB> d(sh, a);
-  sh.head[t] = kDsEnd;
+  d.clear_bits();
   u32x4 w[NB];
   const bool edges = part == 0;
   const int slot0 = part * a.slots;
@@ -702,16 +720,16 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     if (edges && sp.edge(t) >= 0) xe = load_el<kDt>(sp.p, sp.edge(t));
   }
   DsEntry n = d.read_entry(row);
-  if (kSums) {
-    if (part == 0) d.read_logit(n, sp);
-  } else if (d.present(n)) {
+  bool own = part == 0;
+  if (!kSums && d.present(n)) {
     // only what this part holds: in place, other parts are being overwritten
     int thread, slot, e;
     DsRow<kDt, T, NB>::owner(sp, n.id, thread, slot, e);
-    if (slot < 0 ? edges : slot >= slot0 && slot < slot0 + a.slots) d.read_logit(n, sp);
+    own = slot < 0 ? edges : slot >= slot0 && slot < slot0 + a.slots;
   }
+  if (own) d.read_logit(n, sp);
   lds_barrier();
-  d.take_list(sp, n, 0, slot0, a.slots, edges);
+  d.take_list(sp, n, slot0, a.slots, edges);
   d.put_logits(n);
   lds_barrier();
   if constexpr (kSums) {
@@ -745,7 +763,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
     }
     s *= exp2_hw(-fmaf(r, a.c, -rc));
-    ds_join<T>(r, s, a.c, sh);
+    ds_join(r, s, a.c, sh);
     if (!(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast)) ds_exact_sums<kDt, T, NB>(d, sp, slot0, a.slots, xr, r, s, sh);
     if (t == 0) {
       float* o = a.ws_sums + (row * a.parts + part) * 2;
@@ -760,7 +778,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       s = (s == 0.f ? 0.f : s * exp2_hw((r - to) * a.c)) + (o[1] == 0.f ? 0.f : o[1] * exp2_hw((o[0] - to) * a.c));
       r = to;
     }
-    ds_join<T>(r, s, a.c, sh);
+    ds_join(r, s, a.c, sh);
     const float* o = a.ws_list + row * 8;
     const DsList list{o[0], o[1], o[2], o[3], *reinterpret_cast<const double*>(o + 6), o[4]};
     const DsFinal f = ds_final(a, a.weight ? a.weight[row] : 1.f, list, r, s);
@@ -780,7 +798,10 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       ds_gradient<false>(f, f.rest, 0.f, a.c, v, g, E);
       ds_store<kDt>(a, sp, row, first, t, g);
     }
-    ds_fix_listed<kDt, T, NB>(d, sp, row, f, slot0, a.slots, edges);
+    const DsFix fix = ds_fix<kDt, T, NB>(d, f);
+    memory_done();
+    lds_barrier();
+    if (own) ds_store_fix<kDt>(a, row, fix);
   }
 }
 
