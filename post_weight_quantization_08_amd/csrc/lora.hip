@@ -1,9 +1,40 @@
-// Low-rank adapters of many requests beside a shared projection.
+// Low-rank adapters of many requests beside a shared projection:
+//   Y[m] = base[m] + s_a (X[m] A_a^T) B_a^T,   a = adapter[m].
+//
+// Two products through T = X A^T (fp32, in the workspace).  Which rows share
+// an adapter is known to the GPU alone.
+//
+// Few tokens (decode, kLoraFew): every token has its own adapter, so each
+// token's factors are read for it alone, on vector units.  T: one wave per
+// (token, rank).  Y: the r / 8 lanes of a column each take 8 ranks (16 bytes of
+// B), so a wave reads B in order, and exchange their sums.
+//
+// Many tokens (prompts): tiles of 32 tokens on MFMA (16x16x32).  A tile takes
+// one pass per adapter that occurs in it; a request's tokens lie together, so
+// most tiles need one.  Rows of another adapter are left out of a pass by
+// selecting, never by multiplying with zero: a NaN or infinity in one adapter
+// does not reach another's rows.  For the second product T is kept as two
+// 16-bit terms, whose sum carries 16 significant bits (bf16) or 22 (fp16; rows
+// of T are scaled by a power of two first, so that neither their size nor
+// their smallness leaves fp16's range): 16 bits alone would put an error of
+// 2^-9 or 2^-12 of the adapter's part into fp32 results.  Tokens are the MFMA's
+// columns and output columns its rows, dealt so that a lane ends up with eight
+// consecutive outputs of one token: base and Y move 16 or 32 bytes at a time.
+// Operands are read from global memory in the form that the MFMA takes (8
+// consecutive elements per lane), at any alignment.
+//
+// Bound by memory: X, base and Y once, the factors from L2 (a factor's matrix
+// serves every tile of its adapter).
 #include "answer.h"
 
 namespace gq {
 
 size_t w4a16_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out);
+
+constexpr int kLoraFew = 64;        // tokens up to which every one is taken by itself
+constexpr int kLoraTile = 32;       // tokens of an MFMA tile
+constexpr int kLoraCols = 512;      // output columns of a workgroup
+constexpr int kLoraMaxRank = 128;
 
 struct LoraArgs {
   const uint16_t* X;
@@ -13,57 +44,458 @@ struct LoraArgs {
   const int32_t* adapter;
   const void* base;
   void* Y;
-  float* T;                // [M][rank], scaled
+  float* T;                // [splits][M][rank padded to 8]
   int64_t ld_x, ld_b, ld_y, M, d_out;
   int d_in, rank, n;
+  int rp;                  // rank padded to 8
+  int splits, k_split;     // parts of the first product's sum, and their length
 };
 
-// T[m][r] = scale X[m] . A_a[r]: one wave per (token, rank).
 template <int kDt>
-__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
-  const int64_t m = blockIdx.x;
-  const int ad = a.adapter[m];
-  if (ad < 0 || ad >= a.n) return;
+__device__ __forceinline__ float lo16(uint32_t w) {
+  if constexpr (kDt == GPTQ_F16) return f16_bits_to_f32(w & 0xFFFFu);
+  else return __uint_as_float(w << 16);
+}
+template <int kDt>
+__device__ __forceinline__ float hi16(uint32_t w) {
+  if constexpr (kDt == GPTQ_F16) return f16_bits_to_f32(w >> 16);
+  else return __uint_as_float(w & 0xFFFF0000u);
+}
+
+// 8 elements from any address.
+__device__ __forceinline__ u32x4 load8(const uint16_t* p) {
+  u32x4 w;
+  __builtin_memcpy(&w, __builtin_assume_aligned(p, 2), 16);
+  return w;
+}
+
+// Elements k .. k + 7 of a row of n elements, zero behind its end.
+__device__ __forceinline__ u32x4 load8_end(const uint16_t* row, int k, int n) {
+  if (k + 8 <= n) return load8(row + k);
+  u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (k + i < n) w[i / 2] |= (uint32_t)row[k + i] << (16 * (i & 1));
+  return w;
+}
+
+// ---------------------------------------------------------------- few tokens
+// T[m][r] = s_a X[m] . A_a[r].
+template <int kDt>
+__global__ __launch_bounds__(256) void lora_down_few_kernel(LoraArgs a) {
   const int lane = threadIdx.x & 63;
-  for (int r = threadIdx.x >> 6; r < a.rank; r += 4) {
-    const uint16_t* Ar = a.A + ((int64_t)ad * a.rank + r) * a.d_in;
-    float s = 0.f;
-    for (int i = lane; i < a.d_in; i += 64) s = fmaf(load_el<kDt>(a.X, m * a.ld_x + i), load_el<kDt>(Ar, i), s);
-    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    if (lane == 0) a.T[m * a.rank + r] = (a.scale ? a.scale[ad] : 1.f) * s;
-  }
-}
-
-// Y[m][n] = base[m][n] + T[m] . B_a[n].
-template <int kDt, int kY>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
-  const int64_t m = blockIdx.x;
-  const int ad = a.adapter[m];
-  const bool on = ad >= 0 && ad < a.n;
-  for (int64_t n = threadIdx.x; n < a.d_out; n += 256) {
-    float s = a.base ? load_el<kY>(a.base, m * a.ld_b + n) : 0.f;
-    if (on) {
-      float d = 0.f;
-      const uint16_t* b = a.B + ((int64_t)ad * a.d_out + n) * a.rank;
-      for (int r = 0; r < a.rank; ++r) d = fmaf(a.T[m * a.rank + r], load_el<kDt>(b, r), d);
-      s += d;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= a.M * a.rank) return;
+  const int64_t m = at / a.rank;
+  const int r = (int)(at - m * a.rank);
+  const int ad = __builtin_amdgcn_readfirstlane(a.adapter[m]);
+  if (ad < 0 || ad >= a.n) return;
+  const uint16_t* x = a.X + m * a.ld_x;
+  const uint16_t* f = a.A + ((int64_t)ad * a.rank + r) * a.d_in;
+  float s0 = 0.f, s1 = 0.f;
+  auto add = [&](u32x4 u, u32x4 v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s0 = fmaf(lo16<kDt>(u[i]), lo16<kDt>(v[i]), s0);
+      s1 = fmaf(hi16<kDt>(u[i]), hi16<kDt>(v[i]), s1);
     }
-    store_el<kY>(a.Y, m * a.ld_y + n, s);
+  };
+  constexpr int kU = 4;
+  int k = 0;
+  for (; k + 512 * kU <= a.d_in; k += 512 * kU) {
+    u32x4 u[kU], v[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      u[i] = load8(x + k + i * 512 + lane * 8);
+      v[i] = load8(f + k + i * 512 + lane * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) add(u[i], v[i]);
+  }
+  for (; k < a.d_in; k += 512) add(load8_end(x, k + lane * 8, a.d_in), load8_end(f, k + lane * 8, a.d_in));
+  const float s = wave_reduce(s0 + s1, [](float p, float q) { return p + q; });
+  if (lane == 0) a.T[m * a.rp + r] = (a.scale ? a.scale[ad] : 1.f) * s;
+}
+
+// Y[m][n] = base[m][n] + T[m] . B_a[n]: a wave takes 64 columns, kL lanes each
+// column's ranks 8 at a time.
+template <int kDt, int kY, int kL>
+__global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a) {
+  constexpr int kPer = 64 / kL;            // columns of a step
+  const int lane = threadIdx.x & 63;
+  const int64_t m = blockIdx.y;
+  const int64_t n0 = (int64_t)blockIdx.x * 256 + (threadIdx.x & ~63);
+  const int ad = __builtin_amdgcn_readfirstlane(a.adapter[m]);
+  const int64_t n = n0 + lane;
+  float y = 0.f;
+  if (a.base && n < a.d_out) y = load_el<kY>(a.base, m * a.ld_b + n);
+  if (ad >= 0 && ad < a.n && n0 < a.d_out) {
+    const int k = lane % kL * 8;
+    u32x4 b[kL];
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      const int64_t col = n0 + i * kPer + lane / kL;
+      const uint16_t* row = a.B + ((int64_t)ad * a.d_out + (col < a.d_out ? col : a.d_out - 1)) * a.rank;
+      b[i] = load8_end(row, k, a.rank);
+    }
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = k + i < a.rank ? a.T[m * a.rp + k + i] : 0.f;
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // beyond the rank both are zero
+        s = fmaf(t[2 * e], lo16<kDt>(b[i][e]), s);
+        s = fmaf(t[2 * e + 1], hi16<kDt>(b[i][e]), s);
+      }
+#pragma unroll
+      for (int d = 1; d < kL; d <<= 1) s += __shfl_xor(s, d);
+      const float got = __shfl(s, lane % kPer * kL);
+      if (lane / kPer == i) mine = got;
+    }
+    y += mine;
+  }
+  if (n < a.d_out) store_el<kY>(a.Y, m * a.ld_y + n, y);
+}
+
+// ---------------------------------------------------------------- many tokens
+template <int kDt>
+__device__ __forceinline__ f32x4 lora_mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (kDt == GPTQ_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                  0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+}
+
+// Calls f(adapter, lanes' match) for every adapter among the tile's 32 tokens;
+// `mine` is the adapter of token lane % 32, or -1.
+template <class F>
+__device__ __forceinline__ void for_each_adapter(int mine, F f) {
+  uint32_t left = (uint32_t)__ballot(mine >= 0);
+  while (left) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+    left &= ~(uint32_t)__ballot(mine == a);
+    f(a);
   }
 }
 
-size_t lora_workspace_bytes(int64_t M, int64_t, int64_t, int64_t rank) { return align_up((size_t)M * rank * 4, 256); }
+__device__ __forceinline__ int lora_adapter(const LoraArgs& a, int64_t m) {
+  const int ad = m < a.M ? a.adapter[m] : -1;
+  return ad < a.n ? ad : -1;
+}
+
+// T of 32 tokens over one part of the sum: four waves take its 64-element steps
+// in turn and their sums meet in LDS.  kR rank tiles of 16.  D: rows = ranks,
+// columns = tokens.
+template <int kDt, int kR>
+__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
+  constexpr int kStride = kR * 16 + 4;     // floats of a token in LDS
+  __shared__ __align__(16) float red[4][kLoraTile][kStride];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, q = lane >> 4;
+  const int64_t m0 = (int64_t)blockIdx.x * kLoraTile;
+  const int k0 = blockIdx.y * a.k_split, k1 = min(k0 + a.k_split, a.d_in);
+  const int mine = lora_adapter(a, m0 + (lane & 31));
+  const uint16_t* x[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) x[t] = a.X + min(m0 + t * 16 + c16, a.M - 1) * a.ld_x;
+  for_each_adapter(mine, [&](int ad) {
+    const uint16_t* f[kR];
+#pragma unroll
+    for (int t = 0; t < kR; ++t) f[t] = a.A + ((int64_t)ad * a.rank + min(t * 16 + c16, a.rank - 1)) * a.d_in;
+    f32x4 acc[kR][2];
+#pragma unroll
+    for (int t = 0; t < kR; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = k0 + wave * 64; k < k1; k += 256) {
+      u32x4 xv[2][2], av[2][kR];
+      if (k + 64 <= k1) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) xv[j][t] = load8(x[t] + k + 32 * j + 8 * q);
+#pragma unroll
+          for (int t = 0; t < kR; ++t) av[j][t] = load8(f[t] + k + 32 * j + 8 * q);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) xv[j][t] = load8_end(x[t], k + 32 * j + 8 * q, k1);
+#pragma unroll
+          for (int t = 0; t < kR; ++t) av[j][t] = load8_end(f[t], k + 32 * j + 8 * q, k1);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < kR; ++t) {
+          acc[t][0] = lora_mfma<kDt>(av[j][t], xv[j][0], acc[t][0]);
+          acc[t][1] = lora_mfma<kDt>(av[j][t], xv[j][1], acc[t][1]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kR; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) *reinterpret_cast<f32x4*>(&red[wave][u * 16 + c16][t * 16 + 4 * q]) = acc[t][u];
+    __syncthreads();
+    // 8 threads per token
+    const int tok = threadIdx.x >> 3;
+    if (__shfl(mine, tok & 31) == ad) {
+      float* out = a.T + ((int64_t)blockIdx.y * a.M + m0 + tok) * a.rp;
+      for (int r = (threadIdx.x & 7) * 4; r < a.rp; r += 32) {
+        f32x4 s = *reinterpret_cast<const f32x4*>(&red[0][tok][r]);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) s += *reinterpret_cast<const f32x4*>(&red[w][tok][r]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = r + i < a.rank ? s[i] : 0.f;
+        *reinterpret_cast<f32x4*>(out + r) = s;
+      }
+    }
+    __syncthreads();
+  });
+}
+
+// hi and lo terms of 8 values, as MFMA operands.
+template <int kDt>
+__device__ __forceinline__ void lora_split(const float (&v)[8], u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = v[2 * i + e];
+      if constexpr (kDt == GPTQ_F16) {
+        const _Float16 p = (_Float16)x, r = (_Float16)(x - (float)p);
+        h[e] = __builtin_bit_cast(uint16_t, p);
+        l[e] = __builtin_bit_cast(uint16_t, r);
+      } else {
+        const __bf16 p = (__bf16)x, r = (__bf16)(x - (float)p);
+        h[e] = __builtin_bit_cast(uint16_t, p);
+        l[e] = __builtin_bit_cast(uint16_t, r);
+      }
+    }
+    hi[i] = h[0] | h[1] << 16;
+    lo[i] = l[0] | l[1] << 16;
+  }
+}
+
+// 32 tokens by kLoraCols columns; kS steps of 32 ranks.
+template <int kDt, int kY, int kS>
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, q = lane >> 4;
+  const int64_t m0 = (int64_t)blockIdx.x * kLoraTile;
+  const int mine = lora_adapter(a, m0 + (lane & 31));
+  int own[2];                              // adapters of this lane's two tokens
+  float grow[2];                           // 2^e that T's terms were divided by
+  u32x4 hi[2][kS], lo[2][kS];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    own[t] = __shfl(mine, t * 16 + c16);
+    const int64_t m = m0 + t * 16 + c16;
+    const float sc = own[t] >= 0 && a.scale ? a.scale[own[t]] : 1.f;
+    float v[kS][8];
+    float big = 0.f;
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      const int k = s * 32 + 8 * q;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
+      if (own[t] >= 0 && k < a.rp) {
+        for (int p = 0; p < a.splits; ++p) {
+          const float* src = a.T + ((int64_t)p * a.M + m) * a.rp + k;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[s][i] += src[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[s][i] *= sc;
+          big = fmaxf(big, fabsf(v[s][i]));
+        }
+      }
+    }
+    grow[t] = 1.f;
+    if constexpr (kDt == GPTQ_F16) {
+      big = fmaxf(big, __shfl_xor(big, 16));
+      big = fmaxf(big, __shfl_xor(big, 32));
+      if (big > 0.f && big < INFINITY) {
+        int e;
+        frexpf(big, &e);
+        grow[t] = ldexpf(1.f, e - 14);   // the largest below 2^14: the second terms stay normal numbers
+#pragma unroll
+        for (int s = 0; s < kS; ++s)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[s][i] = ldexpf(v[s][i], 14 - e);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kS; ++s) lora_split<kDt>(v[s], hi[t][s], lo[t][s]);
+  }
+  const int64_t n_first = (int64_t)blockIdx.y * kLoraCols;
+  const int64_t n_end = n_first + kLoraCols < a.d_out ? n_first + kLoraCols : a.d_out;
+  for (int64_t n = n_first + wave * 32; n < n_end; n += 128) {
+    const int64_t col = n + 8 * q;         // this lane's eight columns
+    const bool whole = col + 8 <= a.d_out;
+    float y[2][8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t m = m0 + t * 16 + c16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[t][i] = 0.f;
+      if (a.base && m < a.M) {
+        if (whole) {
+          if constexpr (kY == GPTQ_F32) {
+            const float* p = static_cast<const float*>(a.base) + m * a.ld_b + col;
+            f32x4 u, w;
+            __builtin_memcpy(&u, __builtin_assume_aligned(p, 4), 16);
+            __builtin_memcpy(&w, __builtin_assume_aligned(p + 4, 4), 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[t][i] = u[i];
+              y[t][4 + i] = w[i];
+            }
+          } else {
+            const u32x4 u = load8(static_cast<const uint16_t*>(a.base) + m * a.ld_b + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[t][2 * i] = lo16<kY>(u[i]);
+              y[t][2 * i + 1] = hi16<kY>(u[i]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + i < a.d_out) y[t][i] = load_el<kY>(a.base, m * a.ld_b + col + i);
+        }
+      }
+    }
+    f32x4 acc[2][2];                       // [token tile][column half]
+#pragma unroll
+    for (int t = 0; t < 2; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for_each_adapter(mine, [&](int ad) {
+      f32x4 d[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) d[t][0] = d[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // the MFMA's row c16 is column 8 (c16 / 4) + 4 h + c16 % 4
+        int64_t bc = n + 8 * (c16 >> 2) + 4 * h + (c16 & 3);
+        bc = bc < a.d_out ? bc : a.d_out - 1;
+        const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
+        u32x4 b[kS];
+#pragma unroll
+        for (int s = 0; s < kS; ++s) b[s] = load8_end(row, s * 32 + 8 * q, a.rank);
+#pragma unroll
+        for (int s = 0; s < kS; ++s)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            d[t][h] = lora_mfma<kDt>(b[s], lo[t][s], d[t][h]);
+            d[t][h] = lora_mfma<kDt>(b[s], hi[t][s], d[t][h]);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][h][i] = own[t] == ad ? d[t][h][i] : acc[t][h][i];
+    });
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t m = m0 + t * 16 + c16;
+      if (m >= a.M) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[t][4 * h + i] = fmaf(acc[t][h][i], grow[t], y[t][4 * h + i]);
+      if (whole) {
+        if constexpr (kY == GPTQ_F32) {
+          float* p = static_cast<float*>(a.Y) + m * a.ld_y + col;
+          __builtin_memcpy(__builtin_assume_aligned(p, 4), &y[t][0], 16);
+          __builtin_memcpy(__builtin_assume_aligned(p + 4, 4), &y[t][4], 16);
+        } else {
+          typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+          u16x8 w;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (kY == GPTQ_F16) w[i] = __builtin_bit_cast(uint16_t, (_Float16)y[t][i]);
+            else w[i] = __builtin_bit_cast(uint16_t, (__bf16)y[t][i]);
+          }
+          __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(a.Y) + m * a.ld_y + col, 2), &w, 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col + i < a.d_out) store_el<kY>(a.Y, m * a.ld_y + col + i, y[t][i]);
+      }
+    }
+  }
+}
+
+struct LoraPlan {
+  int rp, splits, k_split;
+  size_t total;
+};
+
+static LoraPlan lora_plan(int64_t M, int64_t d_in, int64_t rank) {
+  LoraPlan p;
+  p.rp = (int)(cdiv(rank, 8) * 8);
+  p.splits = 1;
+  if (M > kLoraFew) {
+    // parts of the sum until every CU has two workgroups, of at least one step per wave
+    const int64_t tiles = cdiv(M, kLoraTile);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(512, tiles), d_in / 256));
+  }
+  p.k_split = (int)(cdiv(cdiv(d_in, p.splits), 64) * 64);
+  p.splits = (int)cdiv(d_in, p.k_split);
+  p.total = align_up((size_t)p.splits * M * p.rp * 4, 256);
+  return p;
+}
+
+size_t lora_workspace_bytes(int64_t M, int64_t d_in, int64_t, int64_t rank) { return lora_plan(M, d_in, rank).total; }
 
 size_t w4a16_lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank) {
   return align_up(w4a16_workspace_bytes(M, d_in, d_out), 256) + lora_workspace_bytes(M, d_in, d_out, rank);
 }
 
+template <int kDt, int kY>
+static void lora_up_few(const LoraArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.d_out, 256), (unsigned)a.M);
+  if (a.rp <= 8) hipLaunchKernelGGL((lora_up_few_kernel<kDt, kY, 1>), grid, dim3(256), 0, st, a);
+  else if (a.rp <= 16) hipLaunchKernelGGL((lora_up_few_kernel<kDt, kY, 2>), grid, dim3(256), 0, st, a);
+  else if (a.rp <= 32) hipLaunchKernelGGL((lora_up_few_kernel<kDt, kY, 4>), grid, dim3(256), 0, st, a);
+  else if (a.rp <= 64) hipLaunchKernelGGL((lora_up_few_kernel<kDt, kY, 8>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((lora_up_few_kernel<kDt, kY, 16>), grid, dim3(256), 0, st, a);
+}
+
+template <int kDt, int kY>
+static void lora_up(const LoraArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.M, kLoraTile), (unsigned)cdiv(a.d_out, kLoraCols));
+  if (a.rp <= 32) hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 1>), grid, dim3(256), 0, st, a);
+  else if (a.rp <= 64) hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 2>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 4>), grid, dim3(256), 0, st, a);
+}
+
 template <int kDt>
 static void lora_launch(const LoraArgs& a, int32_t y_dtype, hipStream_t st) {
-  const dim3 grid((unsigned)a.M);
-  hipLaunchKernelGGL(lora_down_kernel<kDt>, grid, dim3(256), 0, st, a);
-  if (y_dtype == GPTQ_F32) hipLaunchKernelGGL((lora_up_kernel<kDt, GPTQ_F32>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((lora_up_kernel<kDt, kDt>), grid, dim3(256), 0, st, a);
+  if (a.M <= kLoraFew) {
+    hipLaunchKernelGGL(lora_down_few_kernel<kDt>, dim3((unsigned)cdiv(a.M * a.rank, 4)), dim3(256), 0, st, a);
+    if (y_dtype == GPTQ_F32) lora_up_few<kDt, GPTQ_F32>(a, st);
+    else lora_up_few<kDt, kDt>(a, st);
+    return;
+  }
+  const dim3 grid((unsigned)cdiv(a.M, kLoraTile), (unsigned)a.splits);
+  if (a.rank <= 16) hipLaunchKernelGGL((lora_down_kernel<kDt, 1>), grid, dim3(256), 0, st, a);
+  else if (a.rank <= 32) hipLaunchKernelGGL((lora_down_kernel<kDt, 2>), grid, dim3(256), 0, st, a);
+  else if (a.rank <= 64) hipLaunchKernelGGL((lora_down_kernel<kDt, 4>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((lora_down_kernel<kDt, 8>), grid, dim3(256), 0, st, a);
+  if (y_dtype == GPTQ_F32) lora_up<kDt, GPTQ_F32>(a, st);
+  else lora_up<kDt, kDt>(a, st);
 }
 
 }  // namespace gq
@@ -83,18 +515,36 @@ extern "C" gptq_status gptq_lora_add(const void* X, int32_t x_dtype, int64_t M, 
   GQ_CHECK_ARG(base == nullptr || (ld_b >= d_out && ld_b <= ((int64_t)1 << 32)));
   GQ_CHECK_ARG(base == nullptr || base != Y || ld_b == ld_y);
   GQ_CHECK_ARG(n_adapters >= 1 && n_adapters <= ((int64_t)1 << 20) && rank >= 1);
-  if (rank > 128) return GPTQ_EUNSUPPORTED;
+  if (rank > kLoraMaxRank) return GPTQ_EUNSUPPORTED;
   if (M == 0) return GPTQ_OK;
   const size_t ys = y_dtype == GPTQ_F32 ? 4 : 2;
   GQ_CHECK_ARG(X && A && B && adapter && Y);
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(X) % 2 == 0 && reinterpret_cast<uintptr_t>(A) % 2 == 0 &&
                reinterpret_cast<uintptr_t>(B) % 2 == 0 && reinterpret_cast<uintptr_t>(Y) % ys == 0 &&
                reinterpret_cast<uintptr_t>(base) % ys == 0);
-  if (workspace == nullptr || ws_bytes < lora_workspace_bytes(M, d_in, d_out, rank)) return GPTQ_ENOMEM;
+  const LoraPlan pl = lora_plan(M, d_in, rank);
+  if (workspace == nullptr || ws_bytes < pl.total) return GPTQ_ENOMEM;
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(workspace) % 256 == 0);
-  LoraArgs a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scale,
-             adapter, base, Y, static_cast<float*>(workspace), ld_x, ld_b, ld_y, M, d_out, (int)d_in, rank,
-             (int)n_adapters};
+  LoraArgs a{};
+  a.X = static_cast<const uint16_t*>(X);
+  a.A = static_cast<const uint16_t*>(A);
+  a.B = static_cast<const uint16_t*>(B);
+  a.scale = scale;
+  a.adapter = adapter;
+  a.base = base;
+  a.Y = Y;
+  a.T = static_cast<float*>(workspace);
+  a.ld_x = ld_x;
+  a.ld_b = ld_b;
+  a.ld_y = ld_y;
+  a.M = M;
+  a.d_out = d_out;
+  a.d_in = (int)d_in;
+  a.rank = rank;
+  a.n = (int)n_adapters;
+  a.rp = pl.rp;
+  a.splits = pl.splits;
+  a.k_split = pl.k_split;
   hipStream_t st = static_cast<hipStream_t>(stream);
   TimedScope ts(kTimeLora, st);
   if (x_dtype == GPTQ_F16) lora_launch<GPTQ_F16>(a, y_dtype, st);
@@ -113,7 +563,7 @@ extern "C" gptq_status gptq_w4a16_lora_matmul(const void* X, int32_t x_dtype, in
   GQ_CHECK_ARG(A && B && adapter);
   GQ_CHECK_ARG(ld_x <= ((int64_t)1 << 32) && ld_y <= ((int64_t)1 << 32));
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(A) % 2 == 0 && reinterpret_cast<uintptr_t>(B) % 2 == 0);
-  if (rank > 128 || M > 64) return GPTQ_EUNSUPPORTED;
+  if (rank > kLoraMaxRank || M > 64) return GPTQ_EUNSUPPORTED;
   if (workspace != nullptr && ws_bytes < w4a16_lora_workspace_bytes(M, d_in, d_out, rank)) return GPTQ_ENOMEM;
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(workspace) % 256 == 0);
   const size_t w4 = align_up(w4a16_workspace_bytes(M, d_in, d_out), 256);
