@@ -25,7 +25,7 @@
 //
 // Bound by memory: X, base and Y once, the factors from L2 (a factor's matrix
 // serves every tile of its adapter).
-#include "answer.h"
+#include "lora.h"
 
 namespace gq {
 
@@ -51,70 +51,10 @@ struct LoraArgs {
   int splits, k_split;     // parts of the first product's sum, and their length
 };
 
-template <int kDt>
-__device__ __forceinline__ float lo16(uint32_t w) {
-  if constexpr (kDt == GPTQ_F16) return f16_bits_to_f32(w & 0xFFFFu);
-  else return __uint_as_float(w << 16);
-}
-template <int kDt>
-__device__ __forceinline__ float hi16(uint32_t w) {
-  if constexpr (kDt == GPTQ_F16) return f16_bits_to_f32(w >> 16);
-  else return __uint_as_float(w & 0xFFFF0000u);
-}
-
-// 8 elements from any address.
-__device__ __forceinline__ u32x4 load8(const uint16_t* p) {
-  u32x4 w;
-  __builtin_memcpy(&w, __builtin_assume_aligned(p, 2), 16);
-  return w;
-}
-
-// Elements k .. k + 7 of a row of n elements, zero behind its end.
-__device__ __forceinline__ u32x4 load8_end(const uint16_t* row, int k, int n) {
-  if (k + 8 <= n) return load8(row + k);
-  u32x4 w = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (k + i < n) w[i / 2] |= (uint32_t)row[k + i] << (16 * (i & 1));
-  return w;
-}
-
 // ---------------------------------------------------------------- few tokens
-// T[m][r] = s_a X[m] . A_a[r].
 template <int kDt>
-__global__ __launch_bounds__(256) void lora_down_few_kernel(LoraArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= a.M * a.rank) return;
-  const int64_t m = at / a.rank;
-  const int r = (int)(at - m * a.rank);
-  const int ad = __builtin_amdgcn_readfirstlane(a.adapter[m]);
-  if (ad < 0 || ad >= a.n) return;
-  const uint16_t* x = a.X + m * a.ld_x;
-  const uint16_t* f = a.A + ((int64_t)ad * a.rank + r) * a.d_in;
-  float s0 = 0.f, s1 = 0.f;
-  auto add = [&](u32x4 u, u32x4 v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s0 = fmaf(lo16<kDt>(u[i]), lo16<kDt>(v[i]), s0);
-      s1 = fmaf(hi16<kDt>(u[i]), hi16<kDt>(v[i]), s1);
-    }
-  };
-  constexpr int kU = 4;
-  int k = 0;
-  for (; k + 512 * kU <= a.d_in; k += 512 * kU) {
-    u32x4 u[kU], v[kU];
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      u[i] = load8(x + k + i * 512 + lane * 8);
-      v[i] = load8(f + k + i * 512 + lane * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < kU; ++i) add(u[i], v[i]);
-  }
-  for (; k < a.d_in; k += 512) add(load8_end(x, k + lane * 8, a.d_in), load8_end(f, k + lane * 8, a.d_in));
-  const float s = wave_reduce(s0 + s1, [](float p, float q) { return p + q; });
-  if (lane == 0) a.T[m * a.rp + r] = (a.scale ? a.scale[ad] : 1.f) * s;
+__global__ __launch_bounds__(256) void lora_down_few_kernel(LoraFew a) {
+  lora_down_one<kDt>(a, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6));
 }
 
 // Y[m][n] = base[m][n] + T[m] . B_a[n]: a wave takes 64 columns, kL lanes each
@@ -484,7 +424,8 @@ static void lora_up(const LoraArgs& a, hipStream_t st) {
 template <int kDt>
 static void lora_launch(const LoraArgs& a, int32_t y_dtype, hipStream_t st) {
   if (a.M <= kLoraFew) {
-    hipLaunchKernelGGL(lora_down_few_kernel<kDt>, dim3((unsigned)cdiv(a.M * a.rank, 4)), dim3(256), 0, st, a);
+    const LoraFew f{a.X, a.A, a.B, a.scale, a.adapter, a.T, a.ld_x, a.M, a.d_out, a.d_in, a.rank, a.n, a.rp};
+    hipLaunchKernelGGL(lora_down_few_kernel<kDt>, dim3((unsigned)cdiv(a.M * a.rank, 4)), dim3(256), 0, st, f);
     if (y_dtype == GPTQ_F32) lora_up_few<kDt, GPTQ_F32>(a, st);
     else lora_up_few<kDt, kDt>(a, st);
     return;
@@ -567,9 +508,9 @@ extern "C" gptq_status gptq_w4a16_lora_matmul(const void* X, int32_t x_dtype, in
   if (workspace != nullptr && ws_bytes < w4a16_lora_workspace_bytes(M, d_in, d_out, rank)) return GPTQ_ENOMEM;
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(workspace) % 256 == 0);
   const size_t w4 = align_up(w4a16_workspace_bytes(M, d_in, d_out), 256);
-  const gptq_status s = gptq_w4a16_matmul(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, perm, d_out, group_size,
-                                          Y, ld_y, workspace, ws_bytes, stream);
-  if (s != GPTQ_OK) return s;
-  return gptq_lora_add(X, x_dtype, M, d_in, ld_x, A, B, n_adapters, rank, scale, adapter, Y, ld_y, Y, GPTQ_F32, d_out,
-                       ld_y, static_cast<char*>(workspace) + w4, ws_bytes - w4, stream);
+  const LoraFew f{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scale,
+                  adapter, reinterpret_cast<float*>(static_cast<char*>(workspace) + w4), ld_x, M, d_out, (int)d_in, rank,
+                  (int)n_adapters, (int)(cdiv(rank, 8) * 8)};
+  return w4a16_run(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, perm, d_out, group_size, Y, ld_y, workspace,
+                   ws_bytes, &f, static_cast<hipStream_t>(stream));
 }

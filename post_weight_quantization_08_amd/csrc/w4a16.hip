@@ -22,7 +22,7 @@
 // order too: every group is then a run of consecutive chunks.
 #include <mutex>
 
-#include "common.h"
+#include "lora.h"
 
 namespace gq {
 
@@ -37,6 +37,8 @@ struct W4Args {
   float* Y;                // [M][ld_y]
   int64_t d_out, ld_y;
   int K, ng, gch, M, Mp, nchunks;
+  int parts;               // waves the chunks are (or count as being) split over
+  LoraFew lora;            // adapters; kernels with kLora only
 };
 
 // Order of the 8 channels of a staged 8-channel unit: position i holds
@@ -53,14 +55,23 @@ __device__ __forceinline__ float act_f32(uint16_t v) {
 // Xs[m][k] = X[m][col(k')] with k' the unit-swizzled channel, col = perm or
 // identity; rows m >= M are zero.  xsum[c][m] = sum of the chunk's 128
 // staged values (fp32, fixed order).
-template <int kDt>
+// One workgroup per chunk and 16 tokens; with kLora the workgroups after those
+// make the adapters' first product, a wave per (token, rank).
+template <int kDt, bool kLora>
 __global__ __launch_bounds__(256) void w4_stage_kernel(const uint16_t* __restrict__ X, int64_t ld_x, int M, int Mp,
                                                        int K, const int32_t* __restrict__ perm,
-                                                       uint16_t* __restrict__ Xs, float* __restrict__ xsum) {
-  const int c = blockIdx.x;
+                                                       uint16_t* __restrict__ Xs, float* __restrict__ xsum,
+                                                       LoraFew lora) {
+  const int staging = K / kW4Chunk * (Mp / 16);
+  if (kLora && (int)blockIdx.x >= staging) {
+    lora_down_one<kDt>(lora, (int64_t)(blockIdx.x - staging) * 4 + (threadIdx.x >> 6));
+    return;
+  }
+  const int c = blockIdx.x % (K / kW4Chunk);
   const int e = threadIdx.x & 15;
   const int k0 = c * kW4Chunk + e * 8;
-  for (int m = threadIdx.x >> 4; m < Mp; m += 16) {
+  {
+    const int m = blockIdx.x / (K / kW4Chunk) * 16 + (threadIdx.x >> 4);
     uint32_t h[4] = {0u, 0u, 0u, 0u};
     float s = 0.0f;
 #pragma unroll
@@ -153,7 +164,9 @@ __host__ __device__ inline int w4_lds_total(int ng, int M, int K, int nchunks, b
 // sums into LDS once and reads each chunk's operands from there, which frees
 // the registers that would hold mostly-zero activation tiles for a deeper
 // stream of codes.
-template <int kDt, int kMT, int kU, int kW, bool kLX>
+// kLora: the adapters' second product joins the sums before they are stored,
+// a thread per (token, row) at a time.
+template <int kDt, int kMT, int kU, int kW, bool kLX, bool kLora>
 __global__ __launch_bounds__(64 * kW) void w4_main_kernel(W4Args a) {
   static_assert(!kLX || kMT == 1, "activations in LDS only for a single token tile");
   const int lane = threadIdx.x & 63;
@@ -277,7 +290,7 @@ __global__ __launch_bounds__(64 * kW) void w4_main_kernel(W4Args a) {
   }
 
   const bool live = row < a.d_out;
-  if constexpr (kW == 1) {
+  if constexpr (kW == 1 && !kLora) {
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -302,11 +315,225 @@ __global__ __launch_bounds__(64 * kW) void w4_main_kernel(W4Args a) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] += o[r];
         }
+        if constexpr (kLora) {
+          red[0][mt][lane] = v;
+          continue;
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int tok = mt * 16 + 4 * q + r;
           if (live && tok < a.M) a.Y[(size_t)tok * a.ld_y + row] = v[r];
         }
+      }
+    }
+    if constexpr (kLora) {
+      __syncthreads();
+      for (int p = threadIdx.x; p < a.M * 16; p += 64 * kW) {
+        const int tok = p >> 4, rr = p & 15;
+        const int64_t n = (int64_t)blockIdx.x * 16 + rr;
+        if (n >= a.d_out) continue;
+        float y = red[0][tok >> 4][(tok & 15) / 4 * 16 + rr][tok & 3];
+        const int ad = a.lora.adapter[tok];
+        if (ad >= 0 && ad < a.lora.n) y += lora_up_one<kDt>(a.lora, ad, tok, n);
+        a.Y[(size_t)tok * a.ld_y + n] = y;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many tokens, many rows
+// For more than 16 tokens and enough rows: four waves of kRT x 16 rows each
+// walk all chunks together, and the chunk's activations come through LDS once
+// for the workgroup (the kernel above reads them for every 16 rows, which for
+// 48 tokens is ten times the codes' traffic).  Chunks arrive through a ring of
+// kRing stages, activations by direct loads into LDS, codes in registers, all
+// kRing - 1 chunks ahead, so that one wait per chunk covers both.  The sums are
+// the ones above bit for bit: the same products in the same order, the chunks
+// of each of the kernel's waves summed apart and added up in the waves' order.
+// A token's 256-byte row of a stage keeps its 16-byte unit u at slot u ^ (token
+// % 16), so that the 16 tokens of a fragment read lie in 16 different slots.
+constexpr int kW4Ring = 6;
+
+// bytes of a row's scales and zeros in LDS
+__host__ __device__ constexpr int w4_wide_pitch(int ng) { return (3 * ng + 3) / 4 * 4 + 4; }
+constexpr int kW4WideParams = 40960;    // LDS bytes for them
+
+// 64 lanes' 16 (4) bytes each, one after the other from `to` on.
+__device__ __forceinline__ void lds_load16(const void* from, char* to) {
+  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+}
+
+template <int kDt, int kMT, int kRT, bool kLora>
+__global__ __launch_bounds__(256, 1) void w4_wide_kernel(W4Args a) {
+  constexpr int kStage = kMT * 16 * 256;
+  constexpr int kOps = kRT + kMT + (kDt == GPTQ_BF16 ? 1 : 0);   // memory operations of a wave per chunk
+  constexpr int kFly = (kW4Ring - 2) * kOps;
+  static_assert(kFly < 64, "counted in six bits");
+  constexpr int kWait = (kFly & 0xF) | ((kFly >> 4) << 14) | (7 << 4) | (0xF << 8);
+  // one array per stage, so the compiler sees which one a read touches
+  __shared__ __attribute__((aligned(1024))) char x0[kStage], x1[kStage], x2[kStage], x3[kStage], x4[kStage], x5[kStage];
+  __shared__ __attribute__((aligned(1024))) float s0[4][64], s1[4][64], s2[4][64], s3[4][64], s4[4][64], s5[4][64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t w4_lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, q = lane >> 4;
+  const int64_t r0 = (int64_t)blockIdx.x * (64 * kRT) + wave * (16 * kRT);
+  const u32x4* wrow[kRT];
+#pragma unroll
+  for (int t = 0; t < kRT; ++t) {
+    const int64_t row = r0 + t * 16 + c16;
+    wrow[t] = a.qw + (row < a.d_out ? row : a.d_out - 1) * (a.K / 32) + q;
+  }
+  u32x4 wq[kW4Ring][kRT];
+  // this lane's part of a stage: token 4 p + lane / 16 of the wave's, slot lane % 16
+  const u32x4* xsrc[kMT];
+#pragma unroll
+  for (int p = 0; p < kMT; ++p) {
+    const int m = wave * 4 * kMT + p * 4 + (lane >> 4);
+    xsrc[p] = a.Xs + (size_t)m * (a.K / 8) + ((lane & 15) ^ (m & 15));
+  }
+  auto fetch = [&](int c, u32x4 (&w)[kRT], char* xr, float (*sr)[64]) {
+    const int cc = c < a.nchunks ? c : a.nchunks - 1;   // clamped: the same operations every chunk
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) w[t] = wrow[t][(size_t)cc * 4];
+#pragma unroll
+    for (int p = 0; p < kMT; ++p)
+      lds_load16(xsrc[p] + (size_t)cc * 16, xr + (wave * 4 * kMT + p * 4) * 256);
+    if constexpr (kDt == GPTQ_BF16) lds_load4(a.xsum + (size_t)cc * a.Mp + (lane < a.Mp ? lane : 0), sr[wave]);
+  };
+  // the rows' scales and zeros, rows padded apart for the banks
+  const int pitch = w4_wide_pitch(a.ng);
+  for (int e = threadIdx.x; e < 64 * kRT * a.ng; e += 256) {
+    const int rr = e / a.ng, g = e - rr * a.ng;
+    const int64_t row = (int64_t)blockIdx.x * (64 * kRT) + rr;
+    const size_t src = (size_t)(row < a.d_out ? row : a.d_out - 1) * a.ng + g;
+    uint8_t* p = w4_lds + rr * pitch;
+    *reinterpret_cast<uint16_t*>(p + 2 * g) = a.scales[src];
+    p[2 * a.ng + g] = a.zeros[src];
+  }
+  __syncthreads();
+  uint32_t magic_v = kDt == GPTQ_F16 ? 0x64006400u : 0x43004300u;
+  uint32_t mask_s = 0x000F000Fu;
+  asm volatile("" : "+v"(magic_v));
+  asm volatile("" : "+s"(mask_s));
+
+  f32x4 sum[kRT][kMT], tot[kRT][kMT];
+#pragma unroll
+  for (int t = 0; t < kRT; ++t)
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) sum[t][mt] = tot[t][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int part = 0, part_end = a.nchunks / a.parts;
+  auto close_part = [&]() {
+#pragma unroll
+    for (int t = 0; t < kRT; ++t)
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sum[t][mt][r] += tot[t][mt][r];
+          tot[t][mt][r] = 0.f;
+        }
+  };
+  auto multiply = [&](int c, const u32x4 (&w)[kRT], const char* xr, const float (*sr)[64]) {
+    if (c == part_end) {
+      close_part();
+      ++part;
+      part_end = a.nchunks * (part + 1) / a.parts;
+    }
+    const int gi = c / a.gch;
+    f32x4 acc[kRT][kMT];
+#pragma unroll
+    for (int t = 0; t < kRT; ++t)
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) acc[t][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float sc[kRT];
+    uint32_t zb[kRT];
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      const uint8_t* p = w4_lds + (wave * 16 * kRT + t * 16 + c16) * pitch;
+      sc[t] = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p + 2 * gi));
+      zb[t] = p[2 * a.ng + gi];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4 x[kMT];
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+        x[mt] = *reinterpret_cast<const u32x4*>(xr + (mt * 16 + c16) * 256 + (((q * 4 + i) ^ c16) * 16));
+#pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        const u32x4 b = w4_operand<kDt>(w[t][i], (0xE400u | zb[t]) * 0x00010001u, mask_s, magic_v);
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) acc[t][mt] = w4_mfma<kDt>(x[mt], b, acc[t][mt]);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      f32x4 xs = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (kDt == GPTQ_BF16) xs = *reinterpret_cast<const f32x4*>(&sr[wave][mt * 16 + 4 * q]);
+#pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        if constexpr (kDt == GPTQ_BF16) {
+          const float zf = -(128.0f + (float)zb[t]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[t][mt][r] = fmaf(zf, xs[r], acc[t][mt][r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tot[t][mt][r] = fmaf(sc[t], acc[t][mt][r], tot[t][mt][r]);
+      }
+    }
+  };
+  fetch(0, wq[0], x0, s0);
+  fetch(1, wq[1], x1, s1);
+  fetch(2, wq[2], x2, s2);
+  fetch(3, wq[3], x3, s3);
+  fetch(4, wq[4], x4, s4);
+#define GQ_W4_STAGE(u, X, S, PREV, XP, SP)                                   \
+  {                                                                          \
+    __builtin_amdgcn_s_waitcnt(kWait);                                       \
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");          \
+    fetch(c + (u) + 5, wq[PREV], XP, SP);                                    \
+    if (c + (u) < a.nchunks) multiply(c + (u), wq[u], X, S);                 \
+  }
+  for (int c = 0; c < a.nchunks; c += kW4Ring) {
+    GQ_W4_STAGE(0, x0, s0, 5, x5, s5);
+    GQ_W4_STAGE(1, x1, s1, 0, x0, s0);
+    GQ_W4_STAGE(2, x2, s2, 1, x1, s1);
+    GQ_W4_STAGE(3, x3, s3, 2, x2, s2);
+    GQ_W4_STAGE(4, x4, s4, 3, x3, s3);
+    GQ_W4_STAGE(5, x5, s5, 4, x4, s4);
+  }
+#undef GQ_W4_STAGE
+  __builtin_amdgcn_s_waitcnt(0);   // the direct loads have landed before LDS is given back
+  close_part();
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) {
+    int ad[4] = {-1, -1, -1, -1};
+    if constexpr (kLora) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tok = mt * 16 + 4 * q + r;
+        if (tok < a.M) ad[r] = a.lora.adapter[tok];
+        if (ad[r] >= a.lora.n) ad[r] = -1;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      const int64_t row = r0 + t * 16 + c16;
+      if (row >= a.d_out) continue;
+      f32x4 y = sum[t][mt];
+      if constexpr (kLora) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (ad[r] >= 0) y[r] += lora_up_one<kDt>(a.lora, ad[r], mt * 16 + 4 * q + r, row);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tok = mt * 16 + 4 * q + r;
+        if (tok < a.M) a.Y[(size_t)tok * a.ld_y + row] = y[r];
       }
     }
   }
@@ -342,37 +569,83 @@ static bool w4_lx(int64_t M, int64_t d_in, int ng, int nchunks, int W) {
   return M <= 4 && w4_lds_total(ng, (int)M, (int)d_in, nchunks, true, W * 64 * 16) <= 65536;
 }
 
-template <int kDt, int kMT, int kU, bool kLX>
+template <int kDt, int kMT, int kU, bool kLX, bool kLora>
 static void launch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
   const dim3 grid((unsigned)pl.nblocks);
   const size_t lds = w4_lds_total(a.ng, a.M, a.K, a.nchunks, kLX, pl.W * kMT * 64 * (int)sizeof(f32x4));
   switch (pl.W) {
-    case 1: hipLaunchKernelGGL((w4_main_kernel<kDt, kMT, kU, 1, kLX>), grid, dim3(64), lds, st, a); break;
-    case 2: hipLaunchKernelGGL((w4_main_kernel<kDt, kMT, kU, 2, kLX>), grid, dim3(128), lds, st, a); break;
-    default: hipLaunchKernelGGL((w4_main_kernel<kDt, kMT, kU, 4, kLX>), grid, dim3(256), lds, st, a); break;
+    case 1: hipLaunchKernelGGL((w4_main_kernel<kDt, kMT, kU, 1, kLX, kLora>), grid, dim3(64), lds, st, a); break;
+    case 2: hipLaunchKernelGGL((w4_main_kernel<kDt, kMT, kU, 2, kLX, kLora>), grid, dim3(128), lds, st, a); break;
+    default: hipLaunchKernelGGL((w4_main_kernel<kDt, kMT, kU, 4, kLX, kLora>), grid, dim3(256), lds, st, a); break;
   }
 }
 
-// Both entry points: arguments checked, workspace of at least pl.total bytes.
+// Row tiles per wave of the wide kernel, 0 for the other one: it needs more
+// than one token tile, and rows for most of the CUs (one workgroup each).
+static int w4_wide_tiles(int64_t M, int64_t d_out, int ng) {
+  if (M <= 16) return 0;
+  if (d_out >= 192 * 128 && 128 * w4_wide_pitch(ng) <= kW4WideParams) return 2;
+  if (d_out >= 128 * 64 && 64 * w4_wide_pitch(ng) <= kW4WideParams) return 1;
+  return 0;
+}
+
+template <int kDt, int kMT, bool kLora>
+static void launch_w4_wide(const W4Args& a, int tiles, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.d_out, 64 * tiles));
+  const size_t lds = (size_t)64 * tiles * w4_wide_pitch(a.ng);
+  if (tiles == 2) hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 2, kLora>), grid, dim3(256), lds, st, a);
+  else hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 1, kLora>), grid, dim3(256), lds, st, a);
+}
+
+template <int kDt, bool kLora>
+static void dispatch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
+  const int tiles = w4_wide_tiles(a.M, a.d_out, a.ng);
+  const int mt = pl.Mp / 16;
+  if (tiles > 0) {
+    if (a.M <= 32) launch_w4_wide<kDt, 2, kLora>(a, tiles, st);
+    else if (a.M <= 48) launch_w4_wide<kDt, 3, kLora>(a, tiles, st);
+    else launch_w4_wide<kDt, 4, kLora>(a, tiles, st);
+  } else if (w4_lx(a.M, a.K, a.ng, pl.nchunks, pl.W)) {
+    launch_w4<kDt, 1, 8, true, kLora>(a, pl, st);
+  } else if (mt == 1) {
+    launch_w4<kDt, 1, 4, false, kLora>(a, pl, st);
+  } else if (mt == 2) {
+    launch_w4<kDt, 2, 2, false, kLora>(a, pl, st);
+  } else {
+    launch_w4<kDt, 4, 1, false, kLora>(a, pl, st);
+  }
+}
+
+// Every entry point: arguments checked, workspace of at least pl.total bytes.
 static gptq_status w4a16_enqueue(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x,
                                  const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                                  const int32_t* perm, int64_t d_out, int32_t group_size, float* Y, int64_t ld_y,
-                                 const W4Plan& pl, char* ws, bool timed, hipStream_t st) {
+                                 const W4Plan& pl, char* ws, bool timed, const LoraFew* lora, hipStream_t st) {
   uint16_t* Xs = reinterpret_cast<uint16_t*>(ws + pl.off_xs);
   float* xsum = reinterpret_cast<float*>(ws + pl.off_xsum);
   const int K = (int)d_in;
+  W4Args a{};
+  if (lora != nullptr) a.lora = *lora;
   {
     TimedScope ts(timed ? kTimeW4Stage : -1, st);
     const uint16_t* Xh = static_cast<const uint16_t*>(X);
-    if (x_dtype == GPTQ_F16)
-      hipLaunchKernelGGL(w4_stage_kernel<GPTQ_F16>, dim3((unsigned)pl.nchunks), dim3(256), 0, st, Xh, ld_x, (int)M,
-                         pl.Mp, K, perm, Xs, xsum);
+    const int64_t staging = pl.nchunks * (pl.Mp / 16);
+    const dim3 grid((unsigned)(staging + (lora != nullptr ? cdiv(M * lora->rank, 4) : 0)));
+    const bool f16 = x_dtype == GPTQ_F16;
+    if (f16 && lora == nullptr)
+      hipLaunchKernelGGL((w4_stage_kernel<GPTQ_F16, false>), grid, dim3(256), 0, st, Xh, ld_x, (int)M, pl.Mp, K, perm, Xs,
+                         xsum, a.lora);
+    else if (f16)
+      hipLaunchKernelGGL((w4_stage_kernel<GPTQ_F16, true>), grid, dim3(256), 0, st, Xh, ld_x, (int)M, pl.Mp, K, perm, Xs,
+                         xsum, a.lora);
+    else if (lora == nullptr)
+      hipLaunchKernelGGL((w4_stage_kernel<GPTQ_BF16, false>), grid, dim3(256), 0, st, Xh, ld_x, (int)M, pl.Mp, K, perm,
+                         Xs, xsum, a.lora);
     else
-      hipLaunchKernelGGL(w4_stage_kernel<GPTQ_BF16>, dim3((unsigned)pl.nchunks), dim3(256), 0, st, Xh, ld_x, (int)M,
-                         pl.Mp, K, perm, Xs, xsum);
+      hipLaunchKernelGGL((w4_stage_kernel<GPTQ_BF16, true>), grid, dim3(256), 0, st, Xh, ld_x, (int)M, pl.Mp, K, perm, Xs,
+                         xsum, a.lora);
     GQ_LAUNCHED();
   }
-  W4Args a;
   a.qw = reinterpret_cast<const u32x4*>(qweight);
   a.scales = scales;
   a.zeros = zeros;
@@ -387,20 +660,15 @@ static gptq_status w4a16_enqueue(const void* X, int32_t x_dtype, int64_t M, int6
   a.M = (int)M;
   a.Mp = pl.Mp;
   a.nchunks = pl.nchunks;
+  a.parts = pl.W;
   {
     TimedScope ts(timed ? kTimeW4Main : -1, st);
-    const int mt = pl.Mp / 16;
-    const bool lx = w4_lx(M, d_in, a.ng, pl.nchunks, pl.W);
     if (x_dtype == GPTQ_F16) {
-      if (lx) launch_w4<GPTQ_F16, 1, 8, true>(a, pl, st);
-      else if (mt == 1) launch_w4<GPTQ_F16, 1, 4, false>(a, pl, st);
-      else if (mt == 2) launch_w4<GPTQ_F16, 2, 2, false>(a, pl, st);
-      else launch_w4<GPTQ_F16, 4, 1, false>(a, pl, st);
+      if (lora != nullptr) dispatch_w4<GPTQ_F16, true>(a, pl, st);
+      else dispatch_w4<GPTQ_F16, false>(a, pl, st);
     } else {
-      if (lx) launch_w4<GPTQ_BF16, 1, 8, true>(a, pl, st);
-      else if (mt == 1) launch_w4<GPTQ_BF16, 1, 4, false>(a, pl, st);
-      else if (mt == 2) launch_w4<GPTQ_BF16, 2, 2, false>(a, pl, st);
-      else launch_w4<GPTQ_BF16, 4, 1, false>(a, pl, st);
+      if (lora != nullptr) dispatch_w4<GPTQ_BF16, true>(a, pl, st);
+      else dispatch_w4<GPTQ_BF16, false>(a, pl, st);
     }
     GQ_LAUNCHED();
   }
@@ -451,6 +719,18 @@ static gptq_status scratch_address(void** out) {
   return GPTQ_OK;
 }
 
+gptq_status w4a16_run(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x, const uint8_t* qweight,
+                      const uint16_t* scales, const uint8_t* zeros, const int32_t* perm, int64_t d_out,
+                      int32_t group_size, float* Y, int64_t ld_y, void* workspace, size_t ws_bytes, const LoraFew* lora,
+                      hipStream_t st) {
+  gptq_status s = w4a16_check(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, d_out, group_size, Y, ld_y);
+  if (s != GPTQ_OK) return s;
+  const W4Plan pl = w4_plan(M, d_in, d_out);
+  if (workspace == nullptr || ws_bytes < pl.total) return GPTQ_ENOMEM;
+  return w4a16_enqueue(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, perm, d_out, group_size, Y, ld_y, pl,
+                       static_cast<char*>(workspace), true, lora, st);
+}
+
 }  // namespace gq
 
 using namespace gq;
@@ -459,12 +739,8 @@ extern "C" gptq_status gptq_w4a16_matmul(const void* X, int32_t x_dtype, int64_t
                                          const uint8_t* qweight, const uint16_t* scales, const uint8_t* zeros,
                                          const int32_t* perm, int64_t d_out, int32_t group_size, float* Y,
                                          int64_t ld_y, void* workspace, size_t ws_bytes, void* stream) {
-  gptq_status s = w4a16_check(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, d_out, group_size, Y, ld_y);
-  if (s != GPTQ_OK) return s;
-  const W4Plan pl = w4_plan(M, d_in, d_out);
-  if (workspace == nullptr || ws_bytes < pl.total) return GPTQ_ENOMEM;
-  return w4a16_enqueue(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, perm, d_out, group_size, Y, ld_y, pl,
-                       static_cast<char*>(workspace), true, static_cast<hipStream_t>(stream));
+  return w4a16_run(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, perm, d_out, group_size, Y, ld_y, workspace,
+                   ws_bytes, nullptr, static_cast<hipStream_t>(stream));
 }
 
 extern "C" gptq_status gptq_w4a16_matmul_noalloc(const void* X, int32_t x_dtype, int64_t M, int64_t d_in,
@@ -479,5 +755,5 @@ extern "C" gptq_status gptq_w4a16_matmul_noalloc(const void* X, int32_t x_dtype,
   s = scratch_address(&ws);
   if (s != GPTQ_OK) return s;
   return w4a16_enqueue(X, x_dtype, M, d_in, ld_x, qweight, scales, zeros, perm, d_out, group_size, Y, ld_y, pl,
-                       static_cast<char*>(ws), false, static_cast<hipStream_t>(stream));
+                       static_cast<char*>(ws), false, nullptr, static_cast<hipStream_t>(stream));
 }
