@@ -872,11 +872,11 @@ extern "C" gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, in
   GQ_CHECK_ARG(ld_x >= vocab && ld_x <= ((int64_t)1 << 36));
   GQ_CHECK_ARG(temperature >= 1e-4f && temperature <= 1e4f);
   GQ_CHECK_ARG(k >= 1 && (tail == 0 || tail == 1));
-  GQ_CHECK_ARG(loss || grad);
   GQ_CHECK_ARG(grad == nullptr || (ld_g >= vocab && ld_g <= ((int64_t)1 << 36)));
-  GQ_CHECK_ARG(grad == nullptr || grad != logits || ld_g == ld_x);
   if (k > kDsMaxK || vocab > ((int64_t)1 << 21)) return GPTQ_EUNSUPPORTED;
   if (n_rows == 0) return GPTQ_OK;
+  GQ_CHECK_ARG(loss || grad);
+  GQ_CHECK_ARG(grad == nullptr || grad != logits || ld_g == ld_x);
   const int es = x_dtype == GPTQ_F32 ? 4 : 2;
   GQ_CHECK_ARG(logits && top_id && top_logprob && reinterpret_cast<uintptr_t>(logits) % es == 0 &&
                reinterpret_cast<uintptr_t>(grad) % es == 0);

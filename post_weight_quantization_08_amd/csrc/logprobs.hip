@@ -547,11 +547,11 @@ extern "C" gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, 
   GQ_CHECK_ARG(ld_x >= vocab && ld_x <= ((int64_t)1 << 36));
   GQ_CHECK_ARG(temperature >= 1e-4f && temperature <= 1e4f);
   GQ_CHECK_ARG(k >= 0 && k <= vocab);
+  if (k > 128 || vocab > ((int64_t)1 << 21)) return GPTQ_EUNSUPPORTED;
+  if (n_rows == 0) return GPTQ_OK;
   GQ_CHECK_ARG(logprob == nullptr || targets != nullptr);
   GQ_CHECK_ARG(k == 0 || (top_logprob && top_id));
   GQ_CHECK_ARG(logprob || lse || entropy || k > 0);
-  if (k > 128 || vocab > ((int64_t)1 << 21)) return GPTQ_EUNSUPPORTED;
-  if (n_rows == 0) return GPTQ_OK;
   const int es = x_dtype == GPTQ_F32 ? 4 : 2;
   GQ_CHECK_ARG(logits != nullptr && reinterpret_cast<uintptr_t>(logits) % es == 0);
   const size_t need = logprobs_workspace_bytes(n_rows, vocab, k);

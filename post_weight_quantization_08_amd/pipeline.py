@@ -11,12 +11,11 @@ from typing import Dict, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD, OP_HESSIAN, OP_LOGPROBS, OP_LORA,
-               OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, dtype_code, gptq_abs_accumulate,
-               gptq_awq_apply, gptq_awq_search, gptq_distill_topk, gptq_hessian_accumulate, gptq_layer_forward,
-               gptq_lora_add, gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv,
-               gptq_quantize_layer, gptq_token_logprobs, gptq_w4a16_lora_matmul, gptq_w4a16_matmul,
-               gptq_workspace_size)
+from . import (BF16, F16, F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD, OP_HESSIAN,
+               OP_LOGPROBS, OP_LORA, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, _check, dtype_code,
+               gptq_abs_accumulate, gptq_awq_apply, gptq_awq_search, gptq_hessian_accumulate, gptq_layer_forward,
+               gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv, gptq_quantize_layer,
+               gptq_w4a16_matmul, gptq_workspace_size, lib)
 
 
 def to_device(arr: np.ndarray, dtype: str, device="cuda") -> torch.Tensor:
@@ -200,32 +199,75 @@ def layer_forward(X: torch.Tensor, Q: torch.Tensor, act: int, Y: Optional[torch.
     return Y
 
 
-def _rows(t: torch.Tensor, what: str) -> torch.Tensor:
-    if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{what}: a 2-d tensor with contiguous, disjoint rows is needed")
-    return t
+# ---------------------------------------------------------------- answers: scoring, distillation, adapters
+# The calls below are made once per token when a model is served, so they check
+# their arguments with few and cheap questions and hand plain addresses to the
+# library.
+_DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride; a single row may carry any, so its width counts."""
-    return max(t.stride(0), t.shape[1])
+def _stream_of(stream, device: int) -> int:
+    if stream is None:
+        return _raw_stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _dense(t: Optional[torch.Tensor], dtype, shape, what: str, like: torch.Tensor) -> Optional[torch.Tensor]:
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
-                          or t.device != like.device):
-        raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device} is needed")
-    return t
+def _rows(t: torch.Tensor, what: str):
+    """(rows, columns, row stride, device index) of a 2-d GPU tensor with contiguous, disjoint rows."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what}: a GPU tensor is needed")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: a 2-d tensor is needed")
+    n, w = t.shape
+    ld, one = t.stride()
+    if one != 1 and w > 1 or ld < w and n > 1:
+        raise ValueError(f"{what}: contiguous, disjoint rows are needed")
+    return n, w, ld if ld > w else w, device
+
+
+def _dense(t: torch.Tensor, dtype, shape, what: str, device: int) -> int:
+    """Address of a contiguous tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {device} is needed")
+    return t.data_ptr()
+
+
+def _workspace(ws: torch.Tensor, device: int):
+    if not ws.is_contiguous() or ws.get_device() != device:
+        raise ValueError(f"ws: a contiguous tensor on GPU {device} is needed")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+class Buffers(dict):
+    """Output tensors of a call, by name, that were checked when they were made: `key` says for which sizes,
+    `addresses` where they are.  Setting an entry makes them ordinary, to be checked in every call."""
+
+    def __init__(self, key, tensors: Dict[str, torch.Tensor]):
+        super().__init__(tensors)
+        self.key, self.addresses = key, [t.data_ptr() for t in tensors.values()]
+
+    def _changed(self, *args, **kwargs):
+        raise TypeError("use out[name] = tensor")
+
+    def __setitem__(self, name, value):
+        self.key = None
+        super().__setitem__(name, value)
+
+    __delitem__ = pop = popitem = clear = update = setdefault = __ior__ = _changed
 
 
 def token_logprobs_buffers(logits: torch.Tensor, k: int = 0):
-    """(out, ws) of a token_logprobs call with these sizes, to be kept from call to call."""
+    """(out, ws) of token_logprobs calls with these sizes, to be kept from call to call."""
     n, v = logits.shape
     dev = logits.device
     out = {name: torch.empty(n, dtype=torch.float32, device=dev) for name in ("logprob", "lse", "entropy")}
     out["top_logprob"] = torch.empty(n, k, dtype=torch.float32, device=dev)
     out["top_id"] = torch.empty(n, k, dtype=torch.int32, device=dev)
-    return out, _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), dev)
+    return (Buffers(("logprobs", n, k, logits.get_device()), out),
+            _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), dev))
 
 
 def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, k: int = 0, temperature: float = 1.0,
@@ -234,31 +276,35 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     """Log probability of targets[i] (int32; outside the vocabulary: not scored, 0), log-sum-exp, entropy and the k
     best alternatives (log probabilities and ids, ties to the lower id) of every row of logits at a temperature.
     Without targets the logprob entry of the result is not written."""
-    n, v = _rows(logits, "logits").shape
-    _dense(targets, torch.int32, (n,), "targets", logits)
+    n, v, ld, device = _rows(logits, "logits")
+    target = _dense(targets, torch.int32, (n,), "targets", device) if targets is not None else None
     if out is None:
         with _on(stream):
             out = token_logprobs_buffers(logits, k)[0]
-    for name in ("logprob", "lse", "entropy"):
-        _dense(out[name], torch.float32, (n,), name, logits)
-    _dense(out["top_logprob"], torch.float32, (n, k), "top_logprob", logits)
-    _dense(out["top_id"], torch.int32, (n, k), "top_id", logits)
+    if type(out) is Buffers and out.key == ("logprobs", n, k, device):
+        lp, lse, ent, top_lp, top_id = out.addresses
+    else:
+        lp, lse, ent = (_dense(out[name], torch.float32, (n,), name, device) for name in ("logprob", "lse", "entropy"))
+        top_lp = _dense(out["top_logprob"], torch.float32, (n, k), "top_logprob", device)
+        top_id = _dense(out["top_id"], torch.int32, (n, k), "top_id", device)
     if ws is None:
         with _on(stream):
             ws = _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), logits.device)
-    gptq_token_logprobs(logits, dtype_code(logits.dtype), n, v, _ld(logits), targets, temperature, k,
-                        out["logprob"] if targets is not None else None, out["lse"], out["entropy"],
-                        out["top_logprob"], out["top_id"], ws, ws.numel(), stream)
+    at, nbytes = _workspace(ws, device)
+    _check(lib.gptq_token_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), n, v, ld, target, temperature, k,
+                                   lp if target is not None else None, lse, ent, top_lp, top_id, at, nbytes,
+                                   _stream_of(stream, device)), "gptq_token_logprobs")
     return out
 
 
 def distill_topk_buffers(logits: torch.Tensor, k: int, want_grad: bool = True):
-    """(out, ws) of a distill_topk call with these sizes, to be kept from call to call."""
+    """(out, ws) of distill_topk calls with these sizes, to be kept from call to call."""
     n, v = logits.shape
     out = {"loss": torch.empty(n, dtype=torch.float32, device=logits.device)}
     if want_grad:
         out["grad"] = torch.empty(n, v, dtype=logits.dtype, device=logits.device)
-    return out, _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device)
+    return (Buffers(("distill", n, v if want_grad else 0, logits.dtype, logits.get_device()), out),
+            _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device))
 
 
 def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.Tensor, temperature: float = 1.0,
@@ -268,46 +314,59 @@ def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     """Loss of every row of the student's logits against the teacher's top list (int32 ids, fp32 log probabilities
     at the same temperature) and, with want_grad, the gradient of sum(weight * loss) in the logits' type.  out may
     hold the logits themselves as "grad": the gradient then replaces them."""
-    n, v = _rows(logits, "logits").shape
+    n, v, ld, device = _rows(logits, "logits")
+    dtype = logits.dtype
     k = top_id.shape[-1]
-    _dense(top_id, torch.int32, (n, k), "top_id", logits)
-    _dense(top_logprob, torch.float32, (n, k), "top_logprob", logits)
-    _dense(weight, torch.float32, (n,), "weight", logits)
+    ids = _dense(top_id, torch.int32, (n, k), "top_id", device)
+    lps = _dense(top_logprob, torch.float32, (n, k), "top_logprob", device)
+    weights = _dense(weight, torch.float32, (n,), "weight", device) if weight is not None else None
     if out is None:
         with _on(stream):
             out = distill_topk_buffers(logits, k, want_grad)[0]
-    _dense(out["loss"], torch.float32, (n,), "loss", logits)
-    grad = None
-    if want_grad:
-        grad = _rows(out["grad"], "grad")
-        if grad.dtype != logits.dtype or grad.shape != logits.shape or grad.device != logits.device:
-            raise ValueError("grad: the logits' type, shape and device are needed")
+    ld_g, grad = v, None
+    if type(out) is Buffers and out.key == ("distill", n, v if want_grad else 0, dtype, device):
+        loss = out.addresses[0]
+        if want_grad:
+            grad = out.addresses[1]
+    else:
+        loss = _dense(out["loss"], torch.float32, (n,), "loss", device)
+        if want_grad:
+            g = out["grad"]
+            gn, gv, ld_g, g_device = _rows(g, "grad")
+            if g.dtype is not dtype or (gn, gv, g_device) != (n, v, device):
+                raise ValueError("grad: the logits' type, shape and device are needed")
+            grad = g.data_ptr()
     if ws is None:
         with _on(stream):
             ws = _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device)
-    gptq_distill_topk(logits, dtype_code(logits.dtype), n, v, _ld(logits), top_id, top_logprob, k, temperature, tail,
-                      weight, out["loss"], grad, _ld(grad) if grad is not None else v, ws, ws.numel(), stream)
+    at, nbytes = _workspace(ws, device)
+    _check(lib.gptq_distill_topk(logits.data_ptr(), _DTYPE.get(dtype, -1), n, v, ld, ids, lps, k, temperature, bool(tail),
+                                 weights, loss, grad, ld_g, at, nbytes, _stream_of(stream, device)),
+           "gptq_distill_topk")
     return out
 
 
-def _adapters(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, scale):
-    n, r, d_in = A.shape
-    M = _rows(X, "X").shape[0]
-    _dense(A, X.dtype, (n, r, X.shape[1]), "A", X)
-    _dense(B, X.dtype, (n, B.shape[1], r), "B", X)
-    _dense(adapter, torch.int32, (M,), "adapter", X)
-    _dense(scale, torch.float32, (n,), "scale", X)
-    return M, n, r, d_in, B.shape[1]
+def _adapters(A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, scale, dtype, M: int, d_in: int, device: int):
+    """(adapters, rank, d_out, address of A, B, adapter, scale)."""
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A, B: (adapters, rank, d_in) and (adapters, d_out, rank) are needed")
+    n, r, _ = A.shape
+    d_out = B.shape[1]
+    return (n, r, d_out, _dense(A, dtype, (n, r, d_in), "A", device), _dense(B, dtype, (n, d_out, r), "B", device),
+            _dense(adapter, torch.int32, (M,), "adapter", device),
+            _dense(scale, torch.float32, (n,), "scale", device) if scale is not None else None)
 
 
-def _rows_like(t: torch.Tensor, dtype, shape, what: str, like: torch.Tensor) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != like.device:
-        raise ValueError(f"{what}: a {dtype} tensor of shape {tuple(shape)} on {like.device} is needed")
-    return _rows(t, what)
+def _out_rows(t: torch.Tensor, dtype, M: int, d_out: int, what: str, device: int):
+    """(address, row stride) of an (M, d_out) tensor."""
+    m, w, ld, on = _rows(t, what)
+    if t.dtype is not dtype or (m, w, on) != (M, d_out, device):
+        raise ValueError(f"{what}: a {dtype} tensor of shape {(M, d_out)} on GPU {device} is needed")
+    return t.data_ptr(), ld
 
 
 def lora_buffers(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, y_dtype=torch.float32):
-    """(Y, ws) of a lora_add call with these sizes, to be kept from call to call."""
+    """(Y, ws) of lora_add calls with these sizes, to be kept from call to call."""
     M, d_in = X.shape
     d_out, r = B.shape[1], B.shape[2]
     return (torch.empty(M, d_out, dtype=y_dtype, device=X.device),
@@ -319,24 +378,26 @@ def lora_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.T
              Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Y[m] = base[m] + scale[a] (X[m] A_a^T) B_a^T, a = adapter[m] (int32; outside the adapters: none).  A is
     (n, rank, d_in), B (n, d_out, rank) in X's type; Y fp32 or X's type, base in Y's type; Y may be base itself."""
-    M, n, r, d_in, d_out = _adapters(X, A, B, adapter, scale)
+    M, d_in, ld_x, device = _rows(X, "X")
+    dtype = X.dtype
+    n, r, d_out, pa, pb, pad, ps = _adapters(A, B, adapter, scale, dtype, M, d_in, device)
     if Y is None:
         with _on(stream):
             Y = torch.empty(M, d_out, dtype=base.dtype if base is not None else torch.float32, device=X.device)
-    _rows_like(Y, Y.dtype, (M, d_out), "Y", X)
-    if base is not None:
-        _rows_like(base, Y.dtype, (M, d_out), "base", X)
+    py, ld_y = _out_rows(Y, Y.dtype, M, d_out, "Y", device)
+    p0, ld_b = _out_rows(base, Y.dtype, M, d_out, "base", device) if base is not None else (None, d_out)
     if ws is None:
         with _on(stream):
             ws = _ws(gptq_workspace_size(OP_LORA, None, d_out, d_in, M, r), X.device)
-    gptq_lora_add(X, dtype_code(X.dtype), M, d_in, _ld(X), A, B, n, r, scale, adapter, base,
-                  _ld(base) if base is not None else d_out, Y, dtype_code(Y.dtype), d_out, _ld(Y), ws, ws.numel(),
-                  stream)
+    at, nbytes = _workspace(ws, device)
+    _check(lib.gptq_lora_add(X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in, ld_x, pa, pb, n, r, ps, pad, p0, ld_b, py,
+                             _DTYPE.get(Y.dtype, -1), d_out, ld_y, at, nbytes, _stream_of(stream, device)),
+           "gptq_lora_add")
     return Y
 
 
 def w4a16_lora_buffers(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor):
-    """(Y, ws) of a w4a16_lora_matmul call with these sizes, to be kept from call to call."""
+    """(Y, ws) of w4a16_lora_matmul calls with these sizes, to be kept from call to call."""
     M, d_in = X.shape
     d_out, r = B.shape[1], B.shape[2]
     return (torch.empty(M, d_out, dtype=torch.float32, device=X.device),
@@ -349,18 +410,27 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
                       Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
     """w4a16_matmul (up to 64 tokens) plus every token's adapter, as lora_add adds it."""
-    M, n, r, d_in, d_out = _adapters(X, A, B, adapter, scale)
-    if qweight.shape[0] != d_out or qweight.shape[1] * 2 != d_in:
-        raise ValueError("qweight: its rows and columns must match B and X")
+    M, d_in, ld_x, device = _rows(X, "X")
+    dtype = X.dtype
+    n, r, d_out, pa, pb, pad, ps = _adapters(A, B, adapter, scale, dtype, M, d_in, device)
+    ng = d_in // group_size
+    pq = _dense(qweight, torch.uint8, (d_out, d_in // 2), "qweight", device)
+    if scales.dtype is not torch.int16 and scales.dtype is not torch.float16:
+        raise ValueError("scales: fp16, or their bits as int16, are needed")
+    psc = _dense(scales, scales.dtype, (d_out, ng), "scales", device)
+    pz = _dense(zeros, torch.uint8, (d_out, ng), "zeros", device)
+    pp = _dense(perm, torch.int32, (d_in,), "perm", device) if perm is not None else None
     if Y is None:
         with _on(stream):
             Y = torch.empty(M, d_out, dtype=torch.float32, device=X.device)
-    _rows_like(Y, torch.float32, (M, d_out), "Y", X)
+    py, ld_y = _out_rows(Y, torch.float32, M, d_out, "Y", device)
     if ws is None:
         with _on(stream):
             ws = _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, M, r), X.device)
-    gptq_w4a16_lora_matmul(X, dtype_code(X.dtype), M, d_in, _ld(X), qweight, scales, zeros, perm, d_out, group_size,
-                           A, B, n, r, scale, adapter, Y, _ld(Y), ws, ws.numel(), stream)
+    at, nbytes = _workspace(ws, device)
+    _check(lib.gptq_w4a16_lora_matmul(X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in, ld_x, pq, psc, pz, pp, d_out,
+                                      group_size, pa, pb, n, r, ps, pad, py, ld_y, at, nbytes,
+                                      _stream_of(stream, device)), "gptq_w4a16_lora_matmul")
     return Y
 
 
