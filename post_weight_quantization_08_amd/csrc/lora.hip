@@ -33,7 +33,6 @@ size_t w4a16_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out);
 
 constexpr int kLoraFew = 64;        // tokens up to which every one is taken by itself
 constexpr int kLoraTile = 32;       // tokens of an MFMA tile
-constexpr int kLoraCols = 512;      // output columns of a workgroup
 constexpr int kLoraMaxRank = 128;
 
 struct LoraArgs {
@@ -49,6 +48,7 @@ struct LoraArgs {
   int d_in, rank, n;
   int rp;                  // rank padded to 8
   int splits, k_split;     // parts of the first product's sum, and their length
+  int cols;                // output columns of a workgroup
 };
 
 // ---------------------------------------------------------------- few tokens
@@ -151,32 +151,50 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
     f32x4 acc[kR][2];
 #pragma unroll
     for (int t = 0; t < kR; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k = k0 + wave * 64; k < k1; k += 256) {
-      u32x4 xv[2][2], av[2][kR];
+    // a step's operands are asked for while the step before is multiplied
+    struct Step {
+      u32x4 x[2][2], f[2][kR];
+    };
+    auto read = [&](int k, Step& p) {
       if (k + 64 <= k1) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) xv[j][t] = load8(x[t] + k + 32 * j + 8 * q);
+          for (int t = 0; t < 2; ++t) p.x[j][t] = load8(x[t] + k + 32 * j + 8 * q);
 #pragma unroll
-          for (int t = 0; t < kR; ++t) av[j][t] = load8(f[t] + k + 32 * j + 8 * q);
+          for (int t = 0; t < kR; ++t) p.f[j][t] = load8(f[t] + k + 32 * j + 8 * q);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) xv[j][t] = load8_end(x[t], k + 32 * j + 8 * q, k1);
+          for (int t = 0; t < 2; ++t) p.x[j][t] = load8_end(x[t], k + 32 * j + 8 * q, k1);
 #pragma unroll
-          for (int t = 0; t < kR; ++t) av[j][t] = load8_end(f[t], k + 32 * j + 8 * q, k1);
+          for (int t = 0; t < kR; ++t) p.f[j][t] = load8_end(f[t], k + 32 * j + 8 * q, k1);
         }
       }
+    };
+    auto multiply = [&](const Step& p) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int t = 0; t < kR; ++t) {
-          acc[t][0] = lora_mfma<kDt>(av[j][t], xv[j][0], acc[t][0]);
-          acc[t][1] = lora_mfma<kDt>(av[j][t], xv[j][1], acc[t][1]);
+          acc[t][0] = lora_mfma<kDt>(p.f[j][t], p.x[j][0], acc[t][0]);
+          acc[t][1] = lora_mfma<kDt>(p.f[j][t], p.x[j][1], acc[t][1]);
         }
+    };
+    const int first = k0 + wave * 64;
+    if (first < k1) {
+      Step even, odd;
+      read(first, even);
+      for (int k = first; k < k1; k += 512) {
+        if (k + 256 < k1) read(k + 256, odd);
+        multiply(even);
+        if (k + 256 < k1) {
+          if (k + 512 < k1) read(k + 512, even);
+          multiply(odd);
+        }
+      }
     }
 #pragma unroll
     for (int t = 0; t < kR; ++t)
@@ -224,41 +242,60 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4& hi, u32x4
   }
 }
 
-// 32 tokens by kLoraCols columns; kS steps of 32 ranks.
+// 32 tokens by `cols` columns (a multiple of 128); kS steps of 32 ranks.
 template <int kDt, int kY, int kS>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
+  constexpr int kPitch = kS * 32 + 4;
+  __shared__ __align__(16) float tsum[kLoraTile][kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
   const int64_t m0 = (int64_t)blockIdx.x * kLoraTile;
   const int mine = lora_adapter(a, m0 + (lane & 31));
+  // T's parts added up, scaled: 8 threads per token, 4 ranks at a time
+  {
+    const int tok = threadIdx.x >> 3;
+    const int ad = __shfl(mine, tok & 31);
+    const float sc = ad >= 0 && a.scale ? a.scale[ad] : 1.f;
+    for (int r = (threadIdx.x & 7) * 4; r < kS * 32; r += 32) {
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      if (ad >= 0 && r < a.rp) {
+        const float* src = a.T + (m0 + tok) * a.rp + r;
+        const int64_t step = a.M * a.rp;
+        int p = 0;
+        for (; p + 8 <= a.splits; p += 8) {
+          f32x4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const f32x4*>(src + (p + i) * step);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s += v[i];
+        }
+        for (; p < a.splits; ++p) s += *reinterpret_cast<const f32x4*>(src + p * step);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] *= sc;
+      *reinterpret_cast<f32x4*>(&tsum[tok][r]) = s;
+    }
+  }
+  __syncthreads();
   int own[2];                              // adapters of this lane's two tokens
   float grow[2];                           // 2^e that T's terms were divided by
   u32x4 hi[2][kS], lo[2][kS];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     own[t] = __shfl(mine, t * 16 + c16);
-    const int64_t m = m0 + t * 16 + c16;
-    const float sc = own[t] >= 0 && a.scale ? a.scale[own[t]] : 1.f;
     float v[kS][8];
     float big = 0.f;
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-      const int k = s * 32 + 8 * q;
+    for (int s = 0; s < kS; ++s)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
-      if (own[t] >= 0 && k < a.rp) {
-        for (int p = 0; p < a.splits; ++p) {
-          const float* src = a.T + ((int64_t)p * a.M + m) * a.rp + k;
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 u = *reinterpret_cast<const f32x4*>(&tsum[t * 16 + c16][s * 32 + 8 * q + 4 * h]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[s][i] += src[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[s][i] *= sc;
-          big = fmaxf(big, fabsf(v[s][i]));
+        for (int i = 0; i < 4; ++i) {
+          v[s][4 * h + i] = u[i];
+          big = fmaxf(big, fabsf(u[i]));
         }
       }
-    }
     grow[t] = 1.f;
     if constexpr (kDt == GPTQ_F16) {
       big = fmaxf(big, __shfl_xor(big, 16));
@@ -276,113 +313,153 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll
     for (int s = 0; s < kS; ++s) lora_split<kDt>(v[s], hi[t][s], lo[t][s]);
   }
-  const int64_t n_first = (int64_t)blockIdx.y * kLoraCols;
-  const int64_t n_end = n_first + kLoraCols < a.d_out ? n_first + kLoraCols : a.d_out;
-  for (int64_t n = n_first + wave * 32; n < n_end; n += 128) {
-    const int64_t col = n + 8 * q;         // this lane's eight columns
-    const bool whole = col + 8 <= a.d_out;
-    float y[2][8];
+  const int64_t n_first = (int64_t)blockIdx.y * a.cols;
+  const int64_t n_end = n_first + a.cols < a.d_out ? n_first + a.cols : a.d_out;
+  const uint32_t tile = (uint32_t)__ballot(mine >= 0);
+  const int lead = tile ? __builtin_amdgcn_readlane(mine, __builtin_ctz(tile)) : -1;   // the tile's first adapter
+
+  // A step's base and the first adapter's B, in memory's form, asked for while
+  // the step before is worked on.  kYW 16-byte words hold 8 outputs.
+  constexpr int kYW = kY == GPTQ_F32 ? 2 : 1;
+  constexpr int kYE = kY == GPTQ_F32 ? 4 : 2;
+  struct Step {
+    u32x4 y[2][kYW], b[2][kS];
+  };
+  auto read_b = [&](int64_t n, int ad, u32x4 (&b)[2][kS]) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t m = m0 + t * 16 + c16;
+    for (int h = 0; h < 2; ++h) {
+      // the MFMA's row c16 is column 8 (c16 / 4) + 4 h + c16 % 4
+      int64_t bc = n + 8 * (c16 >> 2) + 4 * h + (c16 & 3);
+      bc = bc < a.d_out ? bc : a.d_out - 1;
+      const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[t][i] = 0.f;
-      if (a.base && m < a.M) {
-        if (whole) {
-          if constexpr (kY == GPTQ_F32) {
-            const float* p = static_cast<const float*>(a.base) + m * a.ld_b + col;
-            f32x4 u, w;
-            __builtin_memcpy(&u, __builtin_assume_aligned(p, 4), 16);
-            __builtin_memcpy(&w, __builtin_assume_aligned(p + 4, 4), 16);
+      for (int s = 0; s < kS; ++s) {
+        if (a.rank == kS * 32) b[h][s] = load8(row + s * 32 + 8 * q);
+        else b[h][s] = load8_end(row, s * 32 + 8 * q, a.rank);
+      }
+    }
+  };
+  auto read = [&](int64_t n, Step& p) {
+    if (a.base && a.d_out >= 8) {
+      const int64_t col = min(n + 8 * q, a.d_out - 8);   // lanes at the end read theirs one by one later
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[t][i] = u[i];
-              y[t][4 + i] = w[i];
-            }
-          } else {
-            const u32x4 u = load8(static_cast<const uint16_t*>(a.base) + m * a.ld_b + col);
+      for (int t = 0; t < 2; ++t) {
+        const char* y = static_cast<const char*>(a.base) + (min(m0 + t * 16 + c16, a.M - 1) * a.ld_b + col) * kYE;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[t][2 * i] = lo16<kY>(u[i]);
-              y[t][2 * i + 1] = hi16<kY>(u[i]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + i < a.d_out) y[t][i] = load_el<kY>(a.base, m * a.ld_b + col + i);
+        for (int w = 0; w < kYW; ++w) {
+          if constexpr (kY == GPTQ_F32) __builtin_memcpy(&p.y[t][w], __builtin_assume_aligned(y + 16 * w, 4), 16);
+          else __builtin_memcpy(&p.y[t][w], __builtin_assume_aligned(y, 2), 16);
         }
       }
     }
+    if (lead >= 0) read_b(n, lead, p.b);
+  };
+  auto finish = [&](int64_t n, const Step& p) {
+    const int64_t col = n + 8 * q;         // this lane's eight columns
+    const bool whole = col + 8 <= a.d_out;
     f32x4 acc[2][2];                       // [token tile][column half]
 #pragma unroll
     for (int t = 0; t < 2; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for_each_adapter(mine, [&](int ad) {
+    auto pass = [&](int ad, const u32x4 (&b)[2][kS]) {
       f32x4 d[2][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) d[t][0] = d[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // the MFMA's row c16 is column 8 (c16 / 4) + 4 h + c16 % 4
-        int64_t bc = n + 8 * (c16 >> 2) + 4 * h + (c16 & 3);
-        bc = bc < a.d_out ? bc : a.d_out - 1;
-        const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
-        u32x4 b[kS];
+      for (int s = 0; s < kS; ++s)
 #pragma unroll
-        for (int s = 0; s < kS; ++s) b[s] = load8_end(row, s * 32 + 8 * q, a.rank);
-#pragma unroll
-        for (int s = 0; s < kS; ++s)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            d[t][h] = lora_mfma<kDt>(b[s], lo[t][s], d[t][h]);
-            d[t][h] = lora_mfma<kDt>(b[s], hi[t][s], d[t][h]);
+            d[t][h] = lora_mfma<kDt>(b[h][s], lo[t][s], d[t][h]);
+            d[t][h] = lora_mfma<kDt>(b[h][s], hi[t][s], d[t][h]);
           }
-      }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[t][h][i] = own[t] == ad ? d[t][h][i] : acc[t][h][i];
+    };
+    for_each_adapter(mine, [&](int ad) {
+      if (ad == lead) {
+        pass(ad, p.b);
+      } else {
+        u32x4 b[2][kS];
+        read_b(n, ad, b);
+        pass(ad, b);
+      }
     });
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int64_t m = m0 + t * 16 + c16;
       if (m >= a.M) continue;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = 0.f;
+      if (a.base) {
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (kY == GPTQ_F32) {
+              y[i] = __uint_as_float(p.y[t][0][i]);
+              y[4 + i] = __uint_as_float(p.y[t][kYW - 1][i]);
+            } else {
+              y[2 * i] = lo16<kY>(p.y[t][0][i]);
+              y[2 * i + 1] = hi16<kY>(p.y[t][0][i]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + i < a.d_out) y[i] = load_el<kY>(a.base, m * a.ld_b + col + i);
+        }
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[t][4 * h + i] = fmaf(acc[t][h][i], grow[t], y[t][4 * h + i]);
+        for (int i = 0; i < 4; ++i) y[4 * h + i] = fmaf(acc[t][h][i], grow[t], y[4 * h + i]);
       if (whole) {
         if constexpr (kY == GPTQ_F32) {
-          float* p = static_cast<float*>(a.Y) + m * a.ld_y + col;
-          __builtin_memcpy(__builtin_assume_aligned(p, 4), &y[t][0], 16);
-          __builtin_memcpy(__builtin_assume_aligned(p + 4, 4), &y[t][4], 16);
+          float* o = static_cast<float*>(a.Y) + m * a.ld_y + col;
+          __builtin_memcpy(__builtin_assume_aligned(o, 4), &y[0], 16);
+          __builtin_memcpy(__builtin_assume_aligned(o + 4, 4), &y[4], 16);
         } else {
           typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
           u16x8 w;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if constexpr (kY == GPTQ_F16) w[i] = __builtin_bit_cast(uint16_t, (_Float16)y[t][i]);
-            else w[i] = __builtin_bit_cast(uint16_t, (__bf16)y[t][i]);
+            if constexpr (kY == GPTQ_F16) w[i] = __builtin_bit_cast(uint16_t, (_Float16)y[i]);
+            else w[i] = __builtin_bit_cast(uint16_t, (__bf16)y[i]);
           }
           __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(a.Y) + m * a.ld_y + col, 2), &w, 16);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (col + i < a.d_out) store_el<kY>(a.Y, m * a.ld_y + col + i, y[t][i]);
+          if (col + i < a.d_out) store_el<kY>(a.Y, m * a.ld_y + col + i, y[i]);
       }
+    }
+  };
+  int64_t n = n_first + wave * 32;
+  if (n >= n_end) return;
+  Step even, odd;
+  read(n, even);
+  for (; n < n_end; n += 256) {
+    if (n + 128 < n_end) read(n + 128, odd);
+    finish(n, even);
+    if (n + 128 < n_end) {
+      if (n + 256 < n_end) read(n + 256, even);
+      finish(n + 128, odd);
     }
   }
 }
 
 struct LoraPlan {
-  int rp, splits, k_split;
+  int rp, splits, k_split, cols;
   size_t total;
 };
 
-static LoraPlan lora_plan(int64_t M, int64_t d_in, int64_t rank) {
+static LoraPlan lora_plan(int64_t M, int64_t d_in, int64_t d_out, int64_t rank) {
   LoraPlan p;
   p.rp = (int)(cdiv(rank, 8) * 8);
   p.splits = 1;
@@ -391,13 +468,19 @@ static LoraPlan lora_plan(int64_t M, int64_t d_in, int64_t rank) {
     const int64_t tiles = cdiv(M, kLoraTile);
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(512, tiles), d_in / 256));
   }
+  // columns of a workgroup: as many as leave every CU four workgroups, so that
+  // T's sum is made for more of them
+  p.cols = 1024;
+  while (p.cols > 128 && cdiv(M, kLoraTile) * cdiv(d_out, p.cols) < 1024) p.cols /= 2;
   p.k_split = (int)(cdiv(cdiv(d_in, p.splits), 64) * 64);
   p.splits = (int)cdiv(d_in, p.k_split);
   p.total = align_up((size_t)p.splits * M * p.rp * 4, 256);
   return p;
 }
 
-size_t lora_workspace_bytes(int64_t M, int64_t d_in, int64_t, int64_t rank) { return lora_plan(M, d_in, rank).total; }
+size_t lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank) {
+  return lora_plan(M, d_in, d_out, rank).total;
+}
 
 size_t w4a16_lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank) {
   return align_up(w4a16_workspace_bytes(M, d_in, d_out), 256) + lora_workspace_bytes(M, d_in, d_out, rank);
@@ -415,7 +498,7 @@ static void lora_up_few(const LoraArgs& a, hipStream_t st) {
 
 template <int kDt, int kY>
 static void lora_up(const LoraArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(a.M, kLoraTile), (unsigned)cdiv(a.d_out, kLoraCols));
+  const dim3 grid((unsigned)cdiv(a.M, kLoraTile), (unsigned)cdiv(a.d_out, a.cols));
   if (a.rp <= 32) hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 1>), grid, dim3(256), 0, st, a);
   else if (a.rp <= 64) hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 2>), grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 4>), grid, dim3(256), 0, st, a);
@@ -463,7 +546,7 @@ extern "C" gptq_status gptq_lora_add(const void* X, int32_t x_dtype, int64_t M, 
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(X) % 2 == 0 && reinterpret_cast<uintptr_t>(A) % 2 == 0 &&
                reinterpret_cast<uintptr_t>(B) % 2 == 0 && reinterpret_cast<uintptr_t>(Y) % ys == 0 &&
                reinterpret_cast<uintptr_t>(base) % ys == 0);
-  const LoraPlan pl = lora_plan(M, d_in, rank);
+  const LoraPlan pl = lora_plan(M, d_in, d_out, rank);
   if (workspace == nullptr || ws_bytes < pl.total) return GPTQ_ENOMEM;
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(workspace) % 256 == 0);
   LoraArgs a{};
@@ -486,6 +569,7 @@ extern "C" gptq_status gptq_lora_add(const void* X, int32_t x_dtype, int64_t M, 
   a.rp = pl.rp;
   a.splits = pl.splits;
   a.k_split = pl.k_split;
+  a.cols = pl.cols;
   hipStream_t st = static_cast<hipStream_t>(stream);
   TimedScope ts(kTimeLora, st);
   if (x_dtype == GPTQ_F16) lora_launch<GPTQ_F16>(a, y_dtype, st);
