@@ -17,14 +17,15 @@
 // 16-bit terms, whose sum carries 16 significant bits (bf16) or 22 (fp16; rows
 // of T are scaled by a power of two first, so that neither their size nor
 // their smallness leaves fp16's range): 16 bits alone would put an error of
-// 2^-9 or 2^-12 of the adapter's part into fp32 results.  Tokens are the MFMA's
-// columns and output columns its rows, dealt so that a lane ends up with eight
-// consecutive outputs of one token: base and Y move 16 or 32 bytes at a time.
-// Operands are read from global memory in the form that the MFMA takes (8
-// consecutive elements per lane), at any alignment.
+// 2^-9 or 2^-12 of the adapter's part into fp32 results.  The second product's
+// columns are dealt to the MFMA tiles so that a lane ends up with four
+// consecutive outputs and sixteen lanes with 64: base and Y move in pieces of
+// 256 (fp32) or 128 bytes, at any alignment.
 //
 // Bound by memory: X, base and Y once, the factors from L2 (a factor's matrix
 // serves every tile of its adapter).
+#include <type_traits>
+
 #include "lora.h"
 
 namespace gq {
@@ -124,6 +125,27 @@ __device__ __forceinline__ void for_each_adapter(int mine, F f) {
   }
 }
 
+// Tile and part of workgroup b of `parts` per tile.  Workgroups go to the eight
+// XCDs in turn, each with an L2 of its own; with many tiles every XCD takes a
+// run of neighbouring ones, whose tokens mostly share an adapter, so that its
+// factors stay in that L2.  With fewer than 64 tiles the runs would leave XCDs
+// idle.
+__device__ __forceinline__ void lora_place(const LoraArgs& a, int parts, int64_t b, int64_t& tile, int& part) {
+  const int64_t tiles = (a.M + kLoraTile - 1) / kLoraTile;
+  if (tiles < 64) {
+    tile = b / parts;
+    part = (int)(b % parts);
+  } else {
+    const int64_t run = (tiles + 7) / 8, i = b / 8;
+    tile = b % 8 * run + i / parts;
+    part = (int)(i % parts);
+  }
+}
+static int64_t lora_blocks(int64_t M, int64_t parts) {
+  const int64_t tiles = cdiv(M, kLoraTile);
+  return (tiles < 64 ? tiles : cdiv(tiles, 8) * 8) * parts;
+}
+
 __device__ __forceinline__ int lora_adapter(const LoraArgs& a, int64_t m) {
   const int ad = m < a.M ? a.adapter[m] : -1;
   return ad < a.n ? ad : -1;
@@ -138,8 +160,12 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
   __shared__ __align__(16) float red[4][kLoraTile][kStride];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
-  const int64_t m0 = (int64_t)blockIdx.x * kLoraTile;
-  const int k0 = blockIdx.y * a.k_split, k1 = min(k0 + a.k_split, a.d_in);
+  int64_t tile;
+  int part;
+  lora_place(a, a.splits, blockIdx.x, tile, part);
+  const int64_t m0 = tile * kLoraTile;
+  if (m0 >= a.M) return;
+  const int k0 = part * a.k_split, k1 = min(k0 + a.k_split, a.d_in);
   const int mine = lora_adapter(a, m0 + (lane & 31));
   const uint16_t* x[2];
 #pragma unroll
@@ -204,7 +230,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
     // 8 threads per token
     const int tok = threadIdx.x >> 3;
     if (__shfl(mine, tok & 31) == ad) {
-      float* out = a.T + ((int64_t)blockIdx.y * a.M + m0 + tok) * a.rp;
+      float* out = a.T + ((int64_t)part * a.M + m0 + tok) * a.rp;
       for (int r = (threadIdx.x & 7) * 4; r < a.rp; r += 32) {
         f32x4 s = *reinterpret_cast<const f32x4*>(&red[0][tok][r]);
 #pragma unroll
@@ -215,6 +241,118 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
       }
     }
     __syncthreads();
+  });
+}
+
+// The same for rows on 16 bytes: operands through LDS.  Reading them straight
+// into MFMA form gives every lane of 16 another row, 64 separate accesses per
+// load, and the address units are what the kernel above waits for (8192 x
+// 11008, rank 64: 97 us, address units busy half of it).  Here 16 lanes load
+// 256 bytes of one row, directly into LDS, two steps of 128 elements ahead; the
+// unit u of row m lies at slot u ^ (m % 16), so that a fragment's 16 rows lie in
+// 16 slots.  Four waves share the kR x 2 tiles of ranks and tokens.
+template <int kDt, int kR>
+__global__ __launch_bounds__(256) void lora_down_lds_kernel(LoraArgs a) {
+  constexpr int kRows = kLoraTile + kR * 16;           // rows of a stage: tokens, then ranks
+  constexpr int kStage = kRows * 256;
+  constexpr int kLoads = kRows / 16;                   // direct loads of a wave per step
+  constexpr int kMine = kR == 2 ? 1 : kR / 4;          // rank tiles of a wave
+  constexpr int kTok = kR == 2 ? 1 : 2;                // token tiles of a wave
+  constexpr int kWait = (kLoads & 0xF) | ((kLoads >> 4) << 14) | (7 << 4) | (0xF << 8);
+  static_assert(kRows % 16 == 0 && kLoads < 64, "whole loads, counted in six bits");
+  // one array per stage, so the compiler sees which one a read touches
+  __shared__ __attribute__((aligned(1024))) char x0[kStage], x1[kStage], x2[kStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, q = lane >> 4;
+  int64_t tile;
+  int part;
+  lora_place(a, a.splits, blockIdx.x, tile, part);
+  const int64_t m0 = tile * kLoraTile;
+  if (m0 >= a.M) return;
+  const int k0 = part * a.k_split, k1 = min(k0 + a.k_split, a.d_in);
+  const int steps = (k1 - k0 + 127) / 128;
+  const int mine = lora_adapter(a, m0 + (lane & 31));
+  const int rank0 = kR == 2 ? (wave & 1) * 16 : wave * kMine * 16;   // this wave's first rank and token
+  const int tok0 = kR == 2 ? (wave >> 1) * 16 : 0;
+  for_each_adapter(mine, [&](int ad) {
+    // this lane's part of load i: row 16 i + 4 wave + lane / 16 of the stage, slot lane % 16
+    const uint16_t* src[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = 16 * i + 4 * wave + (lane >> 4);
+      src[i] = row < kLoraTile
+                   ? a.X + min(m0 + row, a.M - 1) * a.ld_x
+                   : a.A + ((int64_t)ad * a.rank + min(row - kLoraTile, a.rank - 1)) * a.d_in;
+    }
+    const int unit = (lane & 15) ^ ((4 * wave + (lane >> 4)) & 15);
+    auto fetch = [&](int step, char* to) {
+      // units behind the part's end read its last one and are never multiplied;
+      // steps behind the last one are read so that every step has as many loads
+      const int k = min(k0 + min(step, steps - 1) * 128 + unit * 8, k1 - 8);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) lds_load16(src[i] + k, to + (16 * i + 4 * wave) * 256);
+    };
+    f32x4 acc[kMine][kTok];
+#pragma unroll
+    for (int r = 0; r < kMine; ++r)
+#pragma unroll
+      for (int t = 0; t < kTok; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](int step, const char* from) {
+      const int left = k1 - (k0 + step * 128);         // elements of the step
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int u = 4 * j + q;
+        u32x4 xv[kTok], fv[kMine];
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+          xv[t] = *reinterpret_cast<const u32x4*>(from + (tok0 + t * 16 + c16) * 256 + ((u ^ c16) * 16));
+#pragma unroll
+        for (int r = 0; r < kMine; ++r)
+          fv[r] = *reinterpret_cast<const u32x4*>(from + (kLoraTile + rank0 + r * 16 + c16) * 256 + ((u ^ c16) * 16));
+        if (left < 128 && u * 8 >= left) {
+#pragma unroll
+          for (int t = 0; t < kTok; ++t) xv[t] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int r = 0; r < kMine; ++r) fv[r] = u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int r = 0; r < kMine; ++r)
+#pragma unroll
+          for (int t = 0; t < kTok; ++t) acc[r][t] = lora_mfma<kDt>(fv[r], xv[t], acc[r][t]);
+      }
+    };
+    fetch(0, x0);
+    fetch(1, x1);
+#define GQ_LORA_STAGE(u, CUR, NEXT)                               \
+  {                                                               \
+    __builtin_amdgcn_s_waitcnt(kWait);                            \
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); \
+    fetch(s + (u) + 2, NEXT);                                     \
+    if (s + (u) < steps) multiply(s + (u), CUR);                  \
+  }
+    for (int s = 0; s < steps; s += 3) {
+      GQ_LORA_STAGE(0, x0, x2);
+      GQ_LORA_STAGE(1, x1, x0);
+      GQ_LORA_STAGE(2, x2, x1);
+    }
+#undef GQ_LORA_STAGE
+    // the direct loads have landed, and every wave is done reading, before the
+    // next adapter's (or the end)
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) {
+      const int tok = tok0 + t * 16 + c16;
+      if (__shfl(mine, tok) != ad) continue;
+      float* out = a.T + ((int64_t)part * a.M + m0 + tok) * a.rp;
+#pragma unroll
+      for (int r = 0; r < kMine; ++r) {
+        const int k = rank0 + r * 16 + 4 * q;
+        f32x4 v = acc[r][t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = k + i < a.rank ? v[i] : 0.f;
+        if (k < a.rp) *reinterpret_cast<f32x4*>(out + k) = v;
+      }
+    }
   });
 }
 
@@ -242,14 +380,20 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4& hi, u32x4
   }
 }
 
-// 32 tokens by `cols` columns (a multiple of 128); kS steps of 32 ranks.
+// 32 tokens by `cols` columns (a multiple of 256); kS steps of 32 ranks.
 template <int kDt, int kY, int kS>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   constexpr int kPitch = kS * 32 + 4;
   __shared__ __align__(16) float tsum[kLoraTile][kPitch];
+  __shared__ u32x4 terms[2][kS][2][64];    // [token tile][rank step][first, second term][lane]
+  __shared__ __align__(16) float grow[kLoraTile];   // 2^e that a token's terms were divided by
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
-  const int64_t m0 = (int64_t)blockIdx.x * kLoraTile;
+  int64_t tile;
+  int part;
+  lora_place(a, (int)((a.d_out + a.cols - 1) / a.cols), blockIdx.x, tile, part);
+  const int64_t m0 = tile * kLoraTile;
+  if (m0 >= a.M) return;
   const int mine = lora_adapter(a, m0 + (lane & 31));
   // T's parts added up, scaled: 8 threads per token, 4 ranks at a time
   {
@@ -277,12 +421,10 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
     }
   }
   __syncthreads();
-  int own[2];                              // adapters of this lane's two tokens
-  float grow[2];                           // 2^e that T's terms were divided by
-  u32x4 hi[2][kS], lo[2][kS];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    own[t] = __shfl(mine, t * 16 + c16);
+  // T's terms as operands into LDS, one wave per token tile: row c16 = token
+  // t 16 + c16, 8 ranks per lane
+  if (wave < 2) {
+    const int t = wave;
     float v[kS][8];
     float big = 0.f;
 #pragma unroll
@@ -296,160 +438,140 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
           big = fmaxf(big, fabsf(u[i]));
         }
       }
-    grow[t] = 1.f;
+    float g = 1.f;
     if constexpr (kDt == GPTQ_F16) {
       big = fmaxf(big, __shfl_xor(big, 16));
       big = fmaxf(big, __shfl_xor(big, 32));
       if (big > 0.f && big < INFINITY) {
         int e;
         frexpf(big, &e);
-        grow[t] = ldexpf(1.f, e - 14);   // the largest below 2^14: the second terms stay normal numbers
+        g = ldexpf(1.f, e - 14);   // the largest below 2^14: the second terms stay normal numbers
 #pragma unroll
         for (int s = 0; s < kS; ++s)
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[s][i] = ldexpf(v[s][i], 14 - e);
       }
     }
+    if (q == 0) grow[t * 16 + c16] = g;
 #pragma unroll
-    for (int s = 0; s < kS; ++s) lora_split<kDt>(v[s], hi[t][s], lo[t][s]);
+    for (int s = 0; s < kS; ++s) {
+      u32x4 hi, lo;
+      lora_split<kDt>(v[s], hi, lo);
+      terms[t][s][0][lane] = hi;
+      terms[t][s][1][lane] = lo;
+    }
   }
-  const int64_t n_first = (int64_t)blockIdx.y * a.cols;
+  __syncthreads();
+  const int64_t n_first = (int64_t)part * a.cols;
   const int64_t n_end = n_first + a.cols < a.d_out ? n_first + a.cols : a.d_out;
-  const uint32_t tile = (uint32_t)__ballot(mine >= 0);
-  const int lead = tile ? __builtin_amdgcn_readlane(mine, __builtin_ctz(tile)) : -1;   // the tile's first adapter
+  const uint32_t some = (uint32_t)__ballot(mine >= 0);
+  const int lead = some ? __builtin_amdgcn_readlane(mine, __builtin_ctz(some)) : -1;   // the tile's first adapter
 
-  // A step's base and the first adapter's B, in memory's form, asked for while
-  // the step before is worked on.  kYW 16-byte words hold 8 outputs.
-  constexpr int kYW = kY == GPTQ_F32 ? 2 : 1;
+  // 64 columns at a time, column 4 c16 + p in MFMA tile p.
   constexpr int kYE = kY == GPTQ_F32 ? 4 : 2;
-  struct Step {
-    u32x4 y[2][kYW], b[2][kS];
-  };
-  auto read_b = [&](int64_t n, int ad, u32x4 (&b)[2][kS]) {
+  using Four = typename std::conditional<kY == GPTQ_F32, u32x4, uint2>::type;   // four outputs
+  auto read_b = [&](int64_t n, int ad, int p, u32x4 (&b)[kS]) {
+    int64_t bc = n + 4 * c16 + p;
+    bc = bc < a.d_out ? bc : a.d_out - 1;
+    const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // the MFMA's row c16 is column 8 (c16 / 4) + 4 h + c16 % 4
-      int64_t bc = n + 8 * (c16 >> 2) + 4 * h + (c16 & 3);
-      bc = bc < a.d_out ? bc : a.d_out - 1;
-      const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
-#pragma unroll
-      for (int s = 0; s < kS; ++s) {
-        if (a.rank == kS * 32) b[h][s] = load8(row + s * 32 + 8 * q);
-        else b[h][s] = load8_end(row, s * 32 + 8 * q, a.rank);
-      }
+    for (int s = 0; s < kS; ++s) {
+      if (a.rank == kS * 32) b[s] = load8(row + s * 32 + 8 * q);
+      else b[s] = load8_end(row, s * 32 + 8 * q, a.rank);
     }
   };
-  auto read = [&](int64_t n, Step& p) {
-    if (a.base && a.d_out >= 8) {
-      const int64_t col = min(n + 8 * q, a.d_out - 8);   // lanes at the end read theirs one by one later
+  // each wave takes 64 columns in turn; other waves' work covers its loads
+  for (int64_t n = n_first + wave * 64; n < n_end; n += 256) {
+    const int64_t col = n + 4 * c16;       // this lane's four columns
+    const bool whole = col + 4 <= a.d_out;
+    u32x4 b[4][kS];
+    if (lead >= 0) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const char* y = static_cast<const char*>(a.base) + (min(m0 + t * 16 + c16, a.M - 1) * a.ld_b + col) * kYE;
-#pragma unroll
-        for (int w = 0; w < kYW; ++w) {
-          if constexpr (kY == GPTQ_F32) __builtin_memcpy(&p.y[t][w], __builtin_assume_aligned(y + 16 * w, 4), 16);
-          else __builtin_memcpy(&p.y[t][w], __builtin_assume_aligned(y, 2), 16);
-        }
-      }
+      for (int p = 0; p < 4; ++p) read_b(n, lead, p, b[p]);
     }
-    if (lead >= 0) read_b(n, lead, p.b);
-  };
-  auto finish = [&](int64_t n, const Step& p) {
-    const int64_t col = n + 8 * q;         // this lane's eight columns
-    const bool whole = col + 8 <= a.d_out;
-    f32x4 acc[2][2];                       // [token tile][column half]
-#pragma unroll
-    for (int t = 0; t < 2; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto pass = [&](int ad, const u32x4 (&b)[2][kS]) {
-      f32x4 d[2][2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) d[t][0] = d[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < kS; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            d[t][h] = lora_mfma<kDt>(b[h][s], lo[t][s], d[t][h]);
-            d[t][h] = lora_mfma<kDt>(b[h][s], hi[t][s], d[t][h]);
-          }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][h][i] = own[t] == ad ? d[t][h][i] : acc[t][h][i];
-    };
-    for_each_adapter(mine, [&](int ad) {
-      if (ad == lead) {
-        pass(ad, p.b);
-      } else {
-        u32x4 b[2][kS];
-        read_b(n, ad, b);
-        pass(ad, b);
-      }
-    });
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-      const int64_t m = m0 + t * 16 + c16;
-      if (m >= a.M) continue;
-      float y[8];
+      const int64_t m = m0 + t * 16 + 4 * q;   // this lane's four tokens
+      Four in[4];
+      if (a.base && whole) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = 0.f;
-      if (a.base) {
-        if (whole) {
+        for (int i = 0; i < 4; ++i) {
+          const char* y = static_cast<const char*>(a.base) + (min(m + i, a.M - 1) * a.ld_b + col) * kYE;
+          __builtin_memcpy(&in[i], __builtin_assume_aligned(y, kYE), sizeof(Four));
+        }
+      }
+      f32x4 acc[4];                        // [column of the four]
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+      for (int e = 0; e < 4; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+      int own[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = __shfl(mine, t * 16 + 4 * q + i);
+      auto pass = [&](int ad, int e, const u32x4 (&w)[kS]) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+          d = lora_mfma<kDt>(terms[t][s][1][lane], w[s], d);
+          d = lora_mfma<kDt>(terms[t][s][0][lane], w[s], d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[e][i] = own[i] == ad ? d[i] : acc[e][i];
+      };
+      if (lead >= 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pass(lead, e, b[e]);
+      }
+      for_each_adapter((lane & 31) / 16 == t && mine != lead ? mine : -1, [&](int ad) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u32x4 w[kS];
+          read_b(n, ad, e, w);
+          pass(ad, e, w);
+          __builtin_amdgcn_sched_barrier(0);   // one column's operands at a time
+        }
+      });
+      const f32x4 g = *reinterpret_cast<const f32x4*>(&grow[t * 16 + 4 * q]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (m + i >= a.M) continue;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (a.base) {
+          if (whole) {
             if constexpr (kY == GPTQ_F32) {
-              y[i] = __uint_as_float(p.y[t][0][i]);
-              y[4 + i] = __uint_as_float(p.y[t][kYW - 1][i]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(in[i][e]);
             } else {
-              y[2 * i] = lo16<kY>(p.y[t][0][i]);
-              y[2 * i + 1] = hi16<kY>(p.y[t][0][i]);
+              y[0] = lo16<kY>(in[i].x);
+              y[1] = hi16<kY>(in[i].x);
+              y[2] = lo16<kY>(in[i].y);
+              y[3] = hi16<kY>(in[i].y);
             }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < a.d_out) y[e] = load_el<kY>(a.base, (m + i) * a.ld_b + col + e);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e][i], g[i], y[e]);
+        if (whole) {
+          char* o = static_cast<char*>(a.Y) + ((m + i) * a.ld_y + col) * kYE;
+          if constexpr (kY == GPTQ_F32) {
+            __builtin_memcpy(__builtin_assume_aligned(o, 4), y, 16);
+          } else {
+            uint16_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (kY == GPTQ_F16) h[e] = __builtin_bit_cast(uint16_t, (_Float16)y[e]);
+              else h[e] = __builtin_bit_cast(uint16_t, (__bf16)y[e]);
+            }
+            __builtin_memcpy(__builtin_assume_aligned(o, 2), h, 8);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + i < a.d_out) y[i] = load_el<kY>(a.base, m * a.ld_b + col + i);
+          for (int e = 0; e < 4; ++e)
+            if (col + e < a.d_out) store_el<kY>(a.Y, (m + i) * a.ld_y + col + e, y[e]);
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[4 * h + i] = fmaf(acc[t][h][i], grow[t], y[4 * h + i]);
-      if (whole) {
-        if constexpr (kY == GPTQ_F32) {
-          float* o = static_cast<float*>(a.Y) + m * a.ld_y + col;
-          __builtin_memcpy(__builtin_assume_aligned(o, 4), &y[0], 16);
-          __builtin_memcpy(__builtin_assume_aligned(o + 4, 4), &y[4], 16);
-        } else {
-          typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-          u16x8 w;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if constexpr (kY == GPTQ_F16) w[i] = __builtin_bit_cast(uint16_t, (_Float16)y[i]);
-            else w[i] = __builtin_bit_cast(uint16_t, (__bf16)y[i]);
-          }
-          __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(a.Y) + m * a.ld_y + col, 2), &w, 16);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col + i < a.d_out) store_el<kY>(a.Y, m * a.ld_y + col + i, y[i]);
-      }
-    }
-  };
-  int64_t n = n_first + wave * 32;
-  if (n >= n_end) return;
-  Step even, odd;
-  read(n, even);
-  for (; n < n_end; n += 256) {
-    if (n + 128 < n_end) read(n + 128, odd);
-    finish(n, even);
-    if (n + 128 < n_end) {
-      if (n + 256 < n_end) read(n + 256, even);
-      finish(n + 128, odd);
     }
   }
 }
@@ -464,15 +586,17 @@ static LoraPlan lora_plan(int64_t M, int64_t d_in, int64_t d_out, int64_t rank) 
   p.rp = (int)(cdiv(rank, 8) * 8);
   p.splits = 1;
   if (M > kLoraFew) {
-    // parts of the sum until every CU has two workgroups, of at least one step per wave
+    // parts of the sum until every CU has had eight workgroups (a tile of two
+    // adapters takes twice as long, and must not be the last to end), of at
+    // least one step per wave
     const int64_t tiles = cdiv(M, kLoraTile);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(512, tiles), d_in / 256));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(2048, tiles), d_in / 256));
   }
-  // columns of a workgroup: as many as leave every CU four workgroups, so that
+  // columns of a workgroup: as many as leave every CU eight workgroups, so that
   // T's sum is made for more of them
   p.cols = 1024;
-  while (p.cols > 128 && cdiv(M, kLoraTile) * cdiv(d_out, p.cols) < 1024) p.cols /= 2;
-  p.k_split = (int)(cdiv(cdiv(d_in, p.splits), 64) * 64);
+  while (p.cols > 256 && cdiv(M, kLoraTile) * cdiv(d_out, p.cols) < 2048) p.cols /= 2;
+  p.k_split = (int)(cdiv(cdiv(d_in, p.splits), 128) * 128);
   p.splits = (int)cdiv(d_in, p.k_split);
   p.total = align_up((size_t)p.splits * M * p.rp * 4, 256);
   return p;
@@ -498,7 +622,7 @@ static void lora_up_few(const LoraArgs& a, hipStream_t st) {
 
 template <int kDt, int kY>
 static void lora_up(const LoraArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(a.M, kLoraTile), (unsigned)cdiv(a.d_out, a.cols));
+  const dim3 grid((unsigned)lora_blocks(a.M, cdiv(a.d_out, a.cols)));
   if (a.rp <= 32) hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 1>), grid, dim3(256), 0, st, a);
   else if (a.rp <= 64) hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 2>), grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((lora_up_kernel<kDt, kY, 4>), grid, dim3(256), 0, st, a);
@@ -513,11 +637,19 @@ static void lora_launch(const LoraArgs& a, int32_t y_dtype, hipStream_t st) {
     else lora_up_few<kDt, kDt>(a, st);
     return;
   }
-  const dim3 grid((unsigned)cdiv(a.M, kLoraTile), (unsigned)a.splits);
-  if (a.rank <= 16) hipLaunchKernelGGL((lora_down_kernel<kDt, 1>), grid, dim3(256), 0, st, a);
-  else if (a.rank <= 32) hipLaunchKernelGGL((lora_down_kernel<kDt, 2>), grid, dim3(256), 0, st, a);
-  else if (a.rank <= 64) hipLaunchKernelGGL((lora_down_kernel<kDt, 4>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((lora_down_kernel<kDt, 8>), grid, dim3(256), 0, st, a);
+  const dim3 grid((unsigned)lora_blocks(a.M, a.splits));
+  const bool aligned = a.d_in % 8 == 0 && a.ld_x % 8 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.A) % 16 == 0;
+  if (aligned) {
+    if (a.rank <= 32) hipLaunchKernelGGL((lora_down_lds_kernel<kDt, 2>), grid, dim3(256), 0, st, a);
+    else if (a.rank <= 64) hipLaunchKernelGGL((lora_down_lds_kernel<kDt, 4>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((lora_down_lds_kernel<kDt, 8>), grid, dim3(256), 0, st, a);
+  } else {
+    if (a.rank <= 16) hipLaunchKernelGGL((lora_down_kernel<kDt, 1>), grid, dim3(256), 0, st, a);
+    else if (a.rank <= 32) hipLaunchKernelGGL((lora_down_kernel<kDt, 2>), grid, dim3(256), 0, st, a);
+    else if (a.rank <= 64) hipLaunchKernelGGL((lora_down_kernel<kDt, 4>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((lora_down_kernel<kDt, 8>), grid, dim3(256), 0, st, a);
+  }
   if (y_dtype == GPTQ_F32) lora_up<kDt, GPTQ_F32>(a, st);
   else lora_up<kDt, kDt>(a, st);
 }

@@ -358,14 +358,6 @@ constexpr int kW4Ring = 6;
 __host__ __device__ constexpr int w4_wide_pitch(int ng) { return (3 * ng + 3) / 4 * 4 + 4; }
 constexpr int kW4WideParams = 40960;    // LDS bytes for them
 
-// 64 lanes' 16 (4) bytes each, one after the other from `to` on.
-__device__ __forceinline__ void lds_load16(const void* from, char* to) {
-  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
-}
-__device__ __forceinline__ void lds_load4(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
-}
-
 template <int kDt, int kMT, int kRT, bool kLora>
 __global__ __launch_bounds__(256, 1) void w4_wide_kernel(W4Args a) {
   constexpr int kStage = kMT * 16 * 256;
