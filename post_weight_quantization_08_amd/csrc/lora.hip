@@ -395,6 +395,32 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   const int64_t m0 = tile * kLoraTile;
   if (m0 >= a.M) return;
   const int mine = lora_adapter(a, m0 + (lane & 31));
+  const int64_t n_first = (int64_t)part * a.cols;
+  const int64_t n_end = n_first + a.cols < a.d_out ? n_first + a.cols : a.d_out;
+  const uint32_t some = (uint32_t)__ballot(mine >= 0);
+  const int lead = some ? __builtin_amdgcn_readlane(mine, __builtin_ctz(some)) : -1;   // the tile's first adapter
+
+  auto read_b = [&](int64_t n, int ad, int p, u32x4 (&b)[kS]) {
+    int64_t bc = n + 4 * c16 + p;
+    bc = bc < a.d_out ? bc : a.d_out - 1;
+    const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      if (a.rank == kS * 32) b[s] = load8(row + s * 32 + 8 * q);
+      else b[s] = load8_end(row, s * 32 + 8 * q, a.rank);
+    }
+  };
+  // each wave takes 64 columns in turn; the first ones' B is on its way while T
+  // is made, the next ones' while these are stored
+  int64_t n = n_first + wave * 64;
+  u32x4 b[4][kS];
+  auto read_lead = [&]() {
+    if (lead >= 0 && n < n_end) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) read_b(n, lead, p, b[p]);
+    }
+  };
+  read_lead();
   // T's parts added up, scaled: 8 threads per token, 4 ranks at a time
   {
     const int tok = threadIdx.x >> 3;
@@ -462,33 +488,12 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
     }
   }
   __syncthreads();
-  const int64_t n_first = (int64_t)part * a.cols;
-  const int64_t n_end = n_first + a.cols < a.d_out ? n_first + a.cols : a.d_out;
-  const uint32_t some = (uint32_t)__ballot(mine >= 0);
-  const int lead = some ? __builtin_amdgcn_readlane(mine, __builtin_ctz(some)) : -1;   // the tile's first adapter
-
   // 64 columns at a time, column 4 c16 + p in MFMA tile p.
   constexpr int kYE = kY == GPTQ_F32 ? 4 : 2;
   using Four = typename std::conditional<kY == GPTQ_F32, u32x4, uint2>::type;   // four outputs
-  auto read_b = [&](int64_t n, int ad, int p, u32x4 (&b)[kS]) {
-    int64_t bc = n + 4 * c16 + p;
-    bc = bc < a.d_out ? bc : a.d_out - 1;
-    const uint16_t* row = a.B + ((int64_t)ad * a.d_out + bc) * a.rank;
-#pragma unroll
-    for (int s = 0; s < kS; ++s) {
-      if (a.rank == kS * 32) b[s] = load8(row + s * 32 + 8 * q);
-      else b[s] = load8_end(row, s * 32 + 8 * q, a.rank);
-    }
-  };
-  // each wave takes 64 columns in turn; other waves' work covers its loads
-  for (int64_t n = n_first + wave * 64; n < n_end; n += 256) {
+  while (n < n_end) {
     const int64_t col = n + 4 * c16;       // this lane's four columns
     const bool whole = col + 4 <= a.d_out;
-    u32x4 b[4][kS];
-    if (lead >= 0) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) read_b(n, lead, p, b[p]);
-    }
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       const int64_t m = m0 + t * 16 + 4 * q;   // this lane's four tokens
@@ -573,6 +578,8 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
         }
       }
     }
+    n += 256;
+    read_lead();
   }
 }
 
