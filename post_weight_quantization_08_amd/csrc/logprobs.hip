@@ -138,7 +138,13 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t* v, int k) {
 __device__ __forceinline__ int rank_of(uint64_t key, const uint64_t* keys, int n) {
   int r = 0;
   int i = 0;
-  for (; i + 4 <= n; i += 4) r += (keys[i] > key) + (keys[i + 1] > key) + (keys[i + 2] > key) + (keys[i + 3] > key);
+  for (; i + 8 <= n; i += 8) {
+    uint64_t q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = keys[i + e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r += q[e] > key;
+  }
   for (; i < n; ++i) r += keys[i] > key;
   return r;
 }
@@ -395,10 +401,13 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs a) {
     if (broken) {
       lp_walk<kDt, kGs, false, true>(a, bl, b0, b1, bound, sh);
     } else {
-      lp_collect<kDt, kGs, false>(a, bl, b0, b1, bound, sh);
-      if (sh.count > kLpKeys) {
-        // ties at the bound (masked logits, say): what is above it, then the
-        // first of the ties
+      // a bound that is the type's lowest value or -inf means a masked part
+      // where next to everything ties: not worth a collection
+      const float lowest = kDt == GPTQ_F16 ? -65504.f : kDt == GPTQ_BF16 ? -3.3895314e38f : -3.4028235e38f;
+      const bool masked = bound != 0 && bound <= order_of(lowest) >> kShift;
+      if (!masked) lp_collect<kDt, kGs, false>(a, bl, b0, b1, bound, sh);
+      if (masked || sh.count > kLpKeys) {
+        // ties at the bound: what is above it, then the first of the ties
         lp_collect<kDt, kGs, true>(a, bl, b0, b1, bound, sh);
         if (sh.count < a.k) lp_walk<kDt, kGs, true, false>(a, bl, b0, b1, bound, sh);
         else if (sh.count > kLpKeys) lp_walk<kDt, kGs, false, false>(a, bl, b0, b1, bound, sh);
@@ -458,35 +467,62 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LpArgs a) {
   if (tid == 0) lp_write_row(a, row, out, x_target, scored);
   if (a.k == 0) return;
   sh.lane_order[tid] = (uint32_t)(best >> 32) >> kShift;
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) sh.count = sh.flagged = 0;
   __syncthreads();
   const uint32_t bound = kth_largest<kOrderBits<kDt>>(sh.lane_order, a.k);
 #pragma unroll
   for (int i = 0; i < kMine; ++i)
     if (key[i] != 0 && (uint32_t)(key[i] >> 32) >> kShift >= bound) {
       const int at = atomicAdd(&sh.count, 1);
-      if (at < kLpKeys) sh.keys[at] = key[i];
+      if (at < kLpThreads) sh.keys[at] = key[i];
     }
   __syncthreads();
   const int n = sh.count;
-  if (n <= kLpKeys) {
-    for (int at = tid; at < n; at += kLpThreads) {
-      const uint64_t q = sh.keys[at];
+  if (n <= kLpThreads) {
+    if (tid < n) {
+      const uint64_t q = sh.keys[tid];
       const int r = rank_of(q, sh.keys, n);
-      if (r >= a.k) continue;
-      a.top_lp[row * a.k + r] = out.logprob(value_of((uint32_t)(q >> 32)));
-      a.top_id[row * a.k + r] = (int32_t)index_of(q);
+      if (r < a.k) {
+        a.top_lp[row * a.k + r] = out.logprob(value_of((uint32_t)(q >> 32)));
+        a.top_id[row * a.k + r] = (int32_t)index_of(q);
+      }
     }
   } else {
-    // many ties at the bound: every key against every other
+    // many ties at the bound (masked parts hold only such): the k-th largest
+    // key (they differ) itself, its bits from the top: the value's, then those
+    // of 0xFFFFFFFF - index that an index below 2^21 can clear; only the k keys
+    // that reach it are ranked
+    uint64_t kth = 0;
+    int turn = 0;
+    auto settle = [&](int bit, uint64_t fixed) {
+      const uint64_t cand = kth | fixed | 1ull << bit;
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) c += __popcll(__ballot(key[i] >= cand));
+      if ((tid & 63) == 0) sh.list[(turn & 1) * 4 + (tid >> 6)] = (uint16_t)c;
+      __syncthreads();
+      const uint16_t* got = sh.list + (turn & 1) * 4;
+      if (got[0] + got[1] + got[2] + got[3] >= a.k) kth = cand;
+      ++turn;
+    };
+    for (int b = 63; b >= 32 + kShift; --b) settle(b, 0);
+    // a 16-bit value's order ends in zeros, a negative one's or a NaN's in ones
+    const uint32_t top = (uint32_t)(kth >> 32) >> kShift;
+    const bool ones = top >> (31 - kShift) == 0 || top == 0xFFFFFFFFu >> kShift;
+    const uint64_t fixed = 0xFFE00000ull | (ones ? ((1ull << kShift) - 1) << 32 : 0ull);
+    for (int b = 20; b >= 0; --b) settle(b, fixed);
+    kth |= fixed;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      if (key[i] == 0) continue;
-      int r = 0;
-      for (int j = 0; j < total; ++j) r += src[j] > key[i];
-      if (r >= a.k) continue;
-      a.top_lp[row * a.k + r] = out.logprob(value_of((uint32_t)(key[i] >> 32)));
-      a.top_id[row * a.k + r] = (int32_t)index_of(key[i]);
+      if (key[i] == 0 || key[i] < kth) continue;
+      sh.keys[atomicAdd(&sh.flagged, 1)] = key[i];
+    }
+    __syncthreads();
+    if (tid < a.k) {
+      const uint64_t q = sh.keys[tid];
+      const int r = rank_of(q, sh.keys, a.k);
+      a.top_lp[row * a.k + r] = out.logprob(value_of((uint32_t)(q >> 32)));
+      a.top_id[row * a.k + r] = (int32_t)index_of(q);
     }
   }
 }

@@ -458,3 +458,137 @@ def test_wrappers_refuse_wrong_tensors():
         P.distill_topk(x, ids, lps, weight=torch.ones(3, device="cuda"))
     with pytest.raises(ValueError):
         P.distill_topk(x, ids, lps, out={"loss": torch.empty(2, device="cuda"), "grad": x.half()})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tied", [-np.inf, -2.5, 1.5, np.nan, "lowest"])
+def test_logprobs_ties_over_the_parts_of_a_row(dtype, tied):
+    """Far more ties at the k-th place than a list holds, in every part of a long row."""
+    V, k = 262147, 128
+    x = np.random.default_rng(31).standard_normal(V).astype(np.float32) * 0.5 - 9
+    x[:: 3] = D.LOWEST[dtype] if tied == "lowest" else tied
+    if tied in (-np.inf, "lowest"):
+        x[:] = x[0]
+    x[[V - 1, 70000, 5, 140001]] = [8.0, 7.0, 9.0, 7.0]
+    _check_logprobs(D.store(x[None], dtype), dtype, k, 1.0, 31)
+
+
+# (rows that differ, rows, vocab, type, k, tail, in place, gradient): a workgroup
+# per row, of each size, several rows to a workgroup
+DS_ROW_CASES = [
+    (20, 140, 20001, "bf16", 64, True, False, True),
+    (20, 1300, 20001, "f16", 64, False, True, True),
+    (12, 260, 50021, "f16", 128, True, False, True),
+    (12, 140, 25013, "f32", 20, True, True, True),
+    (12, 700, 50021, "bf16", 30, True, True, True),
+    (6, 300, 100003, "bf16", 128, True, False, True),
+    (6, 300, 50003, "f32", 40, False, False, True),
+    (5, 270, 140001, "bf16", 100, True, True, True),
+    (5, 270, 70001, "f32", 100, True, False, True),
+    (9, 1800, 8185, "bf16", 128, True, False, True),
+    (12, 200, 50021, "bf16", 64, True, False, False),
+    (5, 150, 140001, "f16", 16, True, False, False),
+]
+
+
+@pytest.mark.parametrize("distinct,n,V,dtype,k,tail,inplace,want_grad", DS_ROW_CASES)
+def test_distill_of_many_rows(distinct, n, V, dtype, k, tail, inplace, want_grad):
+    """The same few rows over and over, spread and crowded lists: the first
+    ones against the oracle, the others equal to them bit for bit."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    kinds = [("plain", "peaked", "masked", "spread", "far")[i % 5] for i in range(distinct)]
+    xs = D.rows(kinds, V, dtype, 41)
+    x = D.exact(xs, dtype)
+    ids, lps = D.teacher(x, k, 1.0, 41, True)
+    # crowded lists: ids a multiple of 8192 apart, neighbours, one id over and over
+    step = np.arange(k) * 8192
+    ids[1] = np.where(step < V, step, np.arange(k))
+    ids[2] = V - 1 - np.arange(k)
+    ids[3] = np.where(np.arange(k) % 4 == 0, np.arange(k), 77)
+    weight = np.random.default_rng(42).uniform(0.2, 3.0, distinct).astype(np.float32)
+    weight[4] = 0.0
+    o = O.distill_topk(x, ids, lps, 1.0, tail, weight)
+    b = D.distill_bounds(x, ids, lps, 1.0, tail, weight, o, dtype)
+    take = torch.arange(n, device="cuda") % distinct
+    ld = (V + 7) // 8 * 8                                 # every row starts on 16 bytes
+    view = torch.empty(n, ld, dtype=D.to_torch(xs[:1], dtype).dtype, device="cuda")[:, :V]
+    view.copy_(D.to_torch(xs, dtype)[take])
+    out = {"loss": torch.empty(n, device="cuda")}
+    if want_grad:
+        out["grad"] = view if inplace else torch.empty_strided(view.shape, view.stride(), dtype=view.dtype, device="cuda")
+    P.distill_topk(view, torch.from_numpy(ids).cuda()[take], torch.from_numpy(lps).cuda()[take], tail=tail,
+                   weight=torch.from_numpy(weight).cuda()[take], want_grad=want_grad, out=out)
+    torch.cuda.synchronize()
+    _compare({a: v[:distinct].double().cpu().numpy() for a, v in out.items()}, o, *b,
+             f"{n}x{V} {dtype} k={k} tail={tail} inplace={inplace}")
+    for a, v in out.items():
+        bits = v.contiguous().view(torch.int32 if v.dtype == torch.float32 else torch.int16)
+        assert torch.equal(bits, bits[:distinct][take]), a
+
+
+def test_empty_batches_and_cpu_tensors():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    x = torch.zeros(0, 100, device="cuda")
+    o = P.token_logprobs(x, torch.zeros(0, dtype=torch.int32, device="cuda"), 3)
+    assert o["logprob"].shape == (0,) and o["top_id"].shape == (0, 3)
+    ids, lps = torch.zeros(0, 3, dtype=torch.int32, device="cuda"), torch.zeros(0, 3, device="cuda")
+    o = P.distill_topk(x, ids, lps)
+    assert o["loss"].shape == (0,) and o["grad"].shape == (0, 100)
+    y = torch.zeros(2, 100)
+    with pytest.raises(ValueError):
+        P.token_logprobs(y, None, 3)
+    with pytest.raises(ValueError):
+        P.token_logprobs(y.cuda(), torch.zeros(2, dtype=torch.int32), 3)
+    ids, lps = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    with pytest.raises(ValueError):
+        P.distill_topk(y, ids, lps)
+    with pytest.raises(ValueError):
+        P.distill_topk(y.cuda(), ids.cuda(), lps)
+
+
+def test_buffers_serve_many_calls_and_are_checked_again_when_changed():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    x = torch.randn(6, 5000, device="cuda")
+    t = torch.arange(6, dtype=torch.int32, device="cuda")
+    want = P.token_logprobs(x, t, 4)
+    out, ws = P.token_logprobs_buffers(x, 4)
+    for _ in range(3):
+        P.token_logprobs(x, t, 4, out=out, ws=ws)
+    for a, b in want.items():
+        assert torch.equal(b, out[a]), a
+    out["logprob"] = torch.empty(6, dtype=torch.float64, device="cuda")
+    with pytest.raises(ValueError):
+        P.token_logprobs(x, t, 4, out=out, ws=ws)
+    out["logprob"] = torch.empty(5, device="cuda")
+    with pytest.raises(ValueError):
+        P.token_logprobs(x, t, 4, out=out, ws=ws)
+    out["logprob"] = torch.empty(6, device="cuda")
+    P.token_logprobs(x, t, 4, out=out, ws=ws)
+    assert torch.equal(want["logprob"], out["logprob"])
+    with pytest.raises(ValueError):
+        P.token_logprobs(x[:4], t[:4], 4, out=out, ws=ws)     # buffers of another call
+    ids, lps = want["top_id"], want["top_logprob"]
+    out, ws = P.distill_topk_buffers(x, 4)
+    P.distill_topk(x, ids, lps, out=out, ws=ws)
+    out["grad"] = torch.empty(6, 5000, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError):
+        P.distill_topk(x, ids, lps, out=out, ws=ws)
+
+
+def test_vocabularies_past_the_limit_are_refused():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    V = (1 << 21) + 1
+    x = torch.zeros(1, V, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(P.GptqError):
+        P.token_logprobs(x, None, 1)
+    ids, lps = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, device="cuda")
+    with pytest.raises(P.GptqError):
+        P.distill_topk(x, ids, lps)
+    x = x[:, :1 << 21]
+    x[0, (1 << 21) - 1] = 3.0
+    o = P.token_logprobs(x, None, 1)
+    assert int(o["top_id"]) == (1 << 21) - 1

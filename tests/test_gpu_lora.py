@@ -246,3 +246,55 @@ def test_lora_wrappers_refuse_wrong_tensors():
         P.lora_add(X, A, B, ad, Y=torch.zeros(4, 96, device="cuda").half())
     with pytest.raises(P.GptqError):
         P.lora_add(X, A, B, ad, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+# projections with many outputs, where more than 16 tokens take the kernel that
+# keeps several outputs' tiles: (d_out, d_in, M, g, type, act-order, rank, adapters)
+WIDE_CASES = [
+    (8192, 640, 17, 128, "bf16", False, 16, 3),
+    (8195, 896, 33, 128, "f16", True, 32, 9),
+    (9001, 128, 64, 128, "bf16", False, 64, 20),
+    (24576, 384, 48, 128, "f16", False, 8, 5),
+    (24601, 640, 64, 128, "bf16", True, 16, 64),
+    (25003, 256, 29, 256, "bf16", False, 128, 2),
+]
+
+
+@pytest.mark.parametrize("d_out,d_in,m,g,xdt,act_order,rank,n", WIDE_CASES)
+def test_w4a16_of_many_outputs(d_out, d_in, m, g, xdt, act_order, rank, n):
+    """Against the oracle, and bit for bit what calls over slices of the outputs
+    and over 16 tokens at a time give."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+
+    i = WIDE_CASES.index((d_out, d_in, m, g, xdt, act_order, rank, n))
+    cfg = synth.CONFIGS["up_proj_70b"].scaled(f"w4wide:{i}", 600 + i, d_out=d_out, d_in=d_in, group_size=g, x_dtype=xdt)
+    codes, scales, zeros, perm, g_idx = synth.w4_layer(cfg, act_order, 0)
+    Xs, As, Bs, s = D.adapters(m, d_in, d_out, rank, n, xdt, 9)
+    a = _assign(m, n, "mixed", np.random.default_rng([97, i]))
+    X, A, B = (D.to_torch(t, xdt) for t in (Xs, As, Bs))
+    ad, sd = torch.from_numpy(a).cuda(), torch.from_numpy(s).cuda()
+    cd = torch.from_numpy(codes).cuda()
+    pd = torch.from_numpy(perm).cuda() if perm is not None else None
+    qw = P.pack_int4_permuted(cd, pd) if pd is not None else P.pack(cd, 4)
+    sc, zd = torch.from_numpy(scales.view(np.int16)).cuda(), torch.from_numpy(zeros).cuda()
+    plain = P.w4a16_matmul(X, qw, sc, zd, g, perm=pd)
+    Y = P.w4a16_lora_matmul(X, qw, sc, zd, g, A, B, ad, sd, perm=pd)
+    Xf, Af, Bf = D.exact(Xs, xdt), D.exact(As, xdt), D.exact(Bs, xdt)
+    s32 = scales.view(np.float16).astype(np.float32)
+    base = O.w4a16_matmul(Xf, O.pack_int4(codes), s32, zeros, g_idx)
+    tol = w4a16_error_bound(Xf, codes, s32, zeros, g_idx, bias=128.0 if xdt == "bf16" else 0.0)
+    err = np.abs(plain.double().cpu().numpy() - base)
+    assert np.all(err <= tol), float(np.max(err / tol))
+    want = O.lora(Xf, Af, Bf, a, s, base)
+    tol = tol + D.lora_bound(Xf, Af, Bf, a, s, want, xdt, "f32")
+    err = np.abs(Y.double().cpu().numpy() - want)
+    assert np.all(err <= tol), float(np.max(err / tol))
+    for t in range(0, m, 16):
+        e = min(t + 16, m)
+        x, ids = X[t:e].contiguous(), ad[t:e].contiguous()
+        assert torch.equal(P.w4a16_matmul(x, qw, sc, zd, g, perm=pd), plain[t:e])
+        assert torch.equal(P.w4a16_lora_matmul(x, qw, sc, zd, g, A, B, ids, sd, perm=pd), Y[t:e])
+    for o in range(0, d_out, 4000):
+        e = min(o + 4000, d_out)
+        assert torch.equal(P.w4a16_matmul(X, qw[o:e], sc[o:e], zd[o:e], g, perm=pd), plain[:, o:e])
