@@ -413,7 +413,7 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     M, d_in, ld_x, device = _rows(X, "X")
     dtype = X.dtype
     n, r, d_out, pa, pb, pad, ps = _adapters(A, B, adapter, scale, dtype, M, d_in, device)
-    ng = d_in // group_size
+    ng = d_in // group_size if group_size > 0 else 0
     pq = _dense(qweight, torch.uint8, (d_out, d_in // 2), "qweight", device)
     if scales.dtype is not torch.int16 and scales.dtype is not torch.float16:
         raise ValueError("scales: fp16, or their bits as int16, are needed")
