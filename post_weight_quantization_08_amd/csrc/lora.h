@@ -109,6 +109,46 @@ __device__ __forceinline__ float lora_up_one(const LoraFew& a, int ad, int64_t m
   return s;
 }
 
+// y += the same for tokens m .. m + 3 of their own adapters, its loads asked
+// for together: without a branch, at a token or an adapter that is there, and
+// not used where none acts.
+template <int kDt>
+__device__ __forceinline__ void lora_up_four(const LoraFew& a, int m, int64_t row, f32x4& y) {
+  const int64_t at = row < a.d_out ? row : a.d_out - 1;
+  const uint16_t* b[4];
+  const float* t[4];
+  bool acts[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int tok = m + r < a.M ? m + r : (int)a.M - 1;
+    const int ad = a.adapter[tok];
+    acts[r] = ad >= 0 && ad < a.n;
+    b[r] = a.B + ((int64_t)(acts[r] ? ad : 0) * a.d_out + at) * a.rank;
+    t[r] = a.T + (int64_t)tok * a.rp;
+  }
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < a.rank; k += 8) {
+    u32x4 w[4];
+    f32x4 t0[4], t1[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      w[r] = load8_end(b[r], k, a.rank);
+      t0[r] = *reinterpret_cast<const f32x4*>(t[r] + k);
+      t1[r] = *reinterpret_cast<const f32x4*>(t[r] + k + 4);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = e < 2 ? t0[r][2 * e] : t1[r][2 * e - 4], v = e < 2 ? t0[r][2 * e + 1] : t1[r][2 * e - 3];
+        s[r] = fmaf(k + 2 * e < a.rank ? u : 0.f, lo16<kDt>(w[r][e]), s[r]);
+        s[r] = fmaf(k + 2 * e + 1 < a.rank ? v : 0.f, hi16<kDt>(w[r][e]), s[r]);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) y[r] = acts[r] ? y[r] + s[r] : y[r];
+}
+
 // The 4-bit projection (arguments as gptq_w4a16_matmul's), with adapters when
 // `lora` is given; in w4a16.hip.
 gptq_status w4a16_run(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x, const uint8_t* qweight,

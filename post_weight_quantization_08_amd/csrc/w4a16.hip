@@ -342,66 +342,72 @@ __global__ __launch_bounds__(64 * kW) void w4_main_kernel(W4Args a) {
 }
 
 // ---------------------------------------------------------------- many tokens, many rows
-// For more than 16 tokens and enough rows: four waves of kRT x 16 rows each
-// walk all chunks together, and the chunk's activations come through LDS once
-// for the workgroup (the kernel above reads them for every 16 rows, which for
-// 48 tokens is ten times the codes' traffic).  Chunks arrive through a ring of
-// kRing stages, activations by direct loads into LDS, codes in registers, all
-// kRing - 1 chunks ahead, so that one wait per chunk covers both.  The sums are
-// the ones above bit for bit: the same products in the same order, the chunks
-// of each of the kernel's waves summed apart and added up in the waves' order.
-// A token's 256-byte row of a stage keeps its 16-byte unit u at slot u ^ (token
-// % 16), so that the 16 tokens of a fragment read lie in 16 different slots.
+// For more than a few tokens and enough rows: waves of 16 rows each walk all
+// chunks together, and the chunk's activations come through LDS once for the
+// workgroup (the kernel above reads them for every 16 rows, which for 48 tokens
+// is ten times the codes' traffic).  Chunks arrive through a ring of kW4Ring
+// stages, activations by direct loads into LDS, codes in registers, all
+// kW4Ring - 1 chunks ahead, so that one wait per chunk covers both.  The sums
+// are the ones above bit for bit: the same products in the same order, the
+// chunks of each of the kernel's waves summed apart and added up in the waves'
+// order.  A token's 256-byte row of a stage keeps its 16-byte unit u at slot
+// u ^ (token % 16), so that the 16 tokens of a fragment read lie in 16 slots.
+// One tile a wave and up to eight waves, two to a SIMD, rather than two tiles
+// and four waves, and an adapter's loads asked for without a branch: 95 -> 67 us
+// at 48 tokens of 28672 x 8192 with 32 adapters of rank 16 (117 MB of codes,
+// 2.5 TB/s of all it reads).  Half of a wave's time there is waiting at the
+// stages; LDS is busy 31 % of it, VALU 29, MFMA 13.  Activations laid out chunk
+// by chunk and slots without any bank conflict changed nothing.
 constexpr int kW4Ring = 6;
 
 // bytes of a row's scales and zeros in LDS
 __host__ __device__ constexpr int w4_wide_pitch(int ng) { return (3 * ng + 3) / 4 * 4 + 4; }
 constexpr int kW4WideParams = 40960;    // LDS bytes for them
 
-template <int kDt, int kMT, int kRT, bool kLora>
-__global__ __launch_bounds__(256, 1) void w4_wide_kernel(W4Args a) {
+template <int kDt, int kMT, int kMost, bool kLora>
+__global__ __launch_bounds__(64 * kMost, 1) void w4_wide_kernel(W4Args a) {
   constexpr int kStage = kMT * 16 * 256;
-  constexpr int kOps = kRT + kMT + (kDt == GPTQ_BF16 ? 1 : 0);   // memory operations of a wave per chunk
+  constexpr int kLeast = kMost == 8 ? 6 : kMost;                 // waves of a workgroup: kLeast .. kMost
+  constexpr int kPieces = (4 * kMT + kLeast - 1) / kLeast;       // of four tokens' rows of a stage, loaded by a wave
+  constexpr int kOps = 1 + kPieces + (kDt == GPTQ_BF16 ? 1 : 0);   // memory operations of a wave per chunk
   constexpr int kFly = (kW4Ring - 2) * kOps;
   static_assert(kFly < 64, "counted in six bits");
   constexpr int kWait = (kFly & 0xF) | ((kFly >> 4) << 14) | (7 << 4) | (0xF << 8);
   // one array per stage, so the compiler sees which one a read touches
   __shared__ __attribute__((aligned(1024))) char x0[kStage], x1[kStage], x2[kStage], x3[kStage], x4[kStage], x5[kStage];
-  __shared__ __attribute__((aligned(1024))) float s0[4][64], s1[4][64], s2[4][64], s3[4][64], s4[4][64], s5[4][64];
+  __shared__ __attribute__((aligned(1024))) float s0[kMost][64], s1[kMost][64], s2[kMost][64],
+      s3[kMost][64], s4[kMost][64], s5[kMost][64];
   extern __shared__ __attribute__((aligned(16))) uint8_t w4_lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
-  const int64_t r0 = (int64_t)blockIdx.x * (64 * kRT) + wave * (16 * kRT);
-  const u32x4* wrow[kRT];
+  const int rows = blockDim.x / 4;        // 16 per wave
+  const int64_t row = (int64_t)blockIdx.x * rows + wave * 16 + c16;
+  const u32x4* wrow = a.qw + (row < a.d_out ? row : a.d_out - 1) * (a.K / 32) + q;
+  u32x4 wq[kW4Ring];
+  // this lane's part of a piece: its token lane / 16, slot lane % 16; where the
+  // pieces do not go round, the last one comes from several waves
+  const u32x4* xsrc[kPieces];
+  int piece[kPieces];
 #pragma unroll
-  for (int t = 0; t < kRT; ++t) {
-    const int64_t row = r0 + t * 16 + c16;
-    wrow[t] = a.qw + (row < a.d_out ? row : a.d_out - 1) * (a.K / 32) + q;
-  }
-  u32x4 wq[kW4Ring][kRT];
-  // this lane's part of a stage: token 4 p + lane / 16 of the wave's, slot lane % 16
-  const u32x4* xsrc[kMT];
-#pragma unroll
-  for (int p = 0; p < kMT; ++p) {
-    const int m = wave * 4 * kMT + p * 4 + (lane >> 4);
+  for (int p = 0; p < kPieces; ++p) {
+    piece[p] = min(wave * kPieces + p, 4 * kMT - 1);
+    const int m = piece[p] * 4 + (lane >> 4);
     xsrc[p] = a.Xs + (size_t)m * (a.K / 8) + ((lane & 15) ^ (m & 15));
   }
-  auto fetch = [&](int c, u32x4 (&w)[kRT], char* xr, float (*sr)[64]) {
+  auto fetch = [&](int c, u32x4& w, char* xr, float (*sr)[64]) {
     const int cc = c < a.nchunks ? c : a.nchunks - 1;   // clamped: the same operations every chunk
+    w = wrow[(size_t)cc * 4];
 #pragma unroll
-    for (int t = 0; t < kRT; ++t) w[t] = wrow[t][(size_t)cc * 4];
-#pragma unroll
-    for (int p = 0; p < kMT; ++p)
-      lds_load16(xsrc[p] + (size_t)cc * 16, xr + (wave * 4 * kMT + p * 4) * 256);
+    for (int p = 0; p < kPieces; ++p) lds_load16(xsrc[p] + (size_t)cc * 16, xr + piece[p] * 1024);
     if constexpr (kDt == GPTQ_BF16) lds_load4(a.xsum + (size_t)cc * a.Mp + (lane < a.Mp ? lane : 0), sr[wave]);
   };
   // the rows' scales and zeros, rows padded apart for the banks
   const int pitch = w4_wide_pitch(a.ng);
-  for (int e = threadIdx.x; e < 64 * kRT * a.ng; e += 256) {
+  for (int e = threadIdx.x; e < rows * a.ng; e += blockDim.x) {
     const int rr = e / a.ng, g = e - rr * a.ng;
-    const int64_t row = (int64_t)blockIdx.x * (64 * kRT) + rr;
-    const size_t src = (size_t)(row < a.d_out ? row : a.d_out - 1) * a.ng + g;
+    const int64_t n = (int64_t)blockIdx.x * rows + rr;
+    const size_t src = (size_t)(n < a.d_out ? n : a.d_out - 1) * a.ng + g;
     uint8_t* p = w4_lds + rr * pitch;
     *reinterpret_cast<uint16_t*>(p + 2 * g) = a.scales[src];
     p[2 * a.ng + g] = a.zeros[src];
@@ -412,70 +418,52 @@ __global__ __launch_bounds__(256, 1) void w4_wide_kernel(W4Args a) {
   asm volatile("" : "+v"(magic_v));
   asm volatile("" : "+s"(mask_s));
 
-  f32x4 sum[kRT][kMT], tot[kRT][kMT];
+  f32x4 sum[kMT], tot[kMT];
 #pragma unroll
-  for (int t = 0; t < kRT; ++t)
-#pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) sum[t][mt] = tot[t][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int mt = 0; mt < kMT; ++mt) sum[mt] = tot[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   int part = 0, part_end = a.nchunks / a.parts;
   auto close_part = [&]() {
 #pragma unroll
-    for (int t = 0; t < kRT; ++t)
+    for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sum[t][mt][r] += tot[t][mt][r];
-          tot[t][mt][r] = 0.f;
-        }
+      for (int r = 0; r < 4; ++r) {
+        sum[mt][r] += tot[mt][r];
+        tot[mt][r] = 0.f;
+      }
   };
-  auto multiply = [&](int c, const u32x4 (&w)[kRT], const char* xr, const float (*sr)[64]) {
+  auto multiply = [&](int c, const u32x4& w, const char* xr, const float (*sr)[64]) {
     if (c == part_end) {
       close_part();
       ++part;
       part_end = a.nchunks * (part + 1) / a.parts;
     }
     const int gi = c / a.gch;
-    f32x4 acc[kRT][kMT];
+    f32x4 acc[kMT];
 #pragma unroll
-    for (int t = 0; t < kRT; ++t)
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) acc[t][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float sc[kRT];
-    uint32_t zb[kRT];
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      const uint8_t* p = w4_lds + (wave * 16 * kRT + t * 16 + c16) * pitch;
-      sc[t] = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p + 2 * gi));
-      zb[t] = p[2 * a.ng + gi];
-    }
+    for (int mt = 0; mt < kMT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint8_t* p = w4_lds + (wave * 16 + c16) * pitch;
+    const float sc = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p + 2 * gi));
+    const uint32_t zb = p[2 * a.ng + gi];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 x[kMT];
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
         x[mt] = *reinterpret_cast<const u32x4*>(xr + (mt * 16 + c16) * 256 + (((q * 4 + i) ^ c16) * 16));
+      const u32x4 b = w4_operand<kDt>(w[i], (0xE400u | zb) * 0x00010001u, mask_s, magic_v);
 #pragma unroll
-      for (int t = 0; t < kRT; ++t) {
-        const u32x4 b = w4_operand<kDt>(w[t][i], (0xE400u | zb[t]) * 0x00010001u, mask_s, magic_v);
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) acc[t][mt] = w4_mfma<kDt>(x[mt], b, acc[t][mt]);
-      }
+      for (int mt = 0; mt < kMT; ++mt) acc[mt] = w4_mfma<kDt>(x[mt], b, acc[mt]);
     }
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-      f32x4 xs = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (kDt == GPTQ_BF16) xs = *reinterpret_cast<const f32x4*>(&sr[wave][mt * 16 + 4 * q]);
+      if constexpr (kDt == GPTQ_BF16) {
+        const f32x4 xs = *reinterpret_cast<const f32x4*>(&sr[wave][mt * 16 + 4 * q]);
+        const float zf = -(128.0f + (float)zb);
 #pragma unroll
-      for (int t = 0; t < kRT; ++t) {
-        if constexpr (kDt == GPTQ_BF16) {
-          const float zf = -(128.0f + (float)zb[t]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[t][mt][r] = fmaf(zf, xs[r], acc[t][mt][r]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) tot[t][mt][r] = fmaf(sc[t], acc[t][mt][r], tot[t][mt][r]);
+        for (int r = 0; r < 4; ++r) acc[mt][r] = fmaf(zf, xs[r], acc[mt][r]);
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) tot[mt][r] = fmaf(sc, acc[mt][r], tot[mt][r]);
     }
   };
   fetch(0, wq[0], x0, s0);
@@ -503,30 +491,13 @@ __global__ __launch_bounds__(256, 1) void w4_wide_kernel(W4Args a) {
   close_part();
 #pragma unroll
   for (int mt = 0; mt < kMT; ++mt) {
-    int ad[4] = {-1, -1, -1, -1};
-    if constexpr (kLora) {
+    f32x4 y = sum[mt];
+    if constexpr (kLora) lora_up_four<kDt>(a.lora, mt * 16 + 4 * q, row, y);
+    if (row >= a.d_out) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = mt * 16 + 4 * q + r;
-        if (tok < a.M) ad[r] = a.lora.adapter[tok];
-        if (ad[r] >= a.lora.n) ad[r] = -1;
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      const int64_t row = r0 + t * 16 + c16;
-      if (row >= a.d_out) continue;
-      f32x4 y = sum[t][mt];
-      if constexpr (kLora) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (ad[r] >= 0) y[r] += lora_up_one<kDt>(a.lora, ad[r], mt * 16 + 4 * q + r, row);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = mt * 16 + 4 * q + r;
-        if (tok < a.M) a.Y[(size_t)tok * a.ld_y + row] = y[r];
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int tok = mt * 16 + 4 * q + r;
+      if (tok < a.M) a.Y[(size_t)tok * a.ld_y + row] = y[r];
     }
   }
 }
@@ -572,31 +543,46 @@ static void launch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
   }
 }
 
-// Row tiles per wave of the wide kernel, 0 for the other one: it needs more
-// than one token tile, and rows for most of the CUs (one workgroup each).
-static int w4_wide_tiles(int64_t M, int64_t d_out, int ng) {
-  if (M <= 16) return 0;
-  if (d_out >= 192 * 128 && 128 * w4_wide_pitch(ng) <= kW4WideParams) return 2;
-  if (d_out >= 128 * 64 && 64 * w4_wide_pitch(ng) <= kW4WideParams) return 1;
-  return 0;
+// Waves per workgroup of the wide kernel, 0 for the other one.  Four to eight,
+// as many as make the fewest rounds over 256 CUs, weighed by the waves (28672
+// rows: 8 leave 32 CUs idle, 7 none: 57 -> 53 us at 48 tokens).  With up to 16
+// tokens it is taken where at least 192 CUs get four waves: 28672 x 8192, 16
+// tokens, 42 us and 73 in the other kernel, 14336 x 4096 19 and 25, but 8192 x
+// 8192 31 and 26; up to 4 tokens the other kernel keeps the activations in LDS.
+static int w4_wide_waves(int64_t M, int64_t d_out, int ng) {
+  if (M <= 4 || d_out < (M <= 16 ? 192 * 64 : 128 * 64)) return 0;
+  const int64_t tiles = cdiv(d_out, 16);
+  int best = 0;
+  int64_t cost = 0;
+  for (int w = 8; w >= 4; --w) {
+    if (16 * w * w4_wide_pitch(ng) > kW4WideParams) continue;
+    const int64_t c = cdiv(cdiv(tiles, w), 256) * w;
+    if (best == 0 || c < cost) {
+      best = w;
+      cost = c;
+    }
+  }
+  return best;
 }
 
 template <int kDt, int kMT, bool kLora>
-static void launch_w4_wide(const W4Args& a, int tiles, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(a.d_out, 64 * tiles));
-  const size_t lds = (size_t)64 * tiles * w4_wide_pitch(a.ng);
-  if (tiles == 2) hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 2, kLora>), grid, dim3(256), lds, st, a);
-  else hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 1, kLora>), grid, dim3(256), lds, st, a);
+static void launch_w4_wide(const W4Args& a, int waves, hipStream_t st) {
+  const dim3 grid((unsigned)cdiv(a.d_out, 16 * waves)), block(64 * waves);
+  const size_t lds = (size_t)16 * waves * w4_wide_pitch(a.ng);
+  if (waves >= 6) hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 8, kLora>), grid, block, lds, st, a);
+  else if (waves == 5) hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 5, kLora>), grid, block, lds, st, a);
+  else hipLaunchKernelGGL((w4_wide_kernel<kDt, kMT, 4, kLora>), grid, block, lds, st, a);
 }
 
 template <int kDt, bool kLora>
 static void dispatch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
-  const int tiles = w4_wide_tiles(a.M, a.d_out, a.ng);
+  const int waves = w4_wide_waves(a.M, a.d_out, a.ng);
   const int mt = pl.Mp / 16;
-  if (tiles > 0) {
-    if (a.M <= 32) launch_w4_wide<kDt, 2, kLora>(a, tiles, st);
-    else if (a.M <= 48) launch_w4_wide<kDt, 3, kLora>(a, tiles, st);
-    else launch_w4_wide<kDt, 4, kLora>(a, tiles, st);
+  if (waves > 0) {
+    if (a.M <= 16) launch_w4_wide<kDt, 1, kLora>(a, waves, st);
+    else if (a.M <= 32) launch_w4_wide<kDt, 2, kLora>(a, waves, st);
+    else if (a.M <= 48) launch_w4_wide<kDt, 3, kLora>(a, waves, st);
+    else launch_w4_wide<kDt, 4, kLora>(a, waves, st);
   } else if (w4_lx(a.M, a.K, a.ng, pl.nchunks, pl.W)) {
     launch_w4<kDt, 1, 8, true, kLora>(a, pl, st);
   } else if (mt == 1) {
