@@ -298,3 +298,51 @@ def test_w4a16_of_many_outputs(d_out, d_in, m, g, xdt, act_order, rank, n):
     for o in range(0, d_out, 4000):
         e = min(o + 4000, d_out)
         assert torch.equal(P.w4a16_matmul(X, qw[o:e], sc[o:e], zd[o:e], g, perm=pd), plain[:, o:e])
+
+
+@pytest.mark.parametrize("base", ["none", "inplace", "given"])
+@pytest.mark.parametrize("pad,off", [(0, 0), (8, 0), (3, 1), (0, 5)])
+def test_lora_bases_strides_and_starts_of_prompts(base, pad, off):
+    _check(190, 640, 328, 16, 4, "f16", "f16", "mixed", base=base, pad=pad, off=off)
+    _check(190, 640, 328, 16, 4, "bf16", "f32", "runs", base=base, pad=pad, off=off, scaled=False)
+
+
+def test_lora_of_prompts_keeps_broken_adapters_apart():
+    """Factors at any address; NaN in rows without an adapter, in unused adapters, in neighbours."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    M = 161
+    Xs, As, Bs, s = D.adapters(M, 256, 192, 16, 4, "bf16", 15)
+    X, A, B = (D.to_torch(t, "bf16") for t in (Xs, As, Bs))
+    a = np.where(np.arange(M) % 3 == 1, -1, np.arange(M) % 3).astype(np.int32)
+    ad, sd = torch.from_numpy(a).cuda(), torch.from_numpy(s).cuda()
+    clean = P.lora_add(X, A, B, ad, sd)
+    Xf, Af, Bf = D.exact(Xs, "bf16"), D.exact(As, "bf16"), D.exact(Bs, "bf16")
+    want = O.lora(Xf, Af, Bf, a, s)
+    tol = D.lora_bound(Xf, Af, Bf, a, s, want, "bf16", "f32")
+
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:].copy_(t.flatten())
+        return buf[1:].view(t.shape)
+    for args in ((X, A, B), (X, shifted(A), B), (X, A, shifted(B)), (X, shifted(A), shifted(B))):
+        assert np.all(np.abs(P.lora_add(*args, ad, sd).double().cpu().numpy() - want) <= tol)
+    X2, A2, B2 = X.clone(), A.clone(), B.clone()
+    X2[1::3] = float("nan")
+    A2[3], B2[3] = float("nan"), float("inf")
+    A2[1], B2[1] = float("inf"), float("nan")
+    assert torch.equal(clean, P.lora_add(X2, A2, B2, ad, sd))
+    X2[0] = float("inf")
+    got = P.lora_add(X2, A, B, ad, sd)
+    assert torch.equal(clean[1:], got[1:]) and not torch.isfinite(got[0]).all()
+    A2 = A.clone()
+    A2[2] = float("nan")                                  # one adapter broken: its rows alone
+    got = P.lora_add(X, A2, B, ad, sd)
+    keep = torch.from_numpy(a != 2).cuda()
+    assert torch.equal(clean[keep], got[keep]) and torch.isnan(got[~keep]).all()
+
+
+def test_lora_of_prompts_past_4_gib():
+    import torch
+    _check(140, 256, 200, 16, 3, "f16", "f16", "runs", base="inplace", pad=(1 << 24) + 8)
+    torch.cuda.empty_cache()
