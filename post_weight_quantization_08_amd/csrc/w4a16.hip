@@ -545,12 +545,15 @@ static void launch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
 
 // Waves per workgroup of the wide kernel, 0 for the other one.  Four to eight,
 // as many as make the fewest rounds over 256 CUs, weighed by the waves (28672
-// rows: 8 leave 32 CUs idle, 7 none: 57 -> 53 us at 48 tokens).  With up to 16
-// tokens it is taken where at least 192 CUs get four waves: 28672 x 8192, 16
-// tokens, 42 us and 73 in the other kernel, 14336 x 4096 19 and 25, but 8192 x
-// 8192 31 and 26; up to 4 tokens the other kernel keeps the activations in LDS.
+// rows: 8 leave 32 CUs idle, 7 none: 57 -> 53 us at 48 tokens).  Its time hardly
+// depends on the tokens of a tile, the other kernel's does; where they cross
+// depends on the rows too.  Here / the other kernel, us: 28672 x 8192, 5, 16 and
+// 64 tokens 43 / 49, 43 / 74, 69 / 238; 14336 x 4096, 5, 8 and 16 tokens 20.7 /
+// 18.9, 20.8 / 21.5, 21 / 27; 8192 x 8192, 16, 17 and 32 tokens 34 / 29, 39 / 35,
+// 39 / 46.  Up to 4 tokens the other kernel keeps the activations in LDS.
 static int w4_wide_waves(int64_t M, int64_t d_out, int ng) {
   if (M <= 4 || d_out < (M <= 16 ? 192 * 64 : 128 * 64)) return 0;
+  if (M * d_out < (M <= 16 ? 8 * 192 * 64 : 22 * 128 * 64)) return 0;
   const int64_t tiles = cdiv(d_out, 16);
   int best = 0;
   int64_t cost = 0;

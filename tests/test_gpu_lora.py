@@ -259,6 +259,14 @@ WIDE_CASES = [
     (25003, 256, 29, 256, "bf16", False, 128, 2),
 ]
 
+# and with fewer tokens where there are still more outputs
+WIDE_CASES += [
+    (12288, 640, 8, 128, "bf16", True, 16, 3),
+    (20011, 384, 5, 128, "f16", False, 8, 5),
+    (14001, 1280, 13, 128, "bf16", False, 33, 13),
+    (28672, 256, 16, 256, "f16", True, 128, 4),
+]
+
 
 @pytest.mark.parametrize("d_out,d_in,m,g,xdt,act_order,rank,n", WIDE_CASES)
 def test_w4a16_of_many_outputs(d_out, d_in, m, g, xdt, act_order, rank, n):
