@@ -13,11 +13,12 @@
 // one pass per adapter that occurs in it; a request's tokens lie together, so
 // most tiles need one.  Rows of another adapter are left out of a pass by
 // selecting, never by multiplying with zero: a NaN or infinity in one adapter
-// does not reach another's rows.  For the second product T is kept as two
-// 16-bit terms, whose sum carries 16 significant bits (bf16) or 22 (fp16; rows
-// of T are scaled by a power of two first, so that neither their size nor
-// their smallness leaves fp16's range): 16 bits alone would put an error of
-// 2^-9 or 2^-12 of the adapter's part into fp32 results.  The second product's
+// does not reach another's rows.  For the second product T is kept as 16-bit
+// terms: two of fp16, 22 significant bits (rows of T are scaled by a power of
+// two first, so that neither their size nor their smallness leaves fp16's
+// range); of bf16 three for fp32 results, 24 bits, and two, 16 bits, for bf16
+// results, whose own rounding is 2^-9.  Two would put 2^-17 of the adapter's
+// part into fp32 results, three times what fp32 sums do.  The second product's
 // columns are dealt to the MFMA tiles so that a lane ends up with four
 // consecutive outputs and sixteen lanes with 64: base and Y move in pieces of
 // 256 (fp32) or 128 bytes, at any alignment.
@@ -362,27 +363,29 @@ __global__ __launch_bounds__(256) void lora_down_lds_kernel(LoraArgs a) {
   });
 }
 
-// hi and lo terms of 8 values, as MFMA operands.
-template <int kDt>
-__device__ __forceinline__ void lora_split(const float (&v)[8], u32x4& hi, u32x4& lo) {
+// 16-bit terms of 8 values, the largest first, as MFMA operands.
+template <int kDt, int kTerms>
+__device__ __forceinline__ void lora_split(const float (&v)[8], u32x4 (&out)[kTerms]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t h[2], l[2];
+    float x[2] = {v[2 * i], v[2 * i + 1]};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = v[2 * i + e];
-      if constexpr (kDt == GPTQ_F16) {
-        const _Float16 p = (_Float16)x, r = (_Float16)(x - (float)p);
-        h[e] = __builtin_bit_cast(uint16_t, p);
-        l[e] = __builtin_bit_cast(uint16_t, r);
-      } else {
-        const __bf16 p = (__bf16)x, r = (__bf16)(x - (float)p);
-        h[e] = __builtin_bit_cast(uint16_t, p);
-        l[e] = __builtin_bit_cast(uint16_t, r);
+    for (int k = 0; k < kTerms; ++k) {
+      uint32_t h[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (kDt == GPTQ_F16) {
+          const _Float16 p = (_Float16)x[e];
+          h[e] = __builtin_bit_cast(uint16_t, p);
+          x[e] -= (float)p;
+        } else {
+          const __bf16 p = (__bf16)x[e];
+          h[e] = __builtin_bit_cast(uint16_t, p);
+          x[e] -= (float)p;
+        }
       }
+      out[k][i] = h[0] | h[1] << 16;
     }
-    hi[i] = h[0] | h[1] << 16;
-    lo[i] = l[0] | l[1] << 16;
   }
 }
 
@@ -391,7 +394,8 @@ template <int kDt, int kY, int kS>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   constexpr int kPitch = kS * 32 + 4;
   __shared__ __align__(16) float tsum[kLoraTile][kPitch];
-  __shared__ u32x4 terms[2][kS][2][64];    // [token tile][rank step][first, second term][lane]
+  constexpr int kTerms = kDt == GPTQ_BF16 && kY == GPTQ_F32 ? 3 : 2;
+  __shared__ u32x4 terms[2][kS][kTerms][64];   // [token tile][rank step][term][lane]
   __shared__ __align__(16) float grow[kLoraTile];   // 2^e that a token's terms were divided by
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
@@ -487,10 +491,10 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
     if (q == 0) grow[t * 16 + c16] = g;
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
-      u32x4 hi, lo;
-      lora_split<kDt>(v[s], hi, lo);
-      terms[t][s][0][lane] = hi;
-      terms[t][s][1][lane] = lo;
+      u32x4 term[kTerms];
+      lora_split<kDt>(v[s], term);
+#pragma unroll
+      for (int k = 0; k < kTerms; ++k) terms[t][s][k][lane] = term[k];
     }
   }
   __syncthreads();
@@ -520,10 +524,9 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       auto pass = [&](int ad, int e, const u32x4 (&w)[kS]) {
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < kS; ++s) {
-          d = lora_mfma<kDt>(terms[t][s][1][lane], w[s], d);
-          d = lora_mfma<kDt>(terms[t][s][0][lane], w[s], d);
-        }
+        for (int s = 0; s < kS; ++s)
+#pragma unroll
+          for (int k = kTerms - 1; k >= 0; --k) d = lora_mfma<kDt>(terms[t][s][k][lane], w[s], d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[e][i] = own[i] == ad ? d[i] : acc[e][i];
       };

@@ -354,3 +354,20 @@ def test_lora_of_prompts_past_4_gib():
     import torch
     _check(140, 256, 200, 16, 3, "f16", "f16", "runs", base="inplace", pad=(1 << 24) + 8)
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("xdt", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [40, 200])
+def test_fp32_outputs_are_fp32_sums(xdt, m):
+    """In norm, products of 1024 and 64 terms summed in fp32 err by some 2^-24 times the root of the additions in a
+    row (at most 32): 2^-20 leaves a factor of three, and a T of 16 bits (2^-18 of it at worst) does not pass."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    Xs, As, Bs, s = D.adapters(m, 1024, 500, 64, 3, xdt, 21)
+    X, A, B = (D.to_torch(t, xdt) for t in (Xs, As, Bs))
+    a = (np.arange(m) * 3 // m).astype(np.int32)
+    got = P.lora_add(X, A, B, torch.from_numpy(a).cuda(), torch.from_numpy(s).cuda()).double().cpu().numpy()
+    want = O.lora(D.exact(Xs, xdt), D.exact(As, xdt), D.exact(Bs, xdt), a, s)
+    error = np.linalg.norm(got - want) / np.linalg.norm(want)
+    log(f"[gpu] lora {m} {xdt}/f32: error in norm {error:.2e}")
+    assert error <= 2.0 ** -20
