@@ -412,6 +412,10 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, int64_t n_r
  *     max(0, 1 - sum p_i) and q_r = sum of q outside K:
  *       loss = sum_i p_i (l_i - log q_i) + p_r (log p_r - log q_r)
  *       dloss/dx_j = (q_j - p_j) / T in K, q_j (1 - p_r / q_r) / T outside.
+ *     A p_r of at most 2^-19 + 2^-22 sum_i p_i |l_i| may be nothing but the
+ *     rounding of a complete list's l_i: it counts as 0 where q_r is smaller
+ *     still (constrained rows, lists of the whole vocabulary: the loss is then
+ *     that of the listed tokens, and it does not jump where this sets in).
  *   tail = 0: p = softmax of the listed l_i (so l may be raw logits / T):
  *       loss = sum_i p_i (log p_i - log q_i)
  *       dloss/dx_j = (q_j - p_j) / T, p_j = 0 outside K.

@@ -89,8 +89,12 @@ def distill_topk(logits: np.ndarray, top_id: np.ndarray, top_logprob: np.ndarray
                 zr = z[~inside]
                 mr = zr.max() if zr.size else -np.inf
                 sr = np.exp(zr - mr).sum() if mr > -np.inf else 0.0
+                lqr = (mr - m) + np.log(sr) - log_s if sr > 0 else -np.inf
+                # the rounding of a complete list's log probabilities is no mass that the student lacks
+                if pr <= 2.0 ** -19 + 2.0 ** -22 * np.where(p > 0, p * np.abs(lps), 0.0).sum() and np.exp(lqr) < pr:
+                    pr = 0.0
                 if pr > 0:
-                    total += pr * (np.log(pr) - ((mr - m) + np.log(sr) - log_s if sr > 0 else -np.inf))
+                    total += pr * (np.log(pr) - lqr)
                 # q_j (1 - p_r / q_r) = q_j - p_r softmax over the tail
                 if mr > -np.inf:
                     g[~inside] -= pr * np.exp(zr - mr) / sr

@@ -5,7 +5,9 @@
 // the listed ones (at most 128) give their own maximum and sum.  Joined, with
 // m the larger reference and S = s 2^((r - m) c) + s_K 2^((m_K - m) c):
 //   log q_k = (x_k - m) / T - ln S,   log q_r = (r - m) / T + ln s - ln S,
-// so the tail's mass is never the difference of nearly equal sums, and
+// so the student's mass in the tail is never the difference of nearly equal
+// sums (the teacher's is 1 less its list's: below the rounding of the listed
+// log probabilities it counts as far as the student's reaches), and
 //   gradient in the rest = w / T 2^((x - r) c) (2^((r - m) c) / S - p_r / s)
 //   gradient in K        = w / T (2^((x - m) c) / S - p_k).
 //
@@ -59,6 +61,7 @@ struct DsArgs {
 struct DsList {
   float m, s;              // maximum of x, sum of 2^((x - m) c)
   float mass, norm;        // sum of p before (tail) / 1 after normalization; p = e^(l - norm)
+  float left;              // 1 - sum p (0 without a tail); negative: it may be nothing but the rounding of the l
   double gap;              // sum p (log p - (x - m) / T)
   float count;
 };
@@ -342,9 +345,18 @@ struct DsRow {
     const float lm = a.tail ? 0.f : wave_reduce(fmaxf(l[0], l[1]), fmax2);
 #pragma unroll
     for (int i = 0; i < 2; ++i) p[i] = has[i] ? exp2_hw((l[i] - lm) * kLog2e) : 0.f;
-    d.mass = wave_reduce(p[0] + p[1], add2);
+    // in 64 bits: what is left of 1 may be as small as the rounding of the l
+    const double sum = wave_reduce((double)p[0] + (double)p[1], [](double q, double w) { return q + w; });
+    d.mass = (float)sum;
     d.norm = 0.f;
-    if (!a.tail) {
+    d.left = 0.f;
+    if (a.tail) {
+      // The l of a complete list share the rounding of a log-sum below 16 (a few
+      // steps of 2^-21, up to 2^-19) and carry a few of their own, 2^-24 |l| each.
+      const float size = wave_reduce((p[0] > 0.f ? p[0] * fabsf(l[0]) : 0.f) + (p[1] > 0.f ? p[1] * fabsf(l[1]) : 0.f), add2);
+      const float left = (float)fmax(1.0 - sum, 0.0);
+      d.left = left > 0x1p-19f + 0x1p-22f * size ? left : -left;
+    } else {
       d.norm = lm + logf(d.mass);
       p[0] /= d.mass;
       p[1] /= d.mass;
@@ -393,9 +405,11 @@ __device__ __forceinline__ DsFinal ds_final(const DsArgs& a, float weight, const
   const float up = s > 0.f ? exp2_hw((r - f.m) * a.c) : 0.f;
   const float total = (l.s > 0.f || l.s != l.s ? l.s * exp2_hw((l.m - f.m) * a.c) : 0.f) + (s != s ? s : s * up);
   const bool bad = !(total > 0.f && total < INFINITY);
-  const float pr = a.tail ? fmaxf(1.f - l.mass, 0.f) : 0.f;
   f.total = total;
   f.tail_q = s * up / total;
+  // Rounding is no mass that the student lacks: it counts only where the
+  // student's tail is as large.  p_r log(p_r / q_r) is 0 where that ends.
+  const float pr = l.left >= 0.f || f.tail_q >= -l.left ? fabsf(l.left) : 0.f;
   f.pr = pr;
   f.bad = bad;
   f.w = weight * a.inv_t;
@@ -747,6 +761,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
         o[2] = l.mass;
         o[3] = l.norm;
         o[4] = l.count;
+        o[5] = l.left;
         *reinterpret_cast<double*>(o + 6) = l.gap;
       }
     }
@@ -785,7 +800,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     }
     ds_join(r, s, a.c, sh);
     const float* o = a.ws_list + row * 8;
-    const DsList list{o[0], o[1], o[2], o[3], *reinterpret_cast<const double*>(o + 6), o[4]};
+    const DsList list{o[0], o[1], o[2], o[3], o[5], *reinterpret_cast<const double*>(o + 6), o[4]};
     const DsFinal f = ds_final(a, a.weight ? a.weight[row] : 1.f, list, r, s);
     if (part == 0 && t == 0 && a.loss) a.loss[row] = ds_loss(a, list, f, r, s);
     if (!a.grad) return;
