@@ -15,6 +15,24 @@ __device__ __forceinline__ float load_el(const void* p, int64_t i) {
   else return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
+// An element's bits as they are, and their value.
+template <int kDt>
+__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t i) {
+  if constexpr (kDt == GPTQ_F32) return static_cast<const uint32_t*>(p)[i];
+  else return static_cast<const uint16_t*>(p)[i];
+}
+template <int kDt>
+__device__ __forceinline__ float bits_value(uint32_t b) {
+  if constexpr (kDt == GPTQ_F32) return __uint_as_float(b);
+  else if constexpr (kDt == GPTQ_BF16) return bf16_bits_to_f32(b);
+  else return f16_bits_to_f32(b);
+}
+template <int kDt>
+__device__ __forceinline__ void store_bits(void* p, int64_t i, uint32_t b) {
+  if constexpr (kDt == GPTQ_F32) static_cast<uint32_t*>(p)[i] = b;
+  else static_cast<uint16_t*>(p)[i] = (uint16_t)b;
+}
+
 // Rounded once, to nearest even; NaN stays NaN.
 template <int kDt>
 __device__ __forceinline__ void store_el(void* p, int64_t i, float v) {

@@ -186,21 +186,8 @@ __device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T,
   s = uniform(row_reduce(mine, add2));
 }
 
-// A logit's bits as loaded, and its value.  What is read ahead stays in this
-// form: looking at it would wait for it, and for everything loaded before.
-template <int kDt>
-__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t i) {
-  if constexpr (kDt == GPTQ_F32) return static_cast<const uint32_t*>(p)[i];
-  else return static_cast<const uint16_t*>(p)[i];
-}
-template <int kDt>
-__device__ __forceinline__ float bits_value(uint32_t b) {
-  if constexpr (kDt == GPTQ_F32) return __uint_as_float(b);
-  else if constexpr (kDt == GPTQ_BF16) return bf16_bits_to_f32(b);
-  else return f16_bits_to_f32(b);
-}
-
-// A thread's list entry of a row as read from memory.
+// A thread's list entry of a row as read from memory.  Its logit stays as
+// loaded: looking at it would wait for it, and for everything loaded before.
 struct DsEntry {
   int id;
   float lp;

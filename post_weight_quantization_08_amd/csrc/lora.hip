@@ -75,9 +75,13 @@ __global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a) {
   const int64_t n0 = (int64_t)blockIdx.x * 256 + (threadIdx.x & ~63);
   const int ad = __builtin_amdgcn_readfirstlane(a.adapter[m]);
   const int64_t n = n0 + lane;
-  float y = 0.f;
-  if (a.base && n < a.d_out) y = load_el<kY>(a.base, m * a.ld_b + n);
-  if (ad >= 0 && ad < a.n && n0 < a.d_out) {
+  const uint32_t base = a.base && n < a.d_out ? load_bits<kY>(a.base, m * a.ld_b + n) : 0u;
+  if (ad < 0 || ad >= a.n) {
+    if (n < a.d_out) store_bits<kY>(a.Y, m * a.ld_y + n, base);   // the base as it is
+    return;
+  }
+  float y = bits_value<kY>(base);
+  if (n0 < a.d_out) {
     const int k = lane % kL * 8;
     u32x4 b[kL];
 #pragma unroll
@@ -507,7 +511,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       const int64_t m = m0 + t * 16 + 4 * q;   // this lane's four tokens
-      Four in[4];
+      Four in[4] = {};
       if (a.base && whole) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -547,6 +551,19 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (m + i >= a.M) continue;
+        if (own[i] < 0) {                  // the base as it is
+          if (whole) {
+            char* o = static_cast<char*>(a.Y) + ((m + i) * a.ld_y + col) * kYE;
+            __builtin_memcpy(__builtin_assume_aligned(o, kYE), &in[i], sizeof(Four));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < a.d_out)
+                store_bits<kY>(a.Y, (m + i) * a.ld_y + col + e,
+                               a.base ? load_bits<kY>(a.base, (m + i) * a.ld_b + col + e) : 0u);
+          }
+          continue;
+        }
         float y[4] = {0.f, 0.f, 0.f, 0.f};
         if (a.base) {
           if (whole) {
