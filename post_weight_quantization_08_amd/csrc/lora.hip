@@ -367,7 +367,8 @@ __global__ __launch_bounds__(256) void lora_down_lds_kernel(LoraArgs a) {
   });
 }
 
-// 16-bit terms of 8 values, the largest first, as MFMA operands.
+// 16-bit terms of 8 values, the largest first, as MFMA operands.  The first
+// one of an infinity is all of it.
 template <int kDt, int kTerms>
 __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4 (&out)[kTerms]) {
 #pragma unroll
@@ -381,11 +382,11 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4 (&out)[kTe
         if constexpr (kDt == GPTQ_F16) {
           const _Float16 p = (_Float16)x[e];
           h[e] = __builtin_bit_cast(uint16_t, p);
-          x[e] -= (float)p;
+          x[e] = fabsf(x[e]) == INFINITY ? 0.f : x[e] - (float)p;
         } else {
           const __bf16 p = (__bf16)x[e];
           h[e] = __builtin_bit_cast(uint16_t, p);
-          x[e] -= (float)p;
+          x[e] = fabsf(x[e]) == INFINITY ? 0.f : x[e] - (float)p;
         }
       }
       out[k][i] = h[0] | h[1] << 16;
@@ -475,14 +476,14 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[s][4 * h + i] = u[i];
-          big = fmaxf(big, fabsf(u[i]));
+          big = fmaxf(big, fabsf(u[i]) < INFINITY ? fabsf(u[i]) : 0.f);
         }
       }
     float g = 1.f;
     if constexpr (kDt == GPTQ_F16) {
       big = fmaxf(big, __shfl_xor(big, 16));
       big = fmaxf(big, __shfl_xor(big, 32));
-      if (big > 0.f && big < INFINITY) {
+      if (big > 0.f) {
         int e;
         frexpf(big, &e);
         g = ldexpf(1.f, e - 14);   // the largest below 2^14: the second terms stay normal numbers
