@@ -467,9 +467,10 @@ gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, int64_t n_row
  *             stride ld_y.
  *   workspace GPTQ_OP_LORA bytes, 256-byte aligned; calls sharing one
  *             workspace must be stream-ordered.
- * fp32 accumulation; X A^T is kept in fp32 and enters the second product as
- * 16-bit terms (24 significant bits in bf16 with fp32 Y, 16 with bf16 Y, 22 in
- * fp16); Y is rounded once.  Any mix of adapters is right; rows of one adapter next to each other
+ * fp32 accumulation; X A^T keeps fp32's 24 significant bits in the second
+ * product (in prompts as 16-bit terms: in fp16 what is below 2^-38 of a token's
+ * largest is lost, and an infinity in B may give NaN); Y is rounded once.  Any
+ * mix of adapters is right; rows of one adapter next to each other
  * (a request's prompt) share its factors.  M = 0 does nothing. */
 gptq_status gptq_lora_add(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x, const void* A,
                           const void* B, int64_t n_adapters, int32_t rank, const float* scale,

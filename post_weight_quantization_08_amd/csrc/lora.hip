@@ -13,15 +13,13 @@
 // one pass per adapter that occurs in it; a request's tokens lie together, so
 // most tiles need one.  Rows of another adapter are left out of a pass by
 // selecting, never by multiplying with zero: a NaN or infinity in one adapter
-// does not reach another's rows.  For the second product T is kept as 16-bit
-// terms: two of fp16, 22 significant bits (rows of T are scaled by a power of
-// two first, so that neither their size nor their smallness leaves fp16's
-// range); of bf16 three for fp32 results, 24 bits, and two, 16 bits, for bf16
-// results, whose own rounding is 2^-9.  Two would put 2^-17 of the adapter's
-// part into fp32 results, three times what fp32 sums do.  The second product's
-// columns are dealt to the MFMA tiles so that a lane ends up with four
-// consecutive outputs and sixteen lanes with 64: base and Y move in pieces of
-// 256 (fp32) or 128 bytes, at any alignment.
+// does not reach another's rows.  For the second product T is kept as three
+// 16-bit terms, which hold all of an fp32: cut off after 8 bits each for bf16;
+// rounded for fp16, after rows of T were scaled by a power of two, so that
+// neither their size nor their smallness leaves fp16's range.  Two terms (16 and
+// 22 bits) take as long.  The second product's columns are dealt to the MFMA
+// tiles so that a lane ends up with four consecutive outputs and sixteen lanes
+// with 64: base and Y move in pieces of 256 (fp32) or 128 bytes, at any alignment.
 //
 // Bound by memory: X, base and Y once, the factors from L2 (a factor's matrix
 // serves every tile of its adapter).  8192 x 11008 -> 4096, rank 64, fp32 base in
@@ -369,7 +367,8 @@ __global__ __launch_bounds__(256) void lora_down_lds_kernel(LoraArgs a) {
 
 // 16-bit terms of 8 values, the largest first, as MFMA operands.  The first
 // one of an infinity is all of it.
-template <int kDt, int kTerms>
+constexpr int kTerms = 3;
+template <int kDt>
 __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4 (&out)[kTerms]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -384,9 +383,10 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4 (&out)[kTe
           h[e] = __builtin_bit_cast(uint16_t, p);
           x[e] = fabsf(x[e]) == INFINITY ? 0.f : x[e] - (float)p;
         } else {
-          const __bf16 p = (__bf16)x[e];
-          h[e] = __builtin_bit_cast(uint16_t, p);
-          x[e] = fabsf(x[e]) == INFINITY ? 0.f : x[e] - (float)p;
+          // a NaN made by arithmetic stays one: its highest mantissa bit is set
+          const uint32_t p = __float_as_uint(x[e]) & 0xFFFF0000u;
+          h[e] = p >> 16;
+          x[e] = fabsf(x[e]) == INFINITY ? 0.f : x[e] - __uint_as_float(p);
         }
       }
       out[k][i] = h[0] | h[1] << 16;
@@ -399,7 +399,6 @@ template <int kDt, int kY, int kS>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   constexpr int kPitch = kS * 32 + 4;
   __shared__ __align__(16) float tsum[kLoraTile][kPitch];
-  constexpr int kTerms = kDt == GPTQ_BF16 && kY == GPTQ_F32 ? 3 : 2;
   __shared__ u32x4 terms[2][kS][kTerms][64];   // [token tile][rank step][term][lane]
   __shared__ __align__(16) float grow[kLoraTile];   // 2^e that a token's terms were divided by
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -486,7 +485,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       if (big > 0.f) {
         int e;
         frexpf(big, &e);
-        g = ldexpf(1.f, e - 14);   // the largest below 2^14: the second terms stay normal numbers
+        g = ldexpf(1.f, e - 14);   // the largest below 2^14: its third term is above 2^-24, the least fp16
 #pragma unroll
         for (int s = 0; s < kS; ++s)
 #pragma unroll
