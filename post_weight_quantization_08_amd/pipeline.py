@@ -259,15 +259,18 @@ class Buffers(dict):
     __delitem__ = pop = popitem = clear = update = setdefault = __ior__ = _changed
 
 
-def token_logprobs_buffers(logits: torch.Tensor, k: int = 0):
-    """(out, ws) of token_logprobs calls with these sizes, to be kept from call to call."""
-    n, v = logits.shape
-    dev = logits.device
+def _logprobs_out(n: int, k: int, dev) -> Buffers:
     out = {name: torch.empty(n, dtype=torch.float32, device=dev) for name in ("logprob", "lse", "entropy")}
     out["top_logprob"] = torch.empty(n, k, dtype=torch.float32, device=dev)
     out["top_id"] = torch.empty(n, k, dtype=torch.int32, device=dev)
-    return (Buffers(("logprobs", n, k, logits.get_device()), out),
-            _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), dev))
+    return Buffers(("logprobs", n, k, dev.index), out)
+
+
+def token_logprobs_buffers(logits: torch.Tensor, k: int = 0):
+    """(out, ws) of token_logprobs calls with these sizes, to be kept from call to call."""
+    n, v = logits.shape
+    return (_logprobs_out(n, k, logits.device),
+            _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), logits.device))
 
 
 def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, k: int = 0, temperature: float = 1.0,
@@ -280,7 +283,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     target = _dense(targets, torch.int32, (n,), "targets", device) if targets is not None else None
     if out is None:
         with _on(stream):
-            out = token_logprobs_buffers(logits, k)[0]
+            out = _logprobs_out(n, k, logits.device)
     if type(out) is Buffers and out.key == ("logprobs", n, k, device):
         lp, lse, ent, top_lp, top_id = out.addresses
     else:
@@ -297,13 +300,17 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     return out
 
 
+def _distill_out(n: int, v: int, dtype, dev, want_grad: bool) -> Buffers:
+    out = {"loss": torch.empty(n, dtype=torch.float32, device=dev)}
+    if want_grad:
+        out["grad"] = torch.empty(n, v, dtype=dtype, device=dev)
+    return Buffers(("distill", n, v if want_grad else 0, dtype, dev.index), out)
+
+
 def distill_topk_buffers(logits: torch.Tensor, k: int, want_grad: bool = True):
     """(out, ws) of distill_topk calls with these sizes, to be kept from call to call."""
     n, v = logits.shape
-    out = {"loss": torch.empty(n, dtype=torch.float32, device=logits.device)}
-    if want_grad:
-        out["grad"] = torch.empty(n, v, dtype=logits.dtype, device=logits.device)
-    return (Buffers(("distill", n, v if want_grad else 0, logits.dtype, logits.get_device()), out),
+    return (_distill_out(n, v, logits.dtype, logits.device, want_grad),
             _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device))
 
 
@@ -322,7 +329,7 @@ def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     weights = _dense(weight, torch.float32, (n,), "weight", device) if weight is not None else None
     if out is None:
         with _on(stream):
-            out = distill_topk_buffers(logits, k, want_grad)[0]
+            out = _distill_out(n, v, dtype, logits.device, want_grad)
     ld_g, grad = v, None
     if type(out) is Buffers and out.key == ("distill", n, v if want_grad else 0, dtype, device):
         loss = out.addresses[0]
