@@ -259,8 +259,10 @@ class Buffers(dict):
     __delitem__ = pop = popitem = clear = update = setdefault = __ior__ = _changed
 
 
-def _logprobs_out(n: int, k: int, dev) -> Buffers:
-    out = {name: torch.empty(n, dtype=torch.float32, device=dev) for name in ("logprob", "lse", "entropy")}
+def _logprobs_out(n: int, k: int, dev, written: bool) -> Buffers:
+    """written: every call fills in logprob; otherwise it starts as 0, what a row that is not scored has."""
+    out = {"logprob": (torch.empty if written else torch.zeros)(n, dtype=torch.float32, device=dev)}
+    out.update((name, torch.empty(n, dtype=torch.float32, device=dev)) for name in ("lse", "entropy"))
     out["top_logprob"] = torch.empty(n, k, dtype=torch.float32, device=dev)
     out["top_id"] = torch.empty(n, k, dtype=torch.int32, device=dev)
     return Buffers(("logprobs", n, k, dev.index), out)
@@ -269,7 +271,7 @@ def _logprobs_out(n: int, k: int, dev) -> Buffers:
 def token_logprobs_buffers(logits: torch.Tensor, k: int = 0):
     """(out, ws) of token_logprobs calls with these sizes, to be kept from call to call."""
     n, v = logits.shape
-    return (_logprobs_out(n, k, logits.device),
+    return (_logprobs_out(n, k, logits.device, False),
             _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), logits.device))
 
 
@@ -278,12 +280,12 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
                    stream=None) -> Dict[str, torch.Tensor]:
     """Log probability of targets[i] (int32; outside the vocabulary: not scored, 0), log-sum-exp, entropy and the k
     best alternatives (log probabilities and ids, ties to the lower id) of every row of logits at a temperature.
-    Without targets the logprob entry of the result is not written."""
+    Without targets the logprob entry is 0 in a new result (and new buffers), and not written in a given one."""
     n, v, ld, device = _rows(logits, "logits")
     target = _dense(targets, torch.int32, (n,), "targets", device) if targets is not None else None
     if out is None:
         with _on(stream):
-            out = _logprobs_out(n, k, logits.device)
+            out = _logprobs_out(n, k, logits.device, target is not None)
     if type(out) is Buffers and out.key == ("logprobs", n, k, device):
         lp, lse, ent, top_lp, top_id = out.addresses
     else:
