@@ -25,11 +25,11 @@ def to_device(arr: np.ndarray, dtype: str, device="cuda") -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(arr)).to(device)
 
 
-def _on(stream):
-    """Context in which what torch allocates belongs to the call's stream."""
+def _on(stream, device: torch.device):
+    """Context in which what torch allocates on the device belongs to the call's stream."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -214,6 +214,18 @@ def _stream_of(stream, device: int) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(function, name: str, device: int, *args) -> None:
+    """function(*args) with the tensors' GPU as the current one, which the library launches on."""
+    if _current_device() == device:
+        _check(function(*args), name)
+    else:
+        with torch.cuda.device(device):
+            _check(function(*args), name)
+
+
 def _rows(t: torch.Tensor, what: str):
     """(rows, columns, row stride, device index) of a 2-d GPU tensor with contiguous, disjoint rows."""
     device = t.get_device()
@@ -284,7 +296,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     n, v, ld, device = _rows(logits, "logits")
     target = _dense(targets, torch.int32, (n,), "targets", device) if targets is not None else None
     if out is None:
-        with _on(stream):
+        with _on(stream, logits.device):
             out = _logprobs_out(n, k, logits.device, target is not None)
     if type(out) is Buffers and out.key == ("logprobs", n, k, device):
         lp, lse, ent, top_lp, top_id = out.addresses
@@ -293,12 +305,12 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
         top_lp = _dense(out["top_logprob"], torch.float32, (n, k), "top_logprob", device)
         top_id = _dense(out["top_id"], torch.int32, (n, k), "top_id", device)
     if ws is None:
-        with _on(stream):
+        with _on(stream, logits.device):
             ws = _ws(gptq_workspace_size(OP_LOGPROBS, None, 1, v, n, max(k, 1)), logits.device)
     at, nbytes = _workspace(ws, device)
-    _check(lib.gptq_token_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), n, v, ld, target, temperature, k,
-                                   lp if target is not None else None, lse, ent, top_lp, top_id, at, nbytes,
-                                   _stream_of(stream, device)), "gptq_token_logprobs")
+    _call(lib.gptq_token_logprobs, "gptq_token_logprobs", device, logits.data_ptr(), _DTYPE.get(logits.dtype, -1), n, v,
+          ld, target, temperature, k, lp if target is not None else None, lse, ent, top_lp, top_id, at, nbytes,
+          _stream_of(stream, device))
     return out
 
 
@@ -330,7 +342,7 @@ def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     lps = _dense(top_logprob, torch.float32, (n, k), "top_logprob", device)
     weights = _dense(weight, torch.float32, (n,), "weight", device) if weight is not None else None
     if out is None:
-        with _on(stream):
+        with _on(stream, logits.device):
             out = _distill_out(n, v, dtype, logits.device, want_grad)
     ld_g, grad = v, None
     if type(out) is Buffers and out.key == ("distill", n, v if want_grad else 0, dtype, device):
@@ -346,12 +358,11 @@ def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
                 raise ValueError("grad: the logits' type, shape and device are needed")
             grad = g.data_ptr()
     if ws is None:
-        with _on(stream):
+        with _on(stream, logits.device):
             ws = _ws(gptq_workspace_size(OP_DISTILL, None, 1, v, n, k), logits.device)
     at, nbytes = _workspace(ws, device)
-    _check(lib.gptq_distill_topk(logits.data_ptr(), _DTYPE.get(dtype, -1), n, v, ld, ids, lps, k, temperature, bool(tail),
-                                 weights, loss, grad, ld_g, at, nbytes, _stream_of(stream, device)),
-           "gptq_distill_topk")
+    _call(lib.gptq_distill_topk, "gptq_distill_topk", device, logits.data_ptr(), _DTYPE.get(dtype, -1), n, v, ld, ids,
+          lps, k, temperature, bool(tail), weights, loss, grad, ld_g, at, nbytes, _stream_of(stream, device))
     return out
 
 
@@ -391,17 +402,16 @@ def lora_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.T
     dtype = X.dtype
     n, r, d_out, pa, pb, pad, ps = _adapters(A, B, adapter, scale, dtype, M, d_in, device)
     if Y is None:
-        with _on(stream):
+        with _on(stream, X.device):
             Y = torch.empty(M, d_out, dtype=base.dtype if base is not None else torch.float32, device=X.device)
     py, ld_y = _out_rows(Y, Y.dtype, M, d_out, "Y", device)
     p0, ld_b = _out_rows(base, Y.dtype, M, d_out, "base", device) if base is not None else (None, d_out)
     if ws is None:
-        with _on(stream):
+        with _on(stream, X.device):
             ws = _ws(gptq_workspace_size(OP_LORA, None, d_out, d_in, M, r), X.device)
     at, nbytes = _workspace(ws, device)
-    _check(lib.gptq_lora_add(X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in, ld_x, pa, pb, n, r, ps, pad, p0, ld_b, py,
-                             _DTYPE.get(Y.dtype, -1), d_out, ld_y, at, nbytes, _stream_of(stream, device)),
-           "gptq_lora_add")
+    _call(lib.gptq_lora_add, "gptq_lora_add", device, X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in, ld_x, pa, pb, n, r,
+          ps, pad, p0, ld_b, py, _DTYPE.get(Y.dtype, -1), d_out, ld_y, at, nbytes, _stream_of(stream, device))
     return Y
 
 
@@ -430,16 +440,16 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     pz = _dense(zeros, torch.uint8, (d_out, ng), "zeros", device)
     pp = _dense(perm, torch.int32, (d_in,), "perm", device) if perm is not None else None
     if Y is None:
-        with _on(stream):
+        with _on(stream, X.device):
             Y = torch.empty(M, d_out, dtype=torch.float32, device=X.device)
     py, ld_y = _out_rows(Y, torch.float32, M, d_out, "Y", device)
     if ws is None:
-        with _on(stream):
+        with _on(stream, X.device):
             ws = _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, M, r), X.device)
     at, nbytes = _workspace(ws, device)
-    _check(lib.gptq_w4a16_lora_matmul(X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in, ld_x, pq, psc, pz, pp, d_out,
-                                      group_size, pa, pb, n, r, ps, pad, py, ld_y, at, nbytes,
-                                      _stream_of(stream, device)), "gptq_w4a16_lora_matmul")
+    _call(lib.gptq_w4a16_lora_matmul, "gptq_w4a16_lora_matmul", device, X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in,
+          ld_x, pq, psc, pz, pp, d_out, group_size, pa, pb, n, r, ps, pad, py, ld_y, at, nbytes,
+          _stream_of(stream, device))
     return Y
 
 

@@ -1,4 +1,6 @@
 """The wrappers of scoring, distillation and adapters: what they return and what they make of their tensors."""
+import contextlib
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +40,32 @@ def test_without_targets_no_row_is_scored():
     del held
     out, ws = P.token_logprobs_buffers(x, 2)
     assert not bool(P.token_logprobs(x, None, 2, out=out, ws=ws)["logprob"].any())
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_are_made_with_the_tensors_gpu_current(monkeypatch, current):
+    """A call for tensors of a GPU that is not the current one makes it the current one, and only then."""
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    made = []
+
+    @contextlib.contextmanager
+    def device(index):
+        made.append(index)
+        yield
+    x = torch.randn(3, 256, device="cuda").bfloat16()
+    A = torch.randn(1, 8, 256, device="cuda").bfloat16()
+    B = torch.randn(1, 64, 8, device="cuda").bfloat16()
+    ad = torch.zeros(3, dtype=torch.int32, device="cuda")
+    qw = torch.zeros(64, 128, dtype=torch.uint8, device="cuda")
+    sc, z = torch.zeros(64, 2, dtype=torch.int16, device="cuda"), torch.zeros(64, 2, dtype=torch.uint8, device="cuda")
+    calls = [lambda: P.token_logprobs(x, None, 2)["lse"],
+             lambda: P.distill_topk(x, ad[:, None].contiguous(), torch.zeros(3, 1, device="cuda") - 1)["loss"],
+             lambda: P.lora_add(x, A, B, ad), lambda: P.w4a16_lora_matmul(x, qw, sc, z, 128, A, B, ad)]
+    want = [f() for f in calls]
+    monkeypatch.setattr(P, "_current_device", lambda: current)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for i, f in enumerate(calls):
+        made.clear()
+        assert torch.equal(f(), want[i])
+        assert made == ([] if current == 0 else [0]), i
