@@ -420,7 +420,7 @@ def w4a16_lora_buffers(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor):
     M, d_in = X.shape
     d_out, r = B.shape[1], B.shape[2]
     return (torch.empty(M, d_out, dtype=torch.float32, device=X.device),
-            _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, M, r), X.device))
+            _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, max(M, 1), r), X.device))
 
 
 def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
@@ -428,7 +428,7 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
                       scale: Optional[torch.Tensor] = None, perm: Optional[torch.Tensor] = None,
                       Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
-    """w4a16_matmul (up to 64 tokens) plus every token's adapter, as lora_add adds it."""
+    """w4a16_matmul (up to 64 tokens, or none) plus every token's adapter, as lora_add adds it."""
     M, d_in, ld_x, device = _rows(X, "X")
     dtype = X.dtype
     n, r, d_out, pa, pb, pad, ps = _adapters(A, B, adapter, scale, dtype, M, d_in, device)
@@ -443,6 +443,8 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
         with _on(stream, X.device):
             Y = torch.empty(M, d_out, dtype=torch.float32, device=X.device)
     py, ld_y = _out_rows(Y, torch.float32, M, d_out, "Y", device)
+    if M == 0:
+        return Y
     if ws is None:
         with _on(stream, X.device):
             ws = _ws(gptq_workspace_size(OP_W4A16_LORA, None, d_out, d_in, M, r), X.device)

@@ -69,3 +69,20 @@ def test_calls_are_made_with_the_tensors_gpu_current(monkeypatch, current):
         made.clear()
         assert torch.equal(f(), want[i])
         assert made == ([] if current == 0 else [0]), i
+
+
+def test_empty_batches_of_the_adapted_projection():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    X = torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda")
+    A = torch.zeros(2, 8, 256, dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros(2, 64, 8, dtype=torch.bfloat16, device="cuda")
+    ad = torch.zeros(0, dtype=torch.int32, device="cuda")
+    qw = torch.zeros(64, 128, dtype=torch.uint8, device="cuda")
+    sc, z = torch.zeros(64, 2, dtype=torch.int16, device="cuda"), torch.zeros(64, 2, dtype=torch.uint8, device="cuda")
+    assert P.w4a16_lora_matmul(X, qw, sc, z, 128, A, B, ad).shape == (0, 64)
+    Y, ws = P.w4a16_lora_buffers(X, A, B)
+    assert P.w4a16_lora_matmul(X, qw, sc, z, 128, A, B, ad, Y=Y, ws=ws) is Y and Y.shape == (0, 64)
+    with pytest.raises(ValueError):                       # the tensors are looked at all the same
+        P.w4a16_lora_matmul(X, qw, sc, z, 128, A.half(), B, ad)
+    assert P.lora_add(X, A, B, ad).shape == (0, 64)
