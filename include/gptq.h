@@ -381,7 +381,8 @@ gptq_status gptq_layer_forward(const void* X, int32_t x_dtype, int64_t n_tok, in
  *        (-0 and +0 tie), as ids and log probabilities z - lse.
  *
  *   logits    device, n_rows x vocab of x_dtype, row stride ld_x elements;
- *             vocab <= 2^21 (more: GPTQ_EUNSUPPORTED);
+ *             n_rows < 2^24 (else GPTQ_EINVAL), vocab <= 2^21 (more:
+ *             GPTQ_EUNSUPPORTED);
  *             only the elements' own alignment is required (rows that start
  *             anywhere are read with aligned 16-byte loads inside).
  *   targets   device int32 [n_rows], or NULL with logprob NULL.  A target
@@ -420,8 +421,9 @@ gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, int64_t n_r
  *       loss = sum_i p_i (log p_i - log q_i)
  *       dloss/dx_j = (q_j - p_j) / T, p_j = 0 outside K.
  *
- *   logits      device, n_rows x vocab of x_dtype, row stride ld_x; vocab
- *               <= 2^21 (more: GPTQ_EUNSUPPORTED).
+ *   logits      device, n_rows x vocab of x_dtype, row stride ld_x; n_rows
+ *               <= 2^22 (more: GPTQ_EINVAL), vocab <= 2^21 (more:
+ *               GPTQ_EUNSUPPORTED).
  *   top_id      device int32 [n_rows][k], top_logprob device fp32
  *               [n_rows][k].  An entry whose id is outside [0, vocab) or
  *               whose l is -inf is absent (padding of a shorter list); an id

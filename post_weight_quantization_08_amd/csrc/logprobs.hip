@@ -586,7 +586,8 @@ extern "C" gptq_status gptq_token_logprobs(const void* logits, int32_t x_dtype, 
                                            float* logprob, float* lse, float* entropy, float* top_logprob,
                                            int32_t* top_id, void* workspace, size_t ws_bytes, void* stream) {
   GQ_CHECK_ARG(x_dtype == GPTQ_F32 || x_dtype == GPTQ_F16 || x_dtype == GPTQ_BF16);
-  GQ_CHECK_ARG(n_rows >= 0 && n_rows <= ((int64_t)1 << 24) && vocab >= 1 && vocab <= ((int64_t)1 << 30));
+  // a launch holds fewer than 2^32 threads
+  GQ_CHECK_ARG(n_rows >= 0 && n_rows < ((int64_t)1 << 32) / kLpThreads && vocab >= 1 && vocab <= ((int64_t)1 << 30));
   GQ_CHECK_ARG(ld_x >= vocab && ld_x <= ((int64_t)1 << 36));
   GQ_CHECK_ARG(temperature >= 1e-4f && temperature <= 1e4f);
   GQ_CHECK_ARG(k >= 0 && k <= vocab);
