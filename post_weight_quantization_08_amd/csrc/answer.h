@@ -130,6 +130,14 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // flight across it.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// 64 lanes' 16 (4) bytes each, one after the other from `to` on.
+__device__ __forceinline__ void lds_load16(const void* from, char* to) {
+  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+}
+
 // A value that is the same in every lane, kept in a scalar register.
 __device__ __forceinline__ float uniform(float x) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));

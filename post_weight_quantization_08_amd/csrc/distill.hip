@@ -147,10 +147,11 @@ struct DsSource {
     lane = threadIdx.x * 16u;
     asm volatile("" : "+v"(lane));   // a row's own value: offsets of all slots are not kept from row to row
   }
-  __device__ __forceinline__ u32x4 load(int first) const {
+  __device__ __forceinline__ const u32x4* block(int first) const {
     const uint32_t at = (uint32_t)first * 16u + lane;
-    return *reinterpret_cast<const u32x4*>(base + (at < last ? at : last));
+    return reinterpret_cast<const u32x4*>(base + (at < last ? at : last));
   }
+  __device__ __forceinline__ u32x4 load(int first) const { return *block(first); }
 };
 
 // LDS of a workgroup of T threads with W words of bits per lane.
@@ -562,6 +563,12 @@ __device__ __forceinline__ void ds_store(const DsArgs& a, const Span<kDt>& sp, i
   else __builtin_memcpy(__builtin_assume_aligned(p, 2), &w, 16);
 }
 
+// Blocks a lane holds in registers; a row kernel's others lie in LDS, where
+// direct loads put them.  2048 rows of 151936 bf16, k = 64, take 295 us with
+// gradient, 4.2 TB/s, and 123 us without; with all 20 blocks in registers up to
+// 47 of 128 registers were spilled, and it took 339 and 144.
+constexpr int kDsHeld = 16;
+
 // Row kernel: T threads hold a row of at most T NB blocks.
 //
 // What is read ahead is waited for only where nothing younger is in flight:
@@ -579,7 +586,24 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
   if (row >= a.n_rows) return;
   DsRow<kDt, T, NB> d(sh, a);
   d.clear_bits();
-  u32x4 w[NB];
+  constexpr int kHeld = NB < kDsHeld ? NB : kDsHeld;
+  __shared__ __align__(16) u32x4 tail[NB > kHeld ? NB - kHeld : 1][NB > kHeld ? T : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  u32x4 w[kHeld];
+  // the next row's block into the place of block i, which nothing reads any more
+  auto refill = [&](const DsSource<kDt>& src, int i) {
+    if (i < kHeld) w[i < kHeld ? i : 0] = src.load(i * T);
+    else lds_load16(src.block(i * T), reinterpret_cast<char*>(&tail[i - kHeld][wave * 64]));
+  };
+  // together, and after all of them were read: a direct load in flight is
+  // waited for at the next reading
+  auto refill_tail = [&](const DsSource<kDt>& src) {
+    if constexpr (NB > kHeld) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = kHeld; i < NB; ++i) refill(src, i);
+    }
+  };
   Span<kDt> sp(a.x, row, a.ld, a.vocab);
   DsEntry n = d.read_entry(row);
   d.read_logit(n, sp);
@@ -587,7 +611,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
   {
     const DsSource<kDt> src(sp, true);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
+    for (int i = 0; i < NB; ++i) refill(src, i);
   }
   lds_barrier();
   DsFix fix{-1, 0.f};
@@ -603,13 +627,25 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
     float weight = *weights;
     float r = kDsFloor, rc = kDsFloor * a.c, s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < kHeld; ++i) {
       float v[E];
       unpack_held<kDt>(w[i], v);
       hide<kDt, NB>(v, d.bits(i));
       ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
-      if constexpr (!kGrad) w[i] = src.load(i * T);
+      if constexpr (!kGrad) refill(src, i);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (NB > kHeld) {
+      memory_done();   // this wave's part of the tail is there
+#pragma unroll
+      for (int i = kHeld; i < NB; ++i) {
+        float v[E];
+        Blocks<kDt>::unpack(tail[i - kHeld][t], v);
+        hide<kDt, NB>(v, d.bits(i));
+        ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (!kGrad) refill_tail(src);
     }
     const float xe = sp.edge(t) >= 0 ? bits_value<kDt>(edge_bits) : -INFINITY;
     const float xr = d.edge_listed ? -INFINITY : xe;
@@ -657,20 +693,23 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
-          w[i] = src.load(i * T);
+          if (i < kHeld) refill(src, i);
         }
+        refill_tail(src);
       } else if (!exact) {
         const float frc = r * a.c;
         const float rest = f.rest * exp2_hw(-fmaf(r, a.c, -frc));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           float v[E], g[E];
-          unpack_held<kDt>(w[i], v);
+          if (i < kHeld) unpack_held<kDt>(w[i < kHeld ? i : 0], v);
+          else Blocks<kDt>::unpack(tail[i < kHeld ? 0 : i - kHeld][t], v);
           ds_gradient<true>(f, rest, frc, a.c, v, g, E);
           if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
-          w[i] = src.load(i * T);
+          if (i < kHeld) refill(src, i);
           __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
         }
+        refill_tail(src);
       } else {
 #pragma unroll 1
         for (int i = 0; i < NB; ++i) {
@@ -681,7 +720,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
           ds_store<kDt>(a, sp, row, i * T, t, g);
         }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) w[i] = src.load(i * T);
+        for (int i = 0; i < kHeld; ++i) refill(src, i);
+        refill_tail(src);
       }
     }
     if (!more) break;
@@ -690,8 +730,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
     n = ahead;
     edge_bits = edge_ahead;
   }
+  if constexpr (kGrad || NB > kHeld) memory_done();   // no direct load ends after the workgroup
   if constexpr (kGrad) {
-    memory_done();
     lds_barrier();
     ds_store_fix<kDt>(a, fix_row, fix);
   }

@@ -45,14 +45,6 @@ __device__ __forceinline__ u32x4 load8_end(const uint16_t* row, int k, int n) {
   return w;
 }
 
-// 64 lanes' 16 (4) bytes each, one after the other from `to` on.
-__device__ __forceinline__ void lds_load16(const void* from, char* to) {
-  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
-}
-__device__ __forceinline__ void lds_load4(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds(from, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
-}
-
 // T[m][r] = s_a X[m] . A_a[r] for (m, r) number `at`, by one wave.
 template <int kDt>
 __device__ __forceinline__ void lora_down_one(const LoraFew& a, int64_t at) {
