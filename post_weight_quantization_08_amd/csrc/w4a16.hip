@@ -545,16 +545,31 @@ static void launch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
 
 // Waves per workgroup of the wide kernel, 0 for the other one.  Four to eight,
 // as many as make the fewest rounds over 256 CUs, weighed by the waves (28672
-// rows: 8 leave 32 CUs idle, 7 none: 57 -> 53 us at 48 tokens).  Its time hardly
-// depends on the tokens of a tile, the other kernel's does; where they cross
-// depends on the rows too.  Here / the other kernel, us: 28672 x 8192, 5, 16 and
-// 64 tokens 43 / 49, 43 / 74, 69 / 238; 14336 x 4096, 5, 8 and 16 tokens 20.7 /
-// 18.9, 20.8 / 21.5, 21 / 27; 8192 x 8192, 16, 17 and 32 tokens 34 / 29, 39 / 35,
-// 39 / 46.  Up to 4 tokens the other kernel keeps the activations in LDS.
-static int w4_wide_waves(int64_t M, int64_t d_out, int ng) {
-  if (M <= 4 || d_out < (M <= 16 ? 192 * 64 : 128 * 64)) return 0;
-  if (M * d_out < (M <= 16 ? 8 * 192 * 64 : 22 * 128 * 64)) return 0;
-  const int64_t tiles = cdiv(d_out, 16);
+// rows: 8 leave 32 CUs idle, 7 none: 57 -> 53 us at 48 tokens).
+//
+// The other kernel's time goes by whole rounds of its workgroups, one tile of 16
+// rows each, over the CUs, and by the tokens; this one's hardly depends on the
+// tokens of a tile, and is at least that of four waves per CU, which two or three
+// rounds do not fill.  Here / the other kernel, us, bf16 without adapters:
+//   two rounds, 8192 x 4096: 17, 28, 32, 64 tokens 22.5 / 18.9, 22.6 / 22.5, 22.6 /
+//     23.7, 31.7 / 38.7 (with 32 adapters of rank 16: 32 tokens 27.1 / 26.5, 64 38.7 / 43.1)
+//   three, 12288 x 4096: 8, 12, 16, 17 tokens 19.5 / 16.5, 19.6 / 19.7, 19.6 / 21.7,
+//     22.6 / 24.2; more, 14336 x 4096: 5, 7, 16 tokens 19.7 / 18.3, 19.5 / 20.2, 19.6 / 25.7;
+//   five and many chunks: 28672 x 8192, 5, 16, 64 tokens 40 / 47, 40 / 72, 71 / 231;
+//     but 65536 x 1024, 5 tokens 19.0 / 18.2.
+// With few chunks the ring does not fill: 10240 x 256, 17, 33 and 64 tokens 7.3 / 6.6,
+// 8.0 / 8.0, 9.0 / 9.4; 131072 x 128, 33 tokens 22.0 / 18.2.
+// Up to 4 tokens the other kernel keeps the activations in LDS.
+static int w4_wide_waves(int64_t M, int64_t d_in, int64_t d_out, int ng) {
+  const int64_t tiles = cdiv(d_out, 16), rounds = cdiv(tiles, 256);
+  if (M <= 4 || tiles < 512) return 0;
+  if (M <= 16) {
+    const bool large = rounds >= 5 && d_in >= 2048 && rounds * d_in >= 14336;
+    if (rounds == 2 || M < (rounds == 3 ? 12 : large ? 5 : 7)) return 0;
+  } else {
+    if (rounds == 2 && M < 32) return 0;
+    if (d_in < (rounds == 2 || M <= 32 ? 512 : 256)) return 0;
+  }
   int best = 0;
   int64_t cost = 0;
   for (int w = 8; w >= 4; --w) {
@@ -579,7 +594,7 @@ static void launch_w4_wide(const W4Args& a, int waves, hipStream_t st) {
 
 template <int kDt, bool kLora>
 static void dispatch_w4(const W4Args& a, const W4Plan& pl, hipStream_t st) {
-  const int waves = w4_wide_waves(a.M, a.d_out, a.ng);
+  const int waves = w4_wide_waves(a.M, a.K, a.d_out, a.ng);
   const int mt = pl.Mp / 16;
   if (waves > 0) {
     if (a.M <= 16) launch_w4_wide<kDt, 1, kLora>(a, waves, st);
