@@ -27,6 +27,13 @@ __device__ __forceinline__ float bits_value(uint32_t b) {
   else if constexpr (kDt == GPTQ_BF16) return bf16_bits_to_f32(b);
   else return f16_bits_to_f32(b);
 }
+// A value's bits, rounded to nearest even; NaN stays NaN.
+template <int kDt>
+__device__ __forceinline__ uint32_t value_bits(float v) {
+  if constexpr (kDt == GPTQ_F32) return __float_as_uint(v);
+  else if constexpr (kDt == GPTQ_F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+  else return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
 template <int kDt>
 __device__ __forceinline__ void store_bits(void* p, int64_t i, uint32_t b) {
   if constexpr (kDt == GPTQ_F32) static_cast<uint32_t*>(p)[i] = b;

@@ -17,8 +17,8 @@
 // 16-bit terms, which hold all of an fp32: cut off after 8 bits each for bf16;
 // rounded for fp16, after rows of T were scaled by a power of two, so that
 // neither their size nor their smallness leaves fp16's range.  Two terms (16 and
-// 22 bits) take as long.  The second product's columns are dealt to the MFMA
-// tiles so that a lane ends up with four consecutive outputs and sixteen lanes
+// 22 bits) are 0 to 3 % faster.  The second product's columns are dealt to the
+// MFMA tiles so that a lane ends up with four consecutive outputs and sixteen lanes
 // with 64: base and Y move in pieces of 256 (fp32) or 128 bytes, at any alignment.
 //
 // Bound by memory: X, base and Y once, the factors from L2 (a factor's matrix
@@ -394,9 +394,11 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], u32x4 (&out)[kTe
   }
 }
 
-// 32 tokens by `cols` columns (a multiple of 256); kS steps of 32 ranks.
+// 32 tokens by `cols` columns (a multiple of 256); kS steps of 32 ranks.  One
+// step leaves room for four waves per SIMD, two registers short of it without
+// asking (8192 x 4096 -> 14336, rank 16, 16-bit: 182 us).
 template <int kDt, int kY, int kS>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
+__global__ __launch_bounds__(256, kS == 1 ? 4 : 1) void lora_up_kernel(LoraArgs a) {
   constexpr int kPitch = kS * 32 + 4;
   __shared__ __align__(16) float tsum[kLoraTile][kPitch];
   __shared__ u32x4 terms[2][kS][kTerms][64];   // [token tile][rank step][term][lane]
@@ -551,56 +553,31 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (m + i >= a.M) continue;
-        if (own[i] < 0) {                  // the base as it is
-          if (whole) {
-            char* o = static_cast<char*>(a.Y) + ((m + i) * a.ld_y + col) * kYE;
-            __builtin_memcpy(__builtin_assume_aligned(o, kYE), &in[i], sizeof(Four));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (col + e < a.d_out)
-                store_bits<kY>(a.Y, (m + i) * a.ld_y + col + e,
-                               a.base ? load_bits<kY>(a.base, (m + i) * a.ld_b + col + e) : 0u);
-          }
-          continue;
-        }
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (a.base) {
-          if (whole) {
-            if constexpr (kY == GPTQ_F32) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(in[i][e]);
-            } else {
-              y[0] = lo16<kY>(in[i].x);
-              y[1] = hi16<kY>(in[i].x);
-              y[2] = lo16<kY>(in[i].y);
-              y[3] = hi16<kY>(in[i].y);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (col + e < a.d_out) y[e] = load_el<kY>(a.base, (m + i) * a.ld_b + col + e);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = fmaf(acc[e][i], g[i], y[e]);
+        // a token without an adapter keeps the bits of its base
+        const bool keeps = own[i] < 0;
         if (whole) {
-          char* o = static_cast<char*>(a.Y) + ((m + i) * a.ld_y + col) * kYE;
+          Four out;
           if constexpr (kY == GPTQ_F32) {
-            __builtin_memcpy(__builtin_assume_aligned(o, 4), y, 16);
-          } else {
-            uint16_t h[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (kY == GPTQ_F16) h[e] = __builtin_bit_cast(uint16_t, (_Float16)y[e]);
-              else h[e] = __builtin_bit_cast(uint16_t, (__bf16)y[e]);
-            }
-            __builtin_memcpy(__builtin_assume_aligned(o, 2), h, 8);
+            for (int e = 0; e < 4; ++e)
+              out[e] = __float_as_uint(fmaf(acc[e][i], g[i], __uint_as_float(in[i][e])));
+          } else {
+            out.x = value_bits<kY>(fmaf(acc[0][i], g[i], lo16<kY>(in[i].x))) |
+                    value_bits<kY>(fmaf(acc[1][i], g[i], hi16<kY>(in[i].x))) << 16;
+            out.y = value_bits<kY>(fmaf(acc[2][i], g[i], lo16<kY>(in[i].y))) |
+                    value_bits<kY>(fmaf(acc[3][i], g[i], hi16<kY>(in[i].y))) << 16;
           }
+          if (keeps) out = in[i];
+          char* o = static_cast<char*>(a.Y) + ((m + i) * a.ld_y + col) * kYE;
+          __builtin_memcpy(__builtin_assume_aligned(o, kYE), &out, sizeof(Four));
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < a.d_out) store_el<kY>(a.Y, (m + i) * a.ld_y + col + e, y[e]);
+          for (int e = 0; e < 4; ++e) {
+            if (col + e >= a.d_out) continue;
+            const uint32_t base = a.base ? load_bits<kY>(a.base, (m + i) * a.ld_b + col + e) : 0u;
+            const uint32_t y = value_bits<kY>(fmaf(acc[e][i], g[i], bits_value<kY>(base)));
+            store_bits<kY>(a.Y, (m + i) * a.ld_y + col + e, keeps ? base : y);
+          }
         }
       }
     }
