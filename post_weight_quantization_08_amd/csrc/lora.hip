@@ -34,9 +34,12 @@ namespace gq {
 size_t w4a16_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out);
 
 // Tokens up to which every one is taken by itself.  Which adapters they want is
-// not known here: 128 tokens of 4096 -> 4096, rank 16, take 11 us by themselves
-// and in tiles 12 (runs of four adapters) or 96 (every one its own); of 8192 ->
-// 28672, rank 64, 56 or 110 by themselves and 22 or 224 in tiles.
+// not known here.  128 tokens in runs of four adapters, or every one with its own:
+//   4096 -> 4096, rank 16:    9 or 12 us by themselves, 12 or 105 in tiles
+//   4096 -> 14336, rank 32:   20 or 34,                 12 or 121
+//   8192 -> 28672, rank 64:   57 or 108,                20 or 225
+// and 48 tokens 7 or 8, 18 or 105; 11 or 17, 17 or 119; 26 or 46, 26 or 192.  By
+// themselves is never more than 2.9 times the other way, tiles up to 13 times.
 constexpr int kLoraFew = 128;
 constexpr int kLoraTile = 32;       // tokens of an MFMA tile
 constexpr int kLoraMaxRank = 128;
@@ -599,15 +602,16 @@ static LoraPlan lora_plan(int64_t M, int64_t d_in, int64_t d_out, int64_t rank) 
     // parts of the sum, of at least one step per wave: for two workgroups per CU,
     // and up to eight parts also for eight of them (a tile of two adapters takes
     // twice as long and must not be the last to end: 8192 x 11008 -> 4096, rank 64,
-    // 150 us, and 164 with two per CU).  The second product reads every part's T
-    // again: 2048 x 8192 -> 8192, rank 64, takes 46 us in 8 parts and 64 in 32.
+    // 143 us, and 168 with two per CU).  The second product reads every part's T
+    // again: 2048 x 8192 -> 8192, rank 64, takes 68 us in 8 parts and 85 in 32.
     const int64_t tiles = cdiv(M, kLoraTile);
     const int64_t parts = std::max(cdiv(512, tiles), std::min<int64_t>(cdiv(2048, tiles), 8));
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(parts, d_in / 256));
   }
   // columns of a workgroup: as many as leave every CU eight workgroups, so that
-  // T's sum is made for more of them (8192 x 11008 -> 4096, rank 64: 125 us with
-  // 512 columns, 149 with 1024; 300 x 4096 -> 14336, rank 32: 17 and 20 with 256)
+  // T's sum is made for more of them.  Here, with 256, 512 and 1024 columns, us:
+  // 300 x 4096 -> 14336, rank 32 (256) 19, 22, 33; 8192 x 11008 -> 4096, rank 64
+  // (512) 143, 143, 161; 8192 x 4096 -> 14336, rank 64 (1024) 251, 233, 234.
   p.cols = 1024;
   while (p.cols > 256 && cdiv(M, kLoraTile) * cdiv(d_out, p.cols) < 2048) p.cols /= 2;
   p.k_split = (int)(cdiv(cdiv(d_in, p.splits), 128) * 128);
