@@ -425,7 +425,7 @@ __device__ __forceinline__ DsFinal ds_fetch(const DsFinal& g, float r) {
 }
 
 // The rest's sum over what a lane holds.
-template <int kDt, int T, int NB>
+template <int kDt>
 __device__ __forceinline__ void ds_add_block(float& r, float& rc, float& s, const float (&v)[Span<kDt>::E], float c) {
   constexpr int E = Span<kDt>::E;
   float vm = fmaxf(v[0], v[1]);
@@ -456,7 +456,7 @@ __device__ __forceinline__ void unpack_held(u32x4 w, float (&v)[Span<kDt>::E]) {
   Blocks<kDt>::unpack(w, v);
 }
 
-template <int kDt, int NB>
+template <int kDt>
 __device__ __forceinline__ void hide(float (&v)[Span<kDt>::E], uint32_t listed) {
   if (listed) {
 #pragma unroll
@@ -476,7 +476,7 @@ __device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<k
   auto get = [&](int i, float (&v)[E]) {
     const int first = (slot0 + i) * T, t = threadIdx.x;
     Blocks<kDt>::unpack(t < sp.blocks - first ? sp.load(first, t) : masked_block<kDt>(), v);
-    hide<kDt, NB>(v, d.bits_any(i));
+    hide<kDt>(v, d.bits_any(i));
   };
   float m = xe;
 #pragma unroll 1
@@ -630,8 +630,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
     for (int i = 0; i < kHeld; ++i) {
       float v[E];
       unpack_held<kDt>(w[i], v);
-      hide<kDt, NB>(v, d.bits(i));
-      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      hide<kDt>(v, d.bits(i));
+      ds_add_block<kDt>(r, rc, s, v, a.c);
       if constexpr (!kGrad) refill(src, i);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -641,8 +641,8 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
       for (int i = kHeld; i < NB; ++i) {
         float v[E];
         Blocks<kDt>::unpack(tail[i - kHeld][t], v);
-        hide<kDt, NB>(v, d.bits(i));
-        ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+        hide<kDt>(v, d.bits(i));
+        ds_add_block<kDt>(r, rc, s, v, a.c);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (!kGrad) refill_tail(src);
@@ -654,7 +654,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
       v[0] = xr;
 #pragma unroll
       for (int e = 1; e < E; ++e) v[e] = -INFINITY;
-      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      ds_add_block<kDt>(r, rc, s, v, a.c);
     }
     s *= exp2_hw(-fmaf(r, a.c, -rc));
     d.put_logits(n);
@@ -797,8 +797,8 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
     for (int i = 0; i < NB; ++i) {
       float v[E];
       unpack_held<kDt>(w[i], v);
-      hide<kDt, NB>(v, d.bits(i));
-      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      hide<kDt>(v, d.bits(i));
+      ds_add_block<kDt>(r, rc, s, v, a.c);
       __builtin_amdgcn_sched_barrier(0);
     }
     const float xr = d.edge_listed ? -INFINITY : xe;
@@ -807,7 +807,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       v[0] = xr;
 #pragma unroll
       for (int e = 1; e < E; ++e) v[e] = -INFINITY;
-      ds_add_block<kDt, T, NB>(r, rc, s, v, a.c);
+      ds_add_block<kDt>(r, rc, s, v, a.c);
     }
     s *= exp2_hw(-fmaf(r, a.c, -rc));
     ds_join(r, s, a.c, sh);

@@ -28,6 +28,16 @@ __device__ __forceinline__ float hi16(uint32_t w) {
   else return __uint_as_float(w & 0xFFFF0000u);
 }
 
+template <int kDt>
+__device__ __forceinline__ f32x4 mfma_16x16x32(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (kDt == GPTQ_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                  0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+}
+
 // 8 elements from any address.
 __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
   u32x4 w;

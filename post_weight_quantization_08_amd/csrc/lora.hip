@@ -115,16 +115,6 @@ __global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a) {
 }
 
 // ---------------------------------------------------------------- many tokens
-template <int kDt>
-__device__ __forceinline__ f32x4 lora_mfma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (kDt == GPTQ_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
-                                                  0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                   0, 0, 0);
-}
-
 // Calls f(adapter, lanes' match) for every adapter among the tile's 32 tokens;
 // `mine` is the adapter of token lane % 32, or -1.
 template <class F>
@@ -217,8 +207,8 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int t = 0; t < kR; ++t) {
-          acc[t][0] = lora_mfma<kDt>(p.f[j][t], p.x[j][0], acc[t][0]);
-          acc[t][1] = lora_mfma<kDt>(p.f[j][t], p.x[j][1], acc[t][1]);
+          acc[t][0] = mfma_16x16x32<kDt>(p.f[j][t], p.x[j][0], acc[t][0]);
+          acc[t][1] = mfma_16x16x32<kDt>(p.f[j][t], p.x[j][1], acc[t][1]);
         }
     };
     const int first = k0 + wave * 64;
@@ -330,7 +320,7 @@ __global__ __launch_bounds__(256) void lora_down_lds_kernel(LoraArgs a) {
 #pragma unroll
         for (int r = 0; r < kMine; ++r)
 #pragma unroll
-          for (int t = 0; t < kTok; ++t) acc[r][t] = lora_mfma<kDt>(fv[r], xv[t], acc[r][t]);
+          for (int t = 0; t < kTok; ++t) acc[r][t] = mfma_16x16x32<kDt>(fv[r], xv[t], acc[r][t]);
       }
     };
     fetch(0, x0);
@@ -535,7 +525,7 @@ __global__ __launch_bounds__(256, kS == 1 ? 4 : 1) void lora_up_kernel(LoraArgs 
 #pragma unroll
         for (int s = 0; s < kS; ++s)
 #pragma unroll
-          for (int k = kTerms - 1; k >= 0; --k) d = lora_mfma<kDt>(terms[t][s][k][lane], w[s], d);
+          for (int k = kTerms - 1; k >= 0; --k) d = mfma_16x16x32<kDt>(terms[t][s][k][lane], w[s], d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[e][i] = own[i] == ad ? d[i] : acc[e][i];
       };

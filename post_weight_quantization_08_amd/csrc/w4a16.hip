@@ -128,16 +128,6 @@ __device__ __forceinline__ u32x4 w4_operand(uint32_t w, uint32_t zc, uint32_t ma
   return r;
 }
 
-template <int kDt>
-__device__ __forceinline__ f32x4 w4_mfma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (kDt == GPTQ_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
-                                                   0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                    0, 0, 0);
-}
-
 __host__ __device__ constexpr int align_lds(int b) { return (b + 15) / 16 * 16; }
 
 // Dynamic LDS of the main kernel: [scales 16 x ng fp16][zeros 16 x ng]
@@ -274,7 +264,7 @@ __global__ __launch_bounds__(64 * kW) void w4_main_kernel(W4Args a) {
       for (int t = 0; t < 4; ++t) {
         const u32x4 b = w4_operand<kDt>(wq[u][t], zc, mask_s, magic_v);
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) acc[mt] = w4_mfma<kDt>(A[kLX ? 0 : u][mt][t], b, acc[mt]);
+        for (int mt = 0; mt < kMT; ++mt) acc[mt] = mfma_16x16x32<kDt>(A[kLX ? 0 : u][mt][t], b, acc[mt]);
       }
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
@@ -452,7 +442,7 @@ __global__ __launch_bounds__(64 * kMost, 1) void w4_wide_kernel(W4Args a) {
         x[mt] = *reinterpret_cast<const u32x4*>(xr + (mt * 16 + c16) * 256 + (((q * 4 + i) ^ c16) * 16));
       const u32x4 b = w4_operand<kDt>(w[i], (0xE400u | zb) * 0x00010001u, mask_s, magic_v);
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) acc[mt] = w4_mfma<kDt>(x[mt], b, acc[mt]);
+      for (int mt = 0; mt < kMT; ++mt) acc[mt] = mfma_16x16x32<kDt>(x[mt], b, acc[mt]);
     }
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
