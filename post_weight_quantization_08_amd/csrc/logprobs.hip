@@ -20,8 +20,8 @@
 // bound sorted by (value, index).
 //
 // Bound by memory: 2 or 4 bytes and about 6 operations, one exponential, per
-// logit.  4096 rows of 131072 bf16, k = 64: 213 us, 5.0 TB/s of logits; 1000 of
-// 50021 fp32, k = 1: 44 us, 4.5 TB/s.  One row of 131072: 12 us in two launches,
+// logit.  4096 rows of 131072 bf16, k = 64: 220 us, 4.9 TB/s of logits; 1000 of
+// 50021 fp32, k = 1: 46 us, 4.3 TB/s.  One row of 131072: 12.6 us in two launches,
 // of which the reading is a small part.
 #include "answer.h"
 
@@ -538,13 +538,19 @@ struct LpPlan {
 
 // Parts of a row: one workgroup per row when that gives every CU one, else
 // enough parts for four, of at least two blocks a lane.  The join is a second
-// launch and a part ends in a search of its own, so more rows are not split:
-// 512 rows of 131072 bf16, k = 20, take 33 us whole and 38 us in parts, 1000 of
-// 50021 fp32, k = 1, 37.5 and 46; 200 rows of 131072 27 whole or in two and 25 in six.
+// launch and a part ends in a search of its own, which only long rows pay for.
+// Whole / in parts, us, k = 5, blocks of 16 bytes in a row:
+//   up to 48 rows: 1 row of 2000 blocks 8.4 / 11.3, 4000 10.1 / 11.3, 6250 12.4 /
+//     11.4, 16384 22 / 11.5; 48 rows of 4000 11.6 / 12.7, 6250 15.6 / 14.2
+//   100 rows of 12500, k = 1, 21.0 / 17.6; 128 rows of 8192 16.8 / 16.2 (masked 18.8 /
+//     22.8), 16384 fp32 22.8 / 19.9; 200 of 8192 17.1 / 18.9, 12500 21.2 / 22.9, 16384
+//     fp32 26.7 / 25.0; 240 of 16384 31.0 / 27.1 (k = 10)
+//   512 rows of 16384, k = 20, 40.3 / 43.3; 1000 of 12500, k = 1, 46.3 / 56.7
 static LpPlan lp_plan(int64_t n_rows, int64_t vocab, int64_t k, int es) {
   const int64_t blocks = cdiv(vocab * es, 16) + 1;   // a row that starts inside a block has one more
   int64_t parts = 1;
-  if (n_rows < 256) parts = std::min<int64_t>(cdiv(1024, std::max<int64_t>(n_rows, 1)), blocks / 512);
+  if (n_rows < 256 && blocks > std::min<int64_t>(std::max<int64_t>(4096, 80 * n_rows), 12800))
+    parts = std::min<int64_t>(cdiv(1024, std::max<int64_t>(n_rows, 1)), blocks / 512);
   parts = std::min<int64_t>(parts, std::min<int64_t>(64, 4096 / std::max<int64_t>(k, 1)));
   parts = std::max<int64_t>(parts, std::max<int64_t>(cdiv(blocks, kLpMaxBlocks), 1));
   LpPlan p;
