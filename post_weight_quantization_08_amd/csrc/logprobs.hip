@@ -20,8 +20,8 @@
 // bound sorted by (value, index).
 //
 // Bound by memory: 2 or 4 bytes and about 6 operations, one exponential, per
-// logit.  4096 rows of 131072 bf16, k = 64: 220 us, 4.9 TB/s of logits; 1000 of
-// 50021 fp32, k = 1: 46 us, 4.3 TB/s.  One row of 131072: 12.6 us in two launches,
+// logit.  4096 rows of 131072 bf16, k = 64: 213 us, 5.0 TB/s of logits; 1000 of
+// 50021 fp32, k = 1: 44 us, 4.5 TB/s.  One row of 131072: 12.3 us in two launches,
 // of which the reading is a small part.
 #include "answer.h"
 
@@ -260,7 +260,7 @@ __device__ void lp_walk(const LpArgs& a, const Blocks<kDt>& bl, int b0, int b1, 
 
 // One workgroup per part of a row: sums, then the part's best.  Seven
 // workgroups fit a CU's LDS; rows of fp32 are held to the registers for that
-// (1500 rows of 50021, k = 1: 62.8 -> 57 us).
+// (1500 rows of 50021, k = 1: 72 -> 67 us).
 template <int kDt, bool kTop, int kGs, bool kSplit>
 __global__ __launch_bounds__(kLpThreads, kDt == GPTQ_F32 && !kSplit ? 7 : 1) void logprobs_kernel(LpArgs a) {
   __shared__ LpShared sh;
@@ -539,7 +539,8 @@ struct LpPlan {
 // Parts of a row: one workgroup per row when that gives every CU one, else
 // enough parts for four, of at least two blocks a lane.  The join is a second
 // launch and a part ends in a search of its own, which only long rows pay for.
-// Whole / in parts, us, k = 5, blocks of 16 bytes in a row:
+// Whole / in parts, us, k = 5, blocks of 16 bytes in a row (calls on a few inputs
+// in turn, recorded in a graph; 1000 rows of 50021 fp32 take 46 us there):
 //   up to 48 rows: 1 row of 2000 blocks 8.4 / 11.3, 4000 10.1 / 11.3, 6250 12.4 /
 //     11.4, 16384 22 / 11.5; 48 rows of 4000 11.6 / 12.7, 6250 15.6 / 14.2
 //   100 rows of 12500, k = 1, 21.0 / 17.6; 128 rows of 8192 16.8 / 16.2 (masked 18.8 /

@@ -22,9 +22,9 @@
 // with 64: base and Y move in pieces of 256 (fp32) or 128 bytes, at any alignment.
 //
 // Bound by memory: X, base and Y once, the factors from L2 (a factor's matrix
-// serves every tile of its adapter).  8192 x 11008 -> 4096, rank 64, fp32 base in
-// place: 153 us, 76 for each product, 3.0 TB/s over both.  300 x 4096 -> 14336,
-// rank 32, 16-bit: 20 us, two launches that the first loads' latency fills.
+// serves every tile of its adapter).  8192 x 11008 -> 4096, rank 64, fp32 base:
+// 143 us, 75 and 70 for the products, 3.2 TB/s over both.  300 x 4096 -> 14336,
+// rank 32, 16-bit: 18 us, two launches that the first loads' latency fills.
 #include <type_traits>
 
 #include "lora.h"

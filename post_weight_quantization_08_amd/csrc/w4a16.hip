@@ -343,16 +343,16 @@ __global__ __launch_bounds__(64 * kW) void w4_main_kernel(W4Args a) {
 // order.  A token's 256-byte row of a stage keeps its 16-byte unit u at slot
 // u ^ (token % 16), so that the 16 tokens of a fragment read lie in 16 slots.
 // One tile a wave and up to eight waves, two to a SIMD, rather than two tiles
-// and four waves, and an adapter's loads asked for without a branch: 95 -> 67 us
-// at 48 tokens of 28672 x 8192 with 32 adapters of rank 16 (117 MB of codes,
-// 2.5 TB/s of all it reads).  Half of a wave's time there is waiting at the
+// and four waves, and an adapter's loads asked for without a branch: 95 -> 66 us
+// (the call 69) at 48 tokens of 28672 x 8192 with 32 adapters of rank 16 (117 MB of
+// codes, 2.5 TB/s of all it reads).  Half of a wave's time there is waiting at the
 // stages; LDS is busy 31 % of it, VALU 29, MFMA 13.  Activations laid out chunk
 // by chunk and slots without any bank conflict changed nothing.
 constexpr int kW4Ring = 6;
 
 // bytes of a row's scales and zeros in LDS
 __host__ __device__ constexpr int w4_wide_pitch(int ng) { return (3 * ng + 3) / 4 * 4 + 4; }
-constexpr int kW4WideParams = 40960;    // LDS bytes for them
+constexpr int kW4WideParams = 40960;    // LDS bytes for them; d_in above 26000 in groups of 128 takes the other kernel
 
 template <int kDt, int kMT, int kMost, bool kLora>
 __global__ __launch_bounds__(64 * kMost, 1) void w4_wide_kernel(W4Args a) {
