@@ -52,7 +52,9 @@ typedef enum {
   GPTQ_ENOMEM = 5         /* workspace smaller than gptq_workspace_size() */
 } gptq_status;
 
-typedef enum { GPTQ_F32 = 0, GPTQ_F16 = 1, GPTQ_BF16 = 2 } gptq_dtype;
+/* GPTQ_E4M3: codes with block scales as gptq_fp8_quantize writes them; taken only
+ * where a call says so. */
+typedef enum { GPTQ_F32 = 0, GPTQ_F16 = 1, GPTQ_BF16 = 2, GPTQ_E4M3 = 3 } gptq_dtype;
 
 typedef enum {
   GPTQ_OP_HESSIAN = 0,
@@ -66,7 +68,8 @@ typedef enum {
   GPTQ_OP_LOGPROBS = 8,
   GPTQ_OP_DISTILL = 9,
   GPTQ_OP_LORA = 10,
-  GPTQ_OP_W4A16_LORA = 11
+  GPTQ_OP_W4A16_LORA = 11,
+  GPTQ_OP_FP8_MATMUL = 12
 } gptq_op;
 
 /* Quantizer and schedule parameters.
@@ -128,6 +131,7 @@ const char* gptq_status_string(int32_t status);
  *   GPTQ_OP_LOGPROBS: d_in = vocab, n_rows, batch = max(k, 1).
  *   GPTQ_OP_DISTILL:  d_in = vocab, n_rows, batch = k.
  *   GPTQ_OP_LORA, GPTQ_OP_W4A16_LORA: d_out, d_in, n_rows = M, batch = rank.
+ *   GPTQ_OP_FP8_MATMUL: d_out, d_in, n_rows = M.
  * Unused arguments are ignored (p may be NULL except for GPTQ_OP_QUANTIZE).
  * Writes *bytes_out (host). */
 gptq_status gptq_workspace_size(int32_t op, const gptq_params* p, int64_t d_out, int64_t d_in,
@@ -491,6 +495,59 @@ gptq_status gptq_w4a16_lora_matmul(const void* X, int32_t x_dtype, int64_t M, in
                                    const int32_t* adapter, float* Y, int64_t ld_y, void* workspace, size_t ws_bytes,
                                    void* stream);
 
+/* Numbers in 8 bits: e4m3 codes (OCP FP8, one byte, largest 448) with one
+ * power-of-two scale for each block of 128, an E8M0 byte b that stands for
+ * 2^(b - 127).
+ *
+ *   block_rows = 1: a block is 128 consecutive elements of a row (activations).
+ *   block_rows = 128: a block is a 128 x 128 tile (weights).
+ *   b = the smallest byte >= 27 with max |x| <= 448 * 2^(b - 127);
+ *   code = x 2^(127 - b) rounded to the nearest e4m3, ties to even.
+ *   A block that holds a NaN or an infinity has b = 255 and NaN for every code.
+ *
+ *   X         device, rows x cols of x_dtype (GPTQ_F32, GPTQ_F16, GPTQ_BF16), row
+ *             stride ld_x; only the elements' own alignment is required.
+ *   codes     device uint8, rows x ld_c, 16-byte aligned, ld_c a multiple of 16 and
+ *             at least cols rounded up to whole blocks; columns from cols to there
+ *             are written as 0 (the code of 0; NaN in a block with b = 255).
+ *   scales    device uint8 [rows][blocks] (block_rows 1) or [ceil(rows / 128)][blocks],
+ *             blocks = ceil(cols / 128); dense.
+ *   codes_t, scales_t  device, or both NULL: the transpose, for block_rows = 128:
+ *             codes cols x ld_ct (rows rounded up to whole blocks, written as 0 behind
+ *             rows), scales [blocks][ceil(rows / 128)].  A tile has one scale both
+ *             ways, so these are the same numbers.
+ * rows * blocks < 2^30 (else GPTQ_EUNSUPPORTED).  rows = 0 does nothing. */
+gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                              int32_t block_rows, uint8_t* codes, int64_t ld_c, uint8_t* scales, uint8_t* codes_t,
+                              int64_t ld_ct, uint8_t* scales_t, void* stream);
+
+/* Product of numbers in 8 bits:
+ *   Y[m][n] = sum_k x[m][k] w[n][k],   x, w what codes and scales stand for.
+ *
+ *   X         GPTQ_E4M3: codes M x d_in, d_in a multiple of 128, 16-byte aligned with
+ *             ld_x a multiple of 16, x_scales [M][d_in / 128].  Other types: M x d_in
+ *             values, any d_in and stride, quantized in the call exactly as
+ *             gptq_fp8_quantize does with block_rows = 1 (x_scales is not read).
+ *   W         device codes d_out x d_in rounded up to whole blocks, 16-byte aligned,
+ *             ld_w a multiple of 16; w_scales [ceil(d_out / 128)][blocks]
+ *             (block_rows = 128).  Codes behind d_in have to be 0.
+ *   Y         device, M x d_out of y_dtype (GPTQ_F32, GPTQ_F16, GPTQ_BF16), row stride
+ *             ld_y; must not overlap the inputs or the workspace.
+ *   workspace GPTQ_OP_FP8_MATMUL bytes, 256-byte aligned; may be NULL when that size
+ *             is 0; calls sharing one workspace must be stream-ordered.
+ * Y in fp32: products exact, fp32 accumulation.  Y in 16 bits: the matrix unit's 8-bit
+ * products, which are added up eight at a time with every product cut off below 2^-13
+ * of the largest of the eight, then in fp32; Y is rounded once (the cutting is about
+ * 3e-5 of a result, half a step of fp16 5e-4).  Scale bytes are those that
+ * gptq_fp8_quantize writes, and no |x| or |w| above 2^127.  A token's outputs are NaN where its codes or
+ * a row of weights hold a NaN; others do not see it.  Results are bitwise reproducible
+ * for given sizes.  M, d_in, d_out <= 2^22 (more: GPTQ_EUNSUPPORTED).  M = 0 does
+ * nothing.  The input's gradient is the same call on the output's gradient with
+ * the transpose of the weights. */
+gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_scales, int64_t M, int64_t d_in,
+                            int64_t ld_x, const uint8_t* W, int64_t ld_w, const uint8_t* w_scales, int64_t d_out,
+                            void* Y, int32_t y_dtype, int64_t ld_y, void* workspace, size_t ws_bytes, void* stream);
+
 /* Reference rates for measurement (not part of the quantization path): the
  * published peaks of a GPU are not what it sustains under a given load, so
  * the benchmark also measures two simple kernels on the same device.  Both
@@ -521,7 +578,8 @@ gptq_status gptq_probe_copy(const void* src, void* dst, size_t bytes, double* gb
  * 6 = working-copy preparation, 7 = reduction of split Hessian partials,
  * 8 / 9 = W4A16 staging / main kernel, 10 = |x| sums, 11 = scale search,
  * 12 = scale application, 13 = layer forward, 14 = token log probabilities,
- * 15 = distillation, 16 = low-rank adapters).  gptq_timing_read synchronizes those events
+ * 15 = distillation, 16 = low-rank adapters, 17 = quantizing to 8 bits, 18 = products
+ * of 8-bit numbers).  gptq_timing_read synchronizes those events
  * and reports the summed duration (ms) and launch count of `kind`; reset
  * drops all records.  Not thread safe; off by default. */
 gptq_status gptq_timing_enable(int32_t on);

@@ -23,25 +23,27 @@ __all__ = [
     "gptq_abs_accumulate", "gptq_awq_search", "gptq_awq_apply", "gptq_layer_forward",
     "gptq_probe_mfma", "gptq_probe_copy", "gptq_probe_sink_bytes", "gptq_w4a16_matmul_noalloc",
     "gptq_token_logprobs", "gptq_distill_topk", "gptq_lora_add", "gptq_w4a16_lora_matmul",
+    "gptq_fp8_quantize", "gptq_fp8_matmul",
     "ACT_NONE", "ACT_RELU", "ACT_SILU",
     "OP_HESSIAN", "OP_PREPARE", "OP_QUANTIZE", "OP_W4A16", "OP_ABS", "OP_AWQ_SEARCH", "OP_FORWARD",
-    "OP_LOGPROBS", "OP_DISTILL", "OP_LORA", "OP_W4A16_LORA",
+    "OP_LOGPROBS", "OP_DISTILL", "OP_LORA", "OP_W4A16_LORA", "OP_FP8_MATMUL",
     "TIME_SYRK", "TIME_DIAG", "TIME_FACTOR", "TIME_BLOCK_QUANT", "TIME_TRAILING",
     "TIME_PACK", "TIME_PREP", "TIME_SYRK_REDUCE", "TIME_W4_STAGE", "TIME_W4_MAIN", "TIME_ABS",
     "TIME_AWQ_SEARCH", "TIME_AWQ_APPLY", "TIME_FORWARD", "TIME_LOGPROBS", "TIME_DISTILL", "TIME_LORA",
+    "TIME_FP8", "TIME_FP8_MATMUL",
     "dtype_code", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
 
 OK, EINVAL, ENOTPD, EHIP, EUNSUPPORTED, ENOMEM = range(6)
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, E4M3 = 0, 1, 2, 3
 OP_HESSIAN, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_ABS, OP_AWQ_SEARCH, OP_FORWARD = 0, 1, 2, 3, 4, 5, 6
-OP_LOGPROBS, OP_DISTILL, OP_LORA, OP_W4A16_LORA = 8, 9, 10, 11
+OP_LOGPROBS, OP_DISTILL, OP_LORA, OP_W4A16_LORA, OP_FP8_MATMUL = 8, 9, 10, 11, 12
 ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2
 (TIME_SYRK, TIME_DIAG, TIME_FACTOR, TIME_BLOCK_QUANT, TIME_TRAILING, TIME_PACK, TIME_PREP,
  TIME_SYRK_REDUCE, TIME_W4_STAGE, TIME_W4_MAIN, TIME_ABS, TIME_AWQ_SEARCH, TIME_AWQ_APPLY, TIME_FORWARD,
- TIME_LOGPROBS, TIME_DISTILL, TIME_LORA) = range(17)
+ TIME_LOGPROBS, TIME_DISTILL, TIME_LORA, TIME_FP8, TIME_FP8_MATMUL) = range(19)
 
 
 class GptqError(RuntimeError):
@@ -115,6 +117,10 @@ def _load() -> ctypes.CDLL:
     L.gptq_w4a16_lora_matmul.restype = i32
     L.gptq_w4a16_lora_matmul.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, i32, vp, vp, i64, i32, vp, vp,
                                          vp, i64, vp, sz, vp]
+    L.gptq_fp8_quantize.restype = i32
+    L.gptq_fp8_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp]
+    L.gptq_fp8_matmul.restype = i32
+    L.gptq_fp8_matmul.argtypes = [vp, i32, vp, i64, i64, i64, vp, i64, vp, i64, vp, i32, i64, vp, sz, vp]
     L.gptq_timing_enable.restype = i32
     L.gptq_timing_enable.argtypes = [i32]
     L.gptq_timing_reset.restype = i32
@@ -323,6 +329,20 @@ def gptq_w4a16_lora_matmul(X, x_dtype: int, M: int, d_in: int, ld_x: int, qweigh
                                       _ptr(perm), d_out, group_size, _ptr(A), _ptr(B), n_adapters, rank, _ptr(scale),
                                       _ptr(adapter), _ptr(Y), ld_y, _ptr(workspace), ws_bytes, _stream(stream)),
            "gptq_w4a16_lora_matmul")
+
+
+def gptq_fp8_quantize(X, x_dtype: int, rows: int, cols: int, ld_x: int, block_rows: int, codes, ld_c: int, scales,
+                      codes_t=None, ld_ct: int = 0, scales_t=None, stream=None) -> None:
+    """e4m3 codes with a power-of-two scale for each 1 x 128 or 128 x 128 block, and the tiles' transpose."""
+    _check(lib.gptq_fp8_quantize(_ptr(X), x_dtype, rows, cols, ld_x, block_rows, _ptr(codes), ld_c, _ptr(scales),
+                                 _ptr(codes_t), ld_ct, _ptr(scales_t), _stream(stream)), "gptq_fp8_quantize")
+
+
+def gptq_fp8_matmul(X, x_dtype: int, x_scales, M: int, d_in: int, ld_x: int, W, ld_w: int, w_scales, d_out: int, Y,
+                    y_dtype: int, ld_y: int, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    """Y = X W^T of 8-bit numbers with block scales; X codes, or values that the call quantizes."""
+    _check(lib.gptq_fp8_matmul(_ptr(X), x_dtype, _ptr(x_scales), M, d_in, ld_x, _ptr(W), ld_w, _ptr(w_scales), d_out,
+                               _ptr(Y), y_dtype, ld_y, _ptr(workspace), ws_bytes, _stream(stream)), "gptq_fp8_matmul")
 
 
 def gptq_timing_enable(on: bool) -> None:

@@ -60,7 +60,9 @@ enum TimedKind {
   kTimeLogprobs = 14,
   kTimeDistill = 15,
   kTimeLora = 16,
-  kTimeKinds = 17
+  kTimeFp8 = 17,
+  kTimeFp8Matmul = 18,
+  kTimeKinds = 19
 };
 
 // Records a start event before and a stop event after a launch when timing

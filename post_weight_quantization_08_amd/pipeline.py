@@ -11,8 +11,8 @@ from typing import Dict, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (BF16, F16, F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD, OP_HESSIAN,
-               OP_LOGPROBS, OP_LORA, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, _check, dtype_code,
+from . import (BF16, E4M3, F16, F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD,
+               OP_FP8_MATMUL, OP_HESSIAN, OP_LOGPROBS, OP_LORA, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, _check, dtype_code,
                gptq_abs_accumulate, gptq_awq_apply, gptq_awq_search, gptq_hessian_accumulate, gptq_layer_forward,
                gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv, gptq_quantize_layer,
                gptq_w4a16_matmul, gptq_workspace_size, lib)
@@ -452,6 +452,102 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     _call(lib.gptq_w4a16_lora_matmul, "gptq_w4a16_lora_matmul", device, X.data_ptr(), _DTYPE.get(dtype, -1), M, d_in,
           ld_x, pq, psc, pz, pp, d_out, group_size, pa, pb, n, r, ps, pad, py, ld_y, at, nbytes,
           _stream_of(stream, device))
+    return Y
+
+
+# ---------------------------------------------------------------- 8-bit numbers with block scales
+_CODES, _BYTES = torch.float8_e4m3fn, torch.float8_e8m0fnu
+F8_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+def _fp8_out(rows: int, cols: int, dev, tiles: bool) -> Buffers:
+    nb, rt = _blocks(cols), _blocks(rows)
+    out = {"codes": torch.empty(rows, nb * F8_BLOCK, dtype=_CODES, device=dev),
+           "scales": torch.empty(rt if tiles else rows, nb, dtype=_BYTES, device=dev)}
+    if tiles:
+        out["codes_t"] = torch.empty(cols, rt * F8_BLOCK, dtype=_CODES, device=dev)
+        out["scales_t"] = torch.empty(nb, rt, dtype=_BYTES, device=dev)
+    return Buffers(("fp8", rows, cols, tiles, dev.index), out)
+
+
+def fp8_quantize_buffers(X: torch.Tensor, tiles: bool = False) -> Buffers:
+    """out of fp8_quantize calls with these sizes, to be kept from call to call."""
+    return _fp8_out(X.shape[0], X.shape[1], X.device, tiles)
+
+
+def _codes(t: torch.Tensor, rows: int, cols: int, what: str, device: int):
+    """(address, row stride) of a (rows, cols) tensor of codes on 16-byte rows."""
+    n, w, ld, on = _rows(t, what)
+    if t.dtype is not _CODES or (n, w, on) != (rows, cols, device) or ld % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{what}: a {_CODES} tensor of shape {(rows, cols)} with 16-byte aligned rows on GPU {device} "
+                         "is needed")
+    return t.data_ptr(), ld
+
+
+def fp8_quantize(X: torch.Tensor, tiles: bool = False, out: Optional[Dict[str, torch.Tensor]] = None,
+                 stream=None) -> Dict[str, torch.Tensor]:
+    """e4m3 codes of X's rows, padded with zeros to whole blocks of 128, and a power-of-two scale (E8M0) for each
+    block: 128 elements of a row, or with `tiles` (weights) 128 x 128 of them, then with the transpose as
+    "codes_t" and "scales_t" (left out of a given `out` without them)."""
+    rows, cols, ld_x, device = _rows(X, "X")
+    if out is None:
+        with _on(stream, X.device):
+            out = _fp8_out(rows, cols, X.device, tiles)
+    nb, rt = _blocks(cols), _blocks(rows)
+    ld_c, ld_ct, codes_t, scales_t = nb * F8_BLOCK, rt * F8_BLOCK, None, None
+    if type(out) is Buffers and out.key == ("fp8", rows, cols, tiles, device):
+        codes, scales = out.addresses[:2]
+        if tiles:
+            codes_t, scales_t = out.addresses[2:]
+    else:
+        codes, ld_c = _codes(out["codes"], rows, nb * F8_BLOCK, "codes", device)
+        scales = _dense(out["scales"], _BYTES, (rt if tiles else rows, nb), "scales", device)
+        if tiles and "codes_t" in out:
+            codes_t, ld_ct = _codes(out["codes_t"], cols, rt * F8_BLOCK, "codes_t", device)
+            scales_t = _dense(out["scales_t"], _BYTES, (nb, rt), "scales_t", device)
+    _call(lib.gptq_fp8_quantize, "gptq_fp8_quantize", device, X.data_ptr(), _DTYPE.get(X.dtype, -1), rows, cols, ld_x,
+          F8_BLOCK if tiles else 1, codes, ld_c, scales, codes_t, ld_ct, scales_t, _stream_of(stream, device))
+    return out
+
+
+def fp8_matmul_buffers(X: torch.Tensor, W: torch.Tensor, y_dtype=torch.float32):
+    """(Y, ws) of fp8_matmul calls with these sizes, to be kept from call to call."""
+    return (torch.empty(X.shape[0], W.shape[0], dtype=y_dtype, device=X.device),
+            _ws(gptq_workspace_size(OP_FP8_MATMUL, None, W.shape[0], X.shape[1], X.shape[0], 1), X.device))
+
+
+def fp8_matmul(X: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
+               Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, y_dtype=torch.float32,
+               stream=None) -> torch.Tensor:
+    """Y = X W^T.  W: codes (d_out, d_in padded to whole blocks) with the scales of 128 x 128 tiles.  X: codes with
+    x_scales (M, blocks), or fp32, fp16 or bf16 values (M, d_in) that the call quantizes as fp8_quantize does.  Y has
+    the type y_dtype unless it is given.  The input's gradient: the same call with the transposed weights."""
+    M, d_in, ld_x, device = _rows(X, "X")
+    d_out, nb = W.shape[0], _blocks(d_in)
+    pw, ld_w = _codes(W, d_out, nb * F8_BLOCK, "W", device)
+    psw = _dense(w_scales, _BYTES, (_blocks(d_out), nb), "w_scales", device)
+    px, psx, kind = X.data_ptr(), None, _DTYPE.get(X.dtype, -1)
+    if X.dtype is _CODES:
+        px, ld_x = _codes(X, M, d_in, "X", device)
+        if x_scales is None:
+            raise ValueError("x_scales: codes need their scales")
+        psx, kind = _dense(x_scales, _BYTES, (M, nb), "x_scales", device), E4M3
+    elif x_scales is not None:
+        raise ValueError("x_scales: only codes have scales")
+    if Y is None:
+        with _on(stream, X.device):
+            Y = torch.empty(M, d_out, dtype=y_dtype, device=X.device)
+    py, ld_y = _out_rows(Y, Y.dtype, M, d_out, "Y", device)
+    if ws is None:
+        with _on(stream, X.device):
+            ws = _ws(gptq_workspace_size(OP_FP8_MATMUL, None, d_out, d_in, M, 1), X.device)
+    at, nbytes = _workspace(ws, device)
+    _call(lib.gptq_fp8_matmul, "gptq_fp8_matmul", device, px, kind, psx, M, d_in, ld_x, pw, ld_w, psw, d_out, py,
+          _DTYPE.get(Y.dtype, -1), ld_y, at, nbytes, _stream_of(stream, device))
     return Y
 
 
