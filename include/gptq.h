@@ -69,7 +69,8 @@ typedef enum {
   GPTQ_OP_DISTILL = 9,
   GPTQ_OP_LORA = 10,
   GPTQ_OP_W4A16_LORA = 11,
-  GPTQ_OP_FP8_MATMUL = 12
+  GPTQ_OP_FP8_MATMUL = 12,
+  GPTQ_OP_POLICY = 13
 } gptq_op;
 
 /* Quantizer and schedule parameters.
@@ -132,6 +133,7 @@ const char* gptq_status_string(int32_t status);
  *   GPTQ_OP_DISTILL:  d_in = vocab, n_rows, batch = k.
  *   GPTQ_OP_LORA, GPTQ_OP_W4A16_LORA: d_out, d_in, n_rows = M, batch = rank.
  *   GPTQ_OP_FP8_MATMUL: d_out, d_in, n_rows = M.
+ *   GPTQ_OP_POLICY: d_in = vocab, n_rows.
  * Unused arguments are ignored (p may be NULL except for GPTQ_OP_QUANTIZE).
  * Writes *bytes_out (host). */
 gptq_status gptq_workspace_size(int32_t op, const gptq_params* p, int64_t d_out, int64_t d_in,
@@ -455,6 +457,46 @@ gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, int64_t n_row
                               int32_t tail, const float* weight, float* loss, void* grad, int64_t ld_g,
                               void* workspace, size_t ws_bytes, void* stream);
 
+/* Clipped policy loss with a KL term, for training on a model's own answers: loss of
+ * every row and, when grad is given, the gradient of sum_i weight[i] loss[i] with
+ * respect to the logits, in one call.  With z = x / T, t the row's answered token and
+ * l = z_t - log sum_j e^(z_j):
+ *
+ *   ratio = e^(l - old),   kl = e^(ref - l) - (ref - l) - 1   (0 without ref)
+ *   loss = -min(ratio A, clamp(ratio, 1 - clip_low, 1 + clip_high) A) + kl_coef kl
+ *   dloss/dl = (-ratio A where ratio A is the smaller or equal, else 0)
+ *              - kl_coef (e^(ref - l) - 1)
+ *   dloss/dx_j = dloss/dl ([j = t] - e^(z_j) / sum) / T
+ *
+ *   logits      device, n_rows x vocab of x_dtype, row stride ld_x; n_rows <= 2^22
+ *               (more: GPTQ_EINVAL), vocab <= 2^21 (more: GPTQ_EUNSUPPORTED); only the
+ *               elements' own alignment is required.
+ *   targets     device int32 [n_rows]; outside [0, vocab): a row that is not scored,
+ *               whose outputs and gradient are 0, whatever it holds.
+ *   old_logprob, advantage  device fp32 [n_rows]: the behaviour's log probabilities at
+ *               the same temperature, and A.
+ *   ref_logprob device fp32 [n_rows] or NULL (no KL term).
+ *   clip_low in [0, 1], clip_high and kl_coef in [0, 1e4], temperature in [1e-4, 1e4].
+ *   weight      device fp32 [n_rows] or NULL (all 1).  A row of weight 0 has gradient
+ *               0, whatever it holds.
+ *   loss        device fp32 [n_rows], not multiplied by weight.  logprob, ratio, kl:
+ *               device fp32 [n_rows]; any of them may be NULL.
+ *   grad        device, n_rows x vocab of x_dtype, row stride ld_g, each element
+ *               rounded once to x_dtype (nearest even); NULL = no gradient.  It may be
+ *               the logits' own buffer (grad == logits with ld_g == ld_x); otherwise it
+ *               must not overlap them.
+ *   workspace   GPTQ_OP_POLICY bytes, 256-byte aligned; may be NULL when that size is
+ *               0; calls sharing one workspace must be stream-ordered.
+ * Masked logits may be -inf or the type's lowest value.  A masked target (l = -inf)
+ * has ratio 0, with a reference kl +inf, and gradient 0.  A scored row that holds a
+ * NaN or +inf, or nothing above -inf, has NaN for every output (weight 0: gradient 0).
+ * fp32 sums, the row's own numbers in 64 bits; no floating-point atomics. */
+gptq_status gptq_policy_loss(const void* logits, int32_t x_dtype, int64_t n_rows, int64_t vocab, int64_t ld_x,
+                             const int32_t* targets, const float* old_logprob, const float* advantage,
+                             const float* ref_logprob, float clip_low, float clip_high, float kl_coef,
+                             float temperature, const float* weight, float* loss, float* logprob, float* ratio, float* kl,
+                             void* grad, int64_t ld_g, void* workspace, size_t ws_bytes, void* stream);
+
 /* Low-rank adapters of many requests beside a shared projection:
  *
  *   Y[m] = base[m] + scale[a] (X[m] A_a^T) B_a^T,   a = adapter[m].
@@ -579,7 +621,7 @@ gptq_status gptq_probe_copy(const void* src, void* dst, size_t bytes, double* gb
  * 8 / 9 = W4A16 staging / main kernel, 10 = |x| sums, 11 = scale search,
  * 12 = scale application, 13 = layer forward, 14 = token log probabilities,
  * 15 = distillation, 16 = low-rank adapters, 17 = quantizing to 8 bits, 18 = products
- * of 8-bit numbers).  gptq_timing_read synchronizes those events
+ * of 8-bit numbers, 19 = policy loss).  gptq_timing_read synchronizes those events
  * and reports the summed duration (ms) and launch count of `kind`; reset
  * drops all records.  Not thread safe; off by default. */
 gptq_status gptq_timing_enable(int32_t on);

@@ -23,14 +23,14 @@ __all__ = [
     "gptq_abs_accumulate", "gptq_awq_search", "gptq_awq_apply", "gptq_layer_forward",
     "gptq_probe_mfma", "gptq_probe_copy", "gptq_probe_sink_bytes", "gptq_w4a16_matmul_noalloc",
     "gptq_token_logprobs", "gptq_distill_topk", "gptq_lora_add", "gptq_w4a16_lora_matmul",
-    "gptq_fp8_quantize", "gptq_fp8_matmul",
+    "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_policy_loss",
     "ACT_NONE", "ACT_RELU", "ACT_SILU",
     "OP_HESSIAN", "OP_PREPARE", "OP_QUANTIZE", "OP_W4A16", "OP_ABS", "OP_AWQ_SEARCH", "OP_FORWARD",
-    "OP_LOGPROBS", "OP_DISTILL", "OP_LORA", "OP_W4A16_LORA", "OP_FP8_MATMUL",
+    "OP_LOGPROBS", "OP_DISTILL", "OP_LORA", "OP_W4A16_LORA", "OP_FP8_MATMUL", "OP_POLICY",
     "TIME_SYRK", "TIME_DIAG", "TIME_FACTOR", "TIME_BLOCK_QUANT", "TIME_TRAILING",
     "TIME_PACK", "TIME_PREP", "TIME_SYRK_REDUCE", "TIME_W4_STAGE", "TIME_W4_MAIN", "TIME_ABS",
     "TIME_AWQ_SEARCH", "TIME_AWQ_APPLY", "TIME_FORWARD", "TIME_LOGPROBS", "TIME_DISTILL", "TIME_LORA",
-    "TIME_FP8", "TIME_FP8_MATMUL",
+    "TIME_FP8", "TIME_FP8_MATMUL", "TIME_POLICY", "TIME_LORA_GRAD",
     "dtype_code", "LIB_PATH",
 ]
 
@@ -39,11 +39,11 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so"
 OK, EINVAL, ENOTPD, EHIP, EUNSUPPORTED, ENOMEM = range(6)
 F32, F16, BF16, E4M3 = 0, 1, 2, 3
 OP_HESSIAN, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_ABS, OP_AWQ_SEARCH, OP_FORWARD = 0, 1, 2, 3, 4, 5, 6
-OP_LOGPROBS, OP_DISTILL, OP_LORA, OP_W4A16_LORA, OP_FP8_MATMUL = 8, 9, 10, 11, 12
+OP_LOGPROBS, OP_DISTILL, OP_LORA, OP_W4A16_LORA, OP_FP8_MATMUL, OP_POLICY = 8, 9, 10, 11, 12, 13
 ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2
 (TIME_SYRK, TIME_DIAG, TIME_FACTOR, TIME_BLOCK_QUANT, TIME_TRAILING, TIME_PACK, TIME_PREP,
  TIME_SYRK_REDUCE, TIME_W4_STAGE, TIME_W4_MAIN, TIME_ABS, TIME_AWQ_SEARCH, TIME_AWQ_APPLY, TIME_FORWARD,
- TIME_LOGPROBS, TIME_DISTILL, TIME_LORA, TIME_FP8, TIME_FP8_MATMUL) = range(19)
+ TIME_LOGPROBS, TIME_DISTILL, TIME_LORA, TIME_FP8, TIME_FP8_MATMUL, TIME_POLICY, TIME_LORA_GRAD) = range(21)
 
 
 class GptqError(RuntimeError):
@@ -121,6 +121,9 @@ def _load() -> ctypes.CDLL:
     L.gptq_fp8_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp]
     L.gptq_fp8_matmul.restype = i32
     L.gptq_fp8_matmul.argtypes = [vp, i32, vp, i64, i64, i64, vp, i64, vp, i64, vp, i32, i64, vp, sz, vp]
+    L.gptq_policy_loss.restype = i32
+    L.gptq_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, vp,
+                                   i64, vp, sz, vp]
     L.gptq_timing_enable.restype = i32
     L.gptq_timing_enable.argtypes = [i32]
     L.gptq_timing_reset.restype = i32
@@ -343,6 +346,16 @@ def gptq_fp8_matmul(X, x_dtype: int, x_scales, M: int, d_in: int, ld_x: int, W, 
     """Y = X W^T of 8-bit numbers with block scales; X codes, or values that the call quantizes."""
     _check(lib.gptq_fp8_matmul(_ptr(X), x_dtype, _ptr(x_scales), M, d_in, ld_x, _ptr(W), ld_w, _ptr(w_scales), d_out,
                                _ptr(Y), y_dtype, ld_y, _ptr(workspace), ws_bytes, _stream(stream)), "gptq_fp8_matmul")
+
+
+def gptq_policy_loss(logits, x_dtype: int, n_rows: int, vocab: int, ld_x: int, targets, old_logprob, advantage,
+                     ref_logprob, clip_low: float, clip_high: float, kl_coef: float, temperature: float, weight, loss,
+                     logprob, ratio, kl, grad, ld_g: int, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    """Clipped policy loss with a KL term of every row and the gradient of sum(weight * loss)."""
+    _check(lib.gptq_policy_loss(_ptr(logits), x_dtype, n_rows, vocab, ld_x, _ptr(targets), _ptr(old_logprob),
+                                _ptr(advantage), _ptr(ref_logprob), clip_low, clip_high, kl_coef, temperature,
+                                _ptr(weight), _ptr(loss), _ptr(logprob), _ptr(ratio), _ptr(kl), _ptr(grad), ld_g,
+                                _ptr(workspace), ws_bytes, _stream(stream)), "gptq_policy_loss")
 
 
 def gptq_timing_enable(on: bool) -> None:

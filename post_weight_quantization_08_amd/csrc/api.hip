@@ -15,6 +15,7 @@ size_t distill_workspace_bytes(int64_t n_rows, int64_t vocab, int64_t k);
 size_t lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank);
 size_t w4a16_lora_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int64_t rank);
 size_t fp8_matmul_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out);
+size_t policy_workspace_bytes(int64_t n_rows, int64_t vocab);
 
 // ---------------------------------------------------------------- timing state
 namespace {
@@ -125,6 +126,10 @@ extern "C" gptq_status gptq_workspace_size(int32_t op, const gptq_params* p, int
     case GPTQ_OP_FP8_MATMUL:
       GQ_CHECK_ARG(n_rows >= 0 && d_out >= 1);
       *bytes_out = fp8_matmul_workspace_bytes(n_rows, d_in, d_out);
+      return GPTQ_OK;
+    case GPTQ_OP_POLICY:
+      GQ_CHECK_ARG(n_rows >= 0);
+      *bytes_out = policy_workspace_bytes(n_rows, d_in);
       return GPTQ_OK;
     default:
       return GPTQ_EINVAL;

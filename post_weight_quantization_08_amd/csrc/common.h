@@ -62,7 +62,9 @@ enum TimedKind {
   kTimeLora = 16,
   kTimeFp8 = 17,
   kTimeFp8Matmul = 18,
-  kTimeKinds = 19
+  kTimePolicy = 19,
+  kTimeLoraGrad = 20,
+  kTimeKinds = 21
 };
 
 // Records a start event before and a stop event after a launch when timing

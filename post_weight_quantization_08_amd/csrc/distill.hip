@@ -29,16 +29,11 @@
 // 4.6 TB/s read and written; 2048 rows of 32000 bf16, loss alone, 34.5 us, 3.8
 // TB/s, where the workgroups' sums between two rows show; 777 odd rows of
 // 50021 fp16 48 us, 3.2 TB/s: 512 workgroups, of which half take a second row.
-#include "answer.h"
+#include "rows.h"
 
 namespace gq {
 
 constexpr int kDsMaxK = 128;
-
-// References as in the log probabilities: none below the floor (a power of
-// two), a new one when a term would exceed 2^8, another way when r c is so
-// large that its rounding matters.
-constexpr float kDsFloor = -1048576.f, kDsFast = 268435456.f, kDsLag = 8.f;
 
 struct DsArgs {
   const void* x;
@@ -75,85 +70,6 @@ struct DsFinal {
   int zero, nan, bad;
 };
 
-// A row as `head` single logits, `blocks` 16-byte blocks on 16-byte addresses
-// and `rest` single logits.
-template <int kDt>
-struct Span {
-  static constexpr int E = kDt == GPTQ_F32 ? 4 : 8;
-  static constexpr int kSize = 16 / E;
-  const char* p;           // first element
-  int head, blocks, rest;
-  __device__ __forceinline__ Span(const void* x, int64_t row, int64_t ld, int vocab) {
-    p = static_cast<const char*>(x) + row * ld * kSize;
-    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15) / kSize;
-    head = min(vocab, off ? E - off : 0);
-    blocks = (vocab - head) / E;
-    rest = vocab - head - blocks * E;
-  }
-  // block first + lane, `first` the same in every lane
-  __device__ __forceinline__ u32x4 load(int first, int lane) const {
-    return *reinterpret_cast<const u32x4*>(p + head * kSize + (int64_t)first * 16 + (uint32_t)lane * 16u);
-  }
-  // the single logit of thread t (threads 0..7 the head's, 8..15 the rest's), or -1
-  __device__ __forceinline__ int edge(int t) const {
-    if (t < 8) return t < head ? t : -1;
-    return t < 16 && t - 8 < rest ? head + blocks * E + t - 8 : -1;
-  }
-};
-
-template <int kDt>
-__device__ __forceinline__ u32x4 masked_block() {
-  const uint32_t w = kDt == GPTQ_F32 ? 0xFF800000u : kDt == GPTQ_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-  return u32x4{w, w, w, w};
-}
-
-template <int kDt>
-__device__ __forceinline__ u32x4 pack_block(const float (&g)[Span<kDt>::E]) {
-  u32x4 w;
-  if constexpr (kDt == GPTQ_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(g[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kDt == GPTQ_BF16) {
-        uint32_t h;   // two roundings to nearest even in one instruction
-        asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(h) : "v"(g[2 * i]), "v"(g[2 * i + 1]));
-        w[i] = h;
-      } else {
-        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-        const f16x2 h = {(_Float16)g[2 * i], (_Float16)g[2 * i + 1]};
-        w[i] = __builtin_bit_cast(uint32_t, h);
-      }
-    }
-  }
-  return w;
-}
-
-// Where a lane reads that has no block to read: every load is made, so that
-// the compiler can count the ones behind it and wait for one block at a time.
-static __device__ u32x4 ds_pad[1];
-
-// Blocks of a span as a lane reads them: block first + lane, or the last one
-// in its place (or the pad, if there is none).
-template <int kDt>
-struct DsSource {
-  const char* base;
-  uint32_t last, lane;     // byte offsets: of the last block, of the lane's first
-  __device__ __forceinline__ DsSource(const Span<kDt>& sp, bool real) {
-    const bool any = real && sp.blocks > 0;
-    base = any ? sp.p + sp.head * Span<kDt>::kSize : reinterpret_cast<const char*>(ds_pad);
-    last = any ? (uint32_t)(sp.blocks - 1) * 16u : 0u;
-    lane = threadIdx.x * 16u;
-    asm volatile("" : "+v"(lane));   // a row's own value: offsets of all slots are not kept from row to row
-  }
-  __device__ __forceinline__ const u32x4* block(int first) const {
-    const uint32_t at = (uint32_t)first * 16u + lane;
-    return reinterpret_cast<const u32x4*>(base + (at < last ? at : last));
-  }
-  __device__ __forceinline__ u32x4 load(int first) const { return *block(first); }
-};
-
 // LDS of a workgroup of T threads with W words of bits per lane.
 template <int T, int W>
 struct DsShared {
@@ -165,27 +81,6 @@ struct DsShared {
   float red[T / 64][2];
   DsFinal fin;
 };
-
-// Reference and sum joined over the workgroup; every thread gets them.
-template <int T, int W>
-__device__ __forceinline__ void ds_join(float& r, float& s, float c, DsShared<T, W>& sh) {
-  auto fmax2 = [](float p, float q) { return fmaxf(p, q); };
-  auto add2 = [](float p, float q) { return p + q; };
-  const float rw = wave_reduce(r, fmax2);
-  s = wave_reduce(s * exp2_hw((r - rw) * c), add2);
-  if ((threadIdx.x & 63) == 0) {
-    sh.red[threadIdx.x >> 6][0] = rw;
-    sh.red[threadIdx.x >> 6][1] = s;
-  }
-  lds_barrier();
-  static_assert(T / 64 <= 16, "a wave's partial per lane of sixteen");
-  const int w = threadIdx.x & (T / 64 - 1) & 15;
-  const float rl = sh.red[w][0], sl = sh.red[w][1];
-  r = uniform(row_reduce(rl, fmax2));
-  // every wave's partial stands 16 / (T / 64) times in a row of sixteen lanes
-  const float mine = (threadIdx.x & 15) < T / 64 ? sl * exp2_hw((rl - r) * c) : 0.f;
-  s = uniform(row_reduce(mine, add2));
-}
 
 // A thread's list entry of a row as read from memory.  Its logit stays as
 // loaded: looking at it would wait for it, and for everything loaded before.
@@ -364,14 +259,6 @@ struct DsRow {
   }
 };
 
-// ln x in 64 bits of a 32-bit x: the exponent apart, so that the logarithm of
-// a large sum keeps the digits that the loss is made of.
-__device__ __forceinline__ double ln_wide(float x) {
-  int e;
-  const float m = frexpf(x, &e);
-  return (double)e * 0.69314718055994530942 + (double)logf(m);
-}
-
 // loss of a row: sum p (log p - log q) over the list, p_r (log p_r - log q_r).
 __device__ __forceinline__ float ds_loss(const DsArgs& a, const DsList& l, const DsFinal& f, float r, float s) {
   if (l.count == 0.f) return 0.f;
@@ -424,46 +311,6 @@ __device__ __forceinline__ DsFinal ds_fetch(const DsFinal& g, float r) {
   return f;
 }
 
-// The rest's sum over what a lane holds.
-template <int kDt>
-__device__ __forceinline__ void ds_add_block(float& r, float& rc, float& s, const float (&v)[Span<kDt>::E], float c) {
-  constexpr int E = Span<kDt>::E;
-  float vm = fmaxf(v[0], v[1]);
-#pragma unroll
-  for (int e = 2; e < E; ++e) vm = fmaxf(vm, v[e]);
-  if (fmaf(vm, c, -rc) > kDsLag) {
-    // s stands at rc, not at r c: both roundings go into the move
-    const float skew = fmaf(vm, c, -(vm * c)) - fmaf(r, c, -rc);
-    s *= exp2_hw(fmaxf((r - vm) * c, -1e30f) + skew);
-    r = vm;
-    rc = vm * c;
-  }
-  float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    s0 += exp2_hw(fmaf(v[e], c, -rc));
-    s1 += exp2_hw(fmaf(v[e + 1], c, -rc));
-  }
-  s += s0 + s1;
-}
-
-// The block's logits.  The empty asm makes every use of a held block a value
-// of its own: without it the compiler keeps the unpacked logits of the sums
-// for the gradients, eight registers for every four held.
-template <int kDt>
-__device__ __forceinline__ void unpack_held(u32x4 w, float (&v)[Span<kDt>::E]) {
-  asm volatile("" : "+v"(w));
-  Blocks<kDt>::unpack(w, v);
-}
-
-template <int kDt>
-__device__ __forceinline__ void hide(float (&v)[Span<kDt>::E], uint32_t listed) {
-  if (listed) {
-#pragma unroll
-    for (int e = 0; e < Span<kDt>::E; ++e) v[e] = listed >> e & 1u ? -INFINITY : v[e];
-  }
-}
-
 // r, s of the rest among the workgroup's blocks, the slow way: around the true
 // maximum, differences taken before they are scaled.  Reads the row again, so
 // that the common way needs no registers for this.
@@ -512,7 +359,7 @@ __device__ __forceinline__ void ds_exact_sums(DsRow<kDt, T, NB>& d, const Span<k
     for (int e = 0; e < E; ++e) s += exp2_hw((v[e] - m) * d.a.c);
   }
   s += exp2_hw((xe - m) * d.a.c);
-  ds_join(r, s, d.a.c, sh);
+  ds_join<T>(r, s, d.a.c, sh.red);
 }
 
 // Gradients of n logits of the rest.  kFast: rc is r c rounded, `rest` made
@@ -546,21 +393,6 @@ __device__ __forceinline__ DsFix ds_fix(const DsRow<kDt, T, NB>& d, const DsFina
 template <int kDt>
 __device__ __forceinline__ void ds_store_fix(const DsArgs& a, int64_t row, const DsFix& x) {
   if (x.id >= 0) store_el<kDt>(a.grad, row * a.ld_g + x.id, x.g);
-}
-
-// Every memory operation of this wave is done.
-__device__ __forceinline__ void memory_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// A block's gradients, 16 bytes in one store wherever they start (the gradient's
-// rows need not start on their 16 bytes where the logits' do).
-template <int kDt>
-__device__ __forceinline__ void ds_store(const DsArgs& a, const Span<kDt>& sp, int64_t row, int first, int lane,
-                                         const float (&g)[Span<kDt>::E]) {
-  char* p = static_cast<char*>(a.grad) + (row * a.ld_g + sp.head) * Span<kDt>::kSize + (int64_t)first * 16 +
-            (uint32_t)lane * 16u;
-  const u32x4 w = pack_block<kDt>(g);
-  if constexpr (kDt == GPTQ_F32) __builtin_memcpy(__builtin_assume_aligned(p, 4), &w, 16);
-  else __builtin_memcpy(__builtin_assume_aligned(p, 2), &w, 16);
 }
 
 // Blocks a lane holds in registers; a row kernel's others lie in LDS, where
@@ -663,7 +495,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
     asm volatile("" : "+v"(ahead.id), "+v"(ahead.lp), "+v"(weight));
     d.read_logit(ahead, next);
     const uint32_t edge_ahead = d.read_edge(next);
-    ds_join(r, s, a.c, sh);
+    ds_join<T>(r, s, a.c, sh.red);
     if constexpr (kGrad) ds_store_fix<kDt>(a, fix_row, fix);
     // a rest of -inf alone, or out of the fast way's range
     const bool exact = !(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast);
@@ -692,7 +524,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
         for (int e = 0; e < E; ++e) g[e] = f.nan ? NAN : 0.f;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
+          if (t < sp.blocks - i * T) ds_store<kDt>(a.grad, a.ld_g, sp, row, i * T, t, g);
           if (i < kHeld) refill(src, i);
         }
         refill_tail(src);
@@ -705,7 +537,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
           if (i < kHeld) unpack_held<kDt>(w[i < kHeld ? i : 0], v);
           else Blocks<kDt>::unpack(tail[i < kHeld ? 0 : i - kHeld][t], v);
           ds_gradient<true>(f, rest, frc, a.c, v, g, E);
-          if (t < sp.blocks - i * T) ds_store<kDt>(a, sp, row, i * T, t, g);
+          if (t < sp.blocks - i * T) ds_store<kDt>(a.grad, a.ld_g, sp, row, i * T, t, g);
           if (i < kHeld) refill(src, i);
           __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
         }
@@ -717,7 +549,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_waves_per_eu(4))) void dis
           float v[E], g[E];
           Blocks<kDt>::unpack(sp.load(i * T, t), v);
           ds_gradient<false>(f, f.rest, 0.f, a.c, v, g, E);
-          ds_store<kDt>(a, sp, row, i * T, t, g);
+          ds_store<kDt>(a.grad, a.ld_g, sp, row, i * T, t, g);
         }
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) refill(src, i);
@@ -810,7 +642,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       ds_add_block<kDt>(r, rc, s, v, a.c);
     }
     s *= exp2_hw(-fmaf(r, a.c, -rc));
-    ds_join(r, s, a.c, sh);
+    ds_join<T>(r, s, a.c, sh.red);
     if (!(s > 0.f && s < INFINITY && fabsf(r) * a.c < kDsFast)) ds_exact_sums<kDt, T, NB>(d, sp, slot0, a.slots, xr, r, s, sh);
     if (t == 0) {
       float* o = a.ws_sums + (row * a.parts + part) * 2;
@@ -825,7 +657,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       s = (s == 0.f ? 0.f : s * exp2_hw((r - to) * a.c)) + (o[1] == 0.f ? 0.f : o[1] * exp2_hw((o[0] - to) * a.c));
       r = to;
     }
-    ds_join(r, s, a.c, sh);
+    ds_join<T>(r, s, a.c, sh.red);
     const float* o = a.ws_list + row * 8;
     const DsList list{o[0], o[1], o[2], o[3], o[5], *reinterpret_cast<const double*>(o + 6), o[4]};
     const DsFinal f = ds_final(a, a.weight ? a.weight[row] : 1.f, list, r, s);
@@ -843,7 +675,7 @@ __global__ __launch_bounds__(kDsPartThreads) void distill_part_kernel(DsArgs a) 
       float v[E], g[E];
       unpack_held<kDt>(w[i], v);
       ds_gradient<false>(f, f.rest, 0.f, a.c, v, g, E);
-      ds_store<kDt>(a, sp, row, first, t, g);
+      ds_store<kDt>(a.grad, a.ld_g, sp, row, first, t, g);
     }
     const DsFix fix = ds_fix<kDt, T, NB>(d, f);
     memory_done();

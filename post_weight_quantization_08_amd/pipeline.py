@@ -12,7 +12,7 @@ import numpy as np
 import torch
 
 from . import (BF16, E4M3, F16, F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD,
-               OP_FP8_MATMUL, OP_HESSIAN, OP_LOGPROBS, OP_LORA, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, _check, dtype_code,
+               OP_FP8_MATMUL, OP_HESSIAN, OP_LOGPROBS, OP_LORA, OP_POLICY, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, _check, dtype_code,
                gptq_abs_accumulate, gptq_awq_apply, gptq_awq_search, gptq_hessian_accumulate, gptq_layer_forward,
                gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv, gptq_quantize_layer,
                gptq_w4a16_matmul, gptq_workspace_size, lib)
@@ -363,6 +363,61 @@ def distill_topk(logits: torch.Tensor, top_id: torch.Tensor, top_logprob: torch.
     at, nbytes = _workspace(ws, device)
     _call(lib.gptq_distill_topk, "gptq_distill_topk", device, logits.data_ptr(), _DTYPE.get(dtype, -1), n, v, ld, ids,
           lps, k, temperature, bool(tail), weights, loss, grad, ld_g, at, nbytes, _stream_of(stream, device))
+    return out
+
+
+_POLICY = ("loss", "logprob", "ratio", "kl")
+
+
+def _policy_out(n: int, v: int, dtype, dev, want_grad: bool) -> Buffers:
+    out = {name: torch.empty(n, dtype=torch.float32, device=dev) for name in _POLICY}
+    if want_grad:
+        out["grad"] = torch.empty(n, v, dtype=dtype, device=dev)
+    return Buffers(("policy", n, v if want_grad else 0, dtype, dev.index), out)
+
+
+def policy_loss_buffers(logits: torch.Tensor, want_grad: bool = True):
+    """(out, ws) of policy_loss calls with these sizes, to be kept from call to call."""
+    n, v = logits.shape
+    return (_policy_out(n, v, logits.dtype, logits.device, want_grad),
+            _ws(gptq_workspace_size(OP_POLICY, None, 1, v, n, 1), logits.device))
+
+
+def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logprob: torch.Tensor, advantage: torch.Tensor,
+                ref_logprob: Optional[torch.Tensor] = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                kl_coef: float = 0.0, temperature: float = 1.0, weight: Optional[torch.Tensor] = None,
+                want_grad: bool = True, out: Optional[Dict[str, torch.Tensor]] = None,
+                ws: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Clipped policy loss of every row (answered tokens int32, outside the vocabulary: not scored; fp32 log
+    probabilities of the behaviour and the reference at the same temperature, as token_logprobs gives them) with its
+    log probability, ratio and KL term, and with want_grad the gradient of sum(weight * loss) in the logits' type.
+    out may hold the logits themselves as "grad": the gradient then replaces them."""
+    n, v, ld, device = _rows(logits, "logits")
+    dtype = logits.dtype
+    target = _dense(targets, torch.int32, (n,), "targets", device)
+    old = _dense(old_logprob, torch.float32, (n,), "old_logprob", device)
+    adv = _dense(advantage, torch.float32, (n,), "advantage", device)
+    ref = _dense(ref_logprob, torch.float32, (n,), "ref_logprob", device) if ref_logprob is not None else None
+    weights = _dense(weight, torch.float32, (n,), "weight", device) if weight is not None else None
+    if out is None:
+        with _on(stream, logits.device):
+            out = _policy_out(n, v, dtype, logits.device, want_grad)
+    ld_g, grad = v, None
+    if type(out) is Buffers and out.key == ("policy", n, v if want_grad else 0, dtype, device):
+        values = out.addresses[:4]
+        if want_grad:
+            grad = out.addresses[4]
+    else:
+        values = [_dense(out[name], torch.float32, (n,), name, device) for name in _POLICY]
+        if want_grad:
+            grad, ld_g = _out_rows(out["grad"], dtype, n, v, "grad", device)
+    if ws is None:
+        with _on(stream, logits.device):
+            ws = _ws(gptq_workspace_size(OP_POLICY, None, 1, v, n, 1), logits.device)
+    at, nbytes = _workspace(ws, device)
+    _call(lib.gptq_policy_loss, "gptq_policy_loss", device, logits.data_ptr(), _DTYPE.get(dtype, -1), n, v, ld, target,
+          old, adv, ref, clip_low, clip_high, kl_coef, temperature, weights, *values, grad, ld_g, at, nbytes,
+          _stream_of(stream, device))
     return out
 
 
