@@ -590,6 +590,41 @@ gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_sca
                             int64_t ld_x, const uint8_t* W, int64_t ld_w, const uint8_t* w_scales, int64_t d_out,
                             void* Y, int32_t y_dtype, int64_t ld_y, void* workspace, size_t ws_bytes, void* stream);
 
+/* Gradients of gptq_lora_add's factors and input, from activations in 16 bits or from
+ * their 8-bit checkpoint:  with dY the gradient of Y,
+ *
+ *   U[m] = scale[a] dY[m] B_a,   T[m] = scale[a] X[m] A_a^T,   a = adapter[m],
+ *   dA_a = sum U[m]^T X[m],   dB_a = sum dY[m]^T T[m]   over the tokens of adapter a,
+ *   dX[m] = base[m] + U[m] A_a.
+ *
+ *   X         device, M x d_in: of `dtype`, row stride ld_x; or GPTQ_E4M3: codes and
+ *             x_scales [M][blocks] as gptq_fp8_quantize writes them (block_rows = 1),
+ *             16-byte aligned, ld_x a multiple of 16 and at least whole blocks.
+ *   dY        device, M x d_out of `dtype` or GPTQ_F32, row stride ld_dy.
+ *   A, B      device, [n_adapters][rank][d_in] and [n_adapters][d_out][rank] of
+ *             `dtype` (GPTQ_F16 or GPTQ_BF16), dense; rank <= 128, n_adapters <= 1024,
+ *             M, d_in, d_out <= 2^22 (more: GPTQ_EUNSUPPORTED).
+ *   scale     device fp32 [n_adapters], or NULL (all 1); adapter device int32 [M],
+ *             outside [0, n_adapters): no adapter, the token counts nowhere and
+ *             dX = base.
+ *   dA, dB    device fp32, as A and B; written, also for adapters without tokens (0).
+ *   dX        device, M x d_in of dx_dtype (`dtype` or GPTQ_F32), row stride ld_dx, or
+ *             NULL; base in the same type with row stride ld_b, or NULL (zero); it may
+ *             be dX itself (ld_b == ld_dx).
+ *   workspace gptq_lora_grad_workspace_size bytes, 256-byte aligned; calls sharing one
+ *             workspace must be stream-ordered.
+ * fp32 accumulation.  U and T, and values of fp32 dY, enter the sums with 16 bits
+ * (2^-17 of each); everything else enters exactly.  A NaN or an infinity in a token
+ * reaches its adapter's gradients as NaN or infinity, and no other adapter's.  Results
+ * are bitwise reproducible for given inputs.  M = 0 writes zeros to dA and dB. */
+gptq_status gptq_lora_grad(const void* X, int32_t x_dtype, const uint8_t* x_scales, int64_t M, int64_t d_in,
+                           int64_t ld_x, const void* dY, int32_t dy_dtype, int64_t d_out, int64_t ld_dy, const void* A,
+                           const void* B, int32_t dtype, int64_t n_adapters, int32_t rank, const float* scale,
+                           const int32_t* adapter, float* dA, float* dB, const void* base, int64_t ld_b, void* dX,
+                           int32_t dx_dtype, int64_t ld_dx, void* workspace, size_t ws_bytes, void* stream);
+gptq_status gptq_lora_grad_workspace_size(int64_t M, int64_t d_in, int64_t d_out, int32_t rank, int64_t n_adapters,
+                                          size_t* bytes_out);
+
 /* Reference rates for measurement (not part of the quantization path): the
  * published peaks of a GPU are not what it sustains under a given load, so
  * the benchmark also measures two simple kernels on the same device.  Both
@@ -621,7 +656,7 @@ gptq_status gptq_probe_copy(const void* src, void* dst, size_t bytes, double* gb
  * 8 / 9 = W4A16 staging / main kernel, 10 = |x| sums, 11 = scale search,
  * 12 = scale application, 13 = layer forward, 14 = token log probabilities,
  * 15 = distillation, 16 = low-rank adapters, 17 = quantizing to 8 bits, 18 = products
- * of 8-bit numbers, 19 = policy loss).  gptq_timing_read synchronizes those events
+ * of 8-bit numbers, 19 = policy loss, 20 = adapters' gradients).  gptq_timing_read synchronizes those events
  * and reports the summed duration (ms) and launch count of `kind`; reset
  * drops all records.  Not thread safe; off by default. */
 gptq_status gptq_timing_enable(int32_t on);

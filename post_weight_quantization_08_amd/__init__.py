@@ -23,7 +23,8 @@ __all__ = [
     "gptq_abs_accumulate", "gptq_awq_search", "gptq_awq_apply", "gptq_layer_forward",
     "gptq_probe_mfma", "gptq_probe_copy", "gptq_probe_sink_bytes", "gptq_w4a16_matmul_noalloc",
     "gptq_token_logprobs", "gptq_distill_topk", "gptq_lora_add", "gptq_w4a16_lora_matmul",
-    "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_policy_loss",
+    "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_policy_loss", "gptq_lora_grad",
+    "gptq_lora_grad_workspace_size",
     "ACT_NONE", "ACT_RELU", "ACT_SILU",
     "OP_HESSIAN", "OP_PREPARE", "OP_QUANTIZE", "OP_W4A16", "OP_ABS", "OP_AWQ_SEARCH", "OP_FORWARD",
     "OP_LOGPROBS", "OP_DISTILL", "OP_LORA", "OP_W4A16_LORA", "OP_FP8_MATMUL", "OP_POLICY",
@@ -124,6 +125,11 @@ def _load() -> ctypes.CDLL:
     L.gptq_policy_loss.restype = i32
     L.gptq_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, vp,
                                    i64, vp, sz, vp]
+    L.gptq_lora_grad.restype = i32
+    L.gptq_lora_grad.argtypes = [vp, i32, vp, i64, i64, i64, vp, i32, i64, i64, vp, vp, i32, i64, i32, vp, vp, vp, vp, vp,
+                                 i64, vp, i32, i64, vp, sz, vp]
+    L.gptq_lora_grad_workspace_size.restype = i32
+    L.gptq_lora_grad_workspace_size.argtypes = [i64, i64, i64, i32, i64, P(sz)]
     L.gptq_timing_enable.restype = i32
     L.gptq_timing_enable.argtypes = [i32]
     L.gptq_timing_reset.restype = i32
@@ -356,6 +362,23 @@ def gptq_policy_loss(logits, x_dtype: int, n_rows: int, vocab: int, ld_x: int, t
                                 _ptr(advantage), _ptr(ref_logprob), clip_low, clip_high, kl_coef, temperature,
                                 _ptr(weight), _ptr(loss), _ptr(logprob), _ptr(ratio), _ptr(kl), _ptr(grad), ld_g,
                                 _ptr(workspace), ws_bytes, _stream(stream)), "gptq_policy_loss")
+
+
+def gptq_lora_grad(X, x_dtype: int, x_scales, M: int, d_in: int, ld_x: int, dY, dy_dtype: int, d_out: int, ld_dy: int, A,
+                   B, dtype: int, n_adapters: int, rank: int, scale, adapter, dA, dB, base=None, ld_b: int = 0, dX=None,
+                   dx_dtype: int = 0, ld_dx: int = 0, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    """Gradients of the adapters' factors and, with dX, of their input."""
+    _check(lib.gptq_lora_grad(_ptr(X), x_dtype, _ptr(x_scales), M, d_in, ld_x, _ptr(dY), dy_dtype, d_out, ld_dy, _ptr(A),
+                              _ptr(B), dtype, n_adapters, rank, _ptr(scale), _ptr(adapter), _ptr(dA), _ptr(dB),
+                              _ptr(base), ld_b, _ptr(dX), dx_dtype, ld_dx, _ptr(workspace), ws_bytes, _stream(stream)),
+           "gptq_lora_grad")
+
+
+def gptq_lora_grad_workspace_size(M: int, d_in: int, d_out: int, rank: int, n_adapters: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.gptq_lora_grad_workspace_size(M, d_in, d_out, rank, n_adapters, ctypes.byref(out)),
+           "gptq_lora_grad_workspace_size")
+    return int(out.value)
 
 
 def gptq_timing_enable(on: bool) -> None:

@@ -14,6 +14,7 @@ import torch
 from . import (BF16, E4M3, F16, F32, GptqError, GptqParams, OP_ABS, OP_AWQ_SEARCH, OP_DISTILL, OP_FORWARD,
                OP_FP8_MATMUL, OP_HESSIAN, OP_LOGPROBS, OP_LORA, OP_POLICY, OP_PREPARE, OP_QUANTIZE, OP_W4A16, OP_W4A16_LORA, ENOTPD, _check, dtype_code,
                gptq_abs_accumulate, gptq_awq_apply, gptq_awq_search, gptq_hessian_accumulate, gptq_layer_forward,
+               gptq_lora_grad_workspace_size,
                gptq_pack_bits, gptq_pack_int4, gptq_pack_int4_permuted, gptq_prepare_hinv, gptq_quantize_layer,
                gptq_w4a16_matmul, gptq_workspace_size, lib)
 
@@ -604,6 +605,75 @@ def fp8_matmul(X: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, x_scale
     _call(lib.gptq_fp8_matmul, "gptq_fp8_matmul", device, px, kind, psx, M, d_in, ld_x, pw, ld_w, psw, d_out, py,
           _DTYPE.get(Y.dtype, -1), ld_y, at, nbytes, _stream_of(stream, device))
     return Y
+
+
+def _grad_out(A: torch.Tensor, B: torch.Tensor, M: int, dx_dtype) -> Buffers:
+    n, r, d_in = A.shape
+    out = {"dA": torch.empty(A.shape, dtype=torch.float32, device=A.device),
+           "dB": torch.empty(B.shape, dtype=torch.float32, device=A.device)}
+    if dx_dtype is not None:
+        out["dX"] = torch.empty(M, d_in, dtype=dx_dtype, device=A.device)
+    return Buffers(("lora_grad", n, r, d_in, B.shape[1], M if dx_dtype is not None else -1, dx_dtype, A.device.index), out)
+
+
+def _grad_ws(M: int, A: torch.Tensor, B: torch.Tensor) -> torch.Tensor:
+    return _ws(gptq_lora_grad_workspace_size(M, A.shape[2], B.shape[1], A.shape[1], A.shape[0]), A.device)
+
+
+def lora_grad_buffers(X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor, B: torch.Tensor, dx_dtype=None):
+    """(out, ws) of lora_grad calls with these sizes, to be kept from call to call; dX of dx_dtype unless it is None."""
+    return _grad_out(A, B, X.shape[0], dx_dtype), _grad_ws(X.shape[0], A, B)
+
+
+def lora_grad(X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor,
+              scale: Optional[torch.Tensor] = None, x_scales: Optional[torch.Tensor] = None,
+              base: Optional[torch.Tensor] = None, want_dx: bool = False, out: Optional[Dict[str, torch.Tensor]] = None,
+              ws: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients dA, dB (fp32) of lora_add's factors from the gradient dY of its result (A's type or fp32) and, with
+    want_dx, a base or an out that has "dX", dX = base + scale[a] (dY B_a) A_a (base's type, else A's).  X: A's type,
+    or codes of fp8_quantize with x_scales (an 8-bit checkpoint).  base may be dX itself."""
+    dtype = A.dtype
+    M, wide, ld_x, device = _rows(X, "X")
+    d_in = A.shape[-1]
+    n, r, d_out, pa, pb, pad, ps = _adapters(A, B, adapter, scale, dtype, M, d_in, device)
+    px, psx, kind = X.data_ptr(), None, _DTYPE.get(X.dtype, -1)
+    if X.dtype is _CODES:
+        px, ld_x = _codes(X, M, _blocks(d_in) * F8_BLOCK, "X", device)
+        if x_scales is None:
+            raise ValueError("x_scales: codes need their scales")
+        psx, kind = _dense(x_scales, _BYTES, (M, _blocks(d_in)), "x_scales", device), E4M3
+    elif wide != d_in or x_scales is not None:
+        raise ValueError("X: d_in columns are needed, and only codes have scales")
+    py, ld_dy = _out_rows(dY, dY.dtype, M, d_out, "dY", device)
+    if out is None:
+        dx = base.dtype if base is not None else dtype if want_dx else None
+        with _on(stream, X.device):
+            out = _grad_out(A, B, M, dx)
+    pdx, ld_dx, dx = None, d_in, torch.float32
+    has_dx = "dX" in out
+    if has_dx:
+        dx = out["dX"].dtype
+    if type(out) is Buffers and out.key == ("lora_grad", n, r, d_in, d_out, M if has_dx else -1, dx if has_dx else None,
+                                            device):
+        pda, pdb = out.addresses[:2]
+        if has_dx:
+            pdx = out.addresses[2]
+    else:
+        pda = _dense(out["dA"], torch.float32, (n, r, d_in), "dA", device)
+        pdb = _dense(out["dB"], torch.float32, (n, d_out, r), "dB", device)
+        if has_dx:
+            pdx, ld_dx = _out_rows(out["dX"], dx, M, d_in, "dX", device)
+    if base is not None and not has_dx:
+        raise ValueError("base: out has no dX to add it to")
+    p0, ld_b = _out_rows(base, dx, M, d_in, "base", device) if base is not None else (None, d_in)
+    if ws is None:
+        with _on(stream, X.device):
+            ws = _grad_ws(M, A, B)
+    at, nbytes = _workspace(ws, device)
+    _call(lib.gptq_lora_grad, "gptq_lora_grad", device, px, kind, psx, M, d_in, ld_x, py, _DTYPE.get(dY.dtype, -1),
+          d_out, ld_dy, pa, pb, _DTYPE.get(dtype, -1), n, r, ps, pad, pda, pdb, p0, ld_b, pdx, _DTYPE.get(dx, -1), ld_dx,
+          at, nbytes, _stream_of(stream, device))
+    return out
 
 
 def calibrate_block(chunks: Sequence[torch.Tensor], W1: torch.Tensor, W2: torch.Tensor, params: GptqParams,
