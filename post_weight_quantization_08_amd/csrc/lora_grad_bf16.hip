@@ -1,0 +1,10 @@
+// The adapters' gradients for bf16 factors.
+#include "lora_grad_kernels.h"
+
+namespace gq {
+
+void grad_launch_bf16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, bool outer, hipStream_t st) {
+  grad_launch<GPTQ_BF16>(a, codes, wide, max_chunks, outer, st);
+}
+
+}  // namespace gq
