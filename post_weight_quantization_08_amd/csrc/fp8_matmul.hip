@@ -95,131 +95,115 @@ __device__ __forceinline__ void f8_store4(void* Y, int64_t at, int64_t left, f32
 }
 
 // ---------------------------------------------------------------- few tokens
-// 16 kR rows of weights by 16 kT tokens; the waves take the sum's blocks in turn,
-// straight from memory, and their sums meet in LDS.
-template <int kX, int kY, int kT, int kR, int kU>
-__global__ __launch_bounds__(512) void fp8_few_kernel(F8MmArgs a) {
-  constexpr int kW = 8;
-  constexpr int kPitch = kR * 16 + 4;
-  __shared__ __align__(16) float red[kW][kT * 16][kPitch];
+// 16 rows of weights by up to 16 tokens in one launch: the waves take the sum's blocks
+// in turn, straight from memory, quantize the tokens' values as they come, and their
+// sums meet in LDS.
+constexpr int kF8FewWaves = 8;
+
+template <int kX, int kY>
+__global__ __launch_bounds__(64 * kF8FewWaves) void fp8_few_kernel(F8MmArgs a) {
+  constexpr int kPitch = 20;
+  constexpr int kU = kX == GPTQ_F32 ? 2 : 4;                             // blocks asked for together
+  constexpr int kRaw = kX == GPTQ_E4M3 ? 0 : kX == GPTQ_F32 ? 32 : 16;   // words of a lane's values
+  __shared__ __align__(16) float red[kF8FewWaves][16][kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * kR);
-  const uint8_t* w[kR];
-  const uint8_t* sw[kR];
-#pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    const int64_t first = n0 + r * 16, row = first + c16;
-    w[r] = a.W + (row < a.d_out ? row : a.d_out - 1) * a.ld_w + q * 16;
-    sw[r] = a.ws + (first < a.d_out ? first : a.d_out - 1) / kF8Block * a.nb;
-  }
-  const char* x[kT];
-  const uint8_t* sx[kT];
-#pragma unroll
-  for (int t = 0; t < kT; ++t) {
-    const int64_t m = t * 16 + c16 < a.M ? t * 16 + c16 : a.M - 1;
-    x[t] = static_cast<const char*>(a.X) + m * a.ld_x * (kX == GPTQ_F32 ? 4 : kX == GPTQ_E4M3 ? 1 : 2);
-    sx[t] = kX == GPTQ_E4M3 ? a.xs + m * a.nb : nullptr;
-  }
-  f32x4 acc[kR][kT];
-#pragma unroll
-  for (int r = 0; r < kR; ++r)
-#pragma unroll
-    for (int t = 0; t < kT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const uint8_t* w = a.W + min(n0 + c16, a.d_out - 1) * a.ld_w + q * 16;
+  const uint8_t* sw = a.ws + n0 / kF8Block * a.nb;
+  // lanes without a token take the last one's values; nothing of them is stored
+  const int64_t m = min((int64_t)c16, a.M - 1);
+  const char* x = static_cast<const char*>(a.X) + m * a.ld_x * (kX == GPTQ_F32 ? 4 : kX == GPTQ_E4M3 ? 1 : 2);
+  const uint8_t* sx = kX == GPTQ_E4M3 ? a.xs + m * a.nb : nullptr;
+  f32x4 acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
   struct Step {
-    u32x4 w[2][kR], x[2][kT];              // [unit]
-    uint32_t sw[kR], sx[kT];
-    float v[kX == GPTQ_E4M3 ? 1 : kT][kX == GPTQ_E4M3 ? 1 : 4][8];
+    u32x4 w[2][1], x[2][1];                // [unit]
+    uint32_t sw[1], sx[1];
+    uint32_t raw[kRaw ? kRaw : 1];
   };
   auto read = [&](int b, Step& s) {
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      s.w[0][r] = *reinterpret_cast<const u32x4*>(w[r] + b * kF8Block);
-      s.w[1][r] = *reinterpret_cast<const u32x4*>(w[r] + b * kF8Block + 64);
-      s.sw[r] = sw[r][b];
-    }
-#pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      if constexpr (kX == GPTQ_E4M3) {
-        s.x[0][t] = *reinterpret_cast<const u32x4*>(x[t] + b * kF8Block + q * 16);
-        s.x[1][t] = *reinterpret_cast<const u32x4*>(x[t] + b * kF8Block + q * 16 + 64);
-        s.sx[t] = sx[t][b];
+    s.w[0][0] = *reinterpret_cast<const u32x4*>(w + b * kF8Block);
+    s.w[1][0] = *reinterpret_cast<const u32x4*>(w + b * kF8Block + 64);
+    s.sw[0] = sw[b];
+    if constexpr (kX == GPTQ_E4M3) {
+      s.x[0][0] = *reinterpret_cast<const u32x4*>(x + b * kF8Block + q * 16);
+      s.x[1][0] = *reinterpret_cast<const u32x4*>(x + b * kF8Block + q * 16 + 64);
+      s.sx[0] = sx[b];
+    } else {
+      constexpr int kE = kX == GPTQ_F32 ? 4 : 2;
+      const int k = b * kF8Block + q * 16;
+      if ((b + 1) * kF8Block <= a.d_in) {
+        __builtin_memcpy(s.raw, __builtin_assume_aligned(x + (int64_t)k * kE, kE), kRaw * 2);
+        __builtin_memcpy(s.raw + kRaw / 2, __builtin_assume_aligned(x + (int64_t)(k + 64) * kE, kE), kRaw * 2);
       } else {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          // lanes without a token quantize nothing
-          if (t * 16 + c16 < a.M) f8_load8<kX>(x[t], b * kF8Block + q * 16 + (h / 2) * 64 + (h % 2) * 8, a.d_in, s.v[t][h]);
-          else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s.v[t][h][e] = 0.f;
+        for (int i = 0; i < 32; ++i) {
+          const int at = k + i / 16 * 64 + i % 16;
+          const uint32_t v = at < a.d_in ? load_bits<kX>(x, at) : 0u;
+          if constexpr (kX == GPTQ_F32) s.raw[i] = v;
+          else s.raw[i / 2] = i % 2 ? s.raw[i / 2] | v << 16 : v;
         }
       }
     }
   };
   auto multiply = [&](Step& s) {
     if constexpr (kX != GPTQ_E4M3) {
+      float v[32];
 #pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        uint32_t top = max(max(f8_top8(s.v[t][0]), f8_top8(s.v[t][1])), max(f8_top8(s.v[t][2]), f8_top8(s.v[t][3])));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        s.sx[t] = f8_scale(top);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const auto& v = s.v[t][h];
-          s.x[h / 2][t][(h % 2) * 2] = f8_codes4(v[0], v[1], v[2], v[3], s.sx[t]);
-          s.x[h / 2][t][(h % 2) * 2 + 1] = f8_codes4(v[4], v[5], v[6], v[7], s.sx[t]);
-        }
+      for (int i = 0; i < 32; ++i) {
+        if constexpr (kX == GPTQ_F32) v[i] = __uint_as_float(s.raw[i]);
+        else v[i] = i % 2 ? hi16<kX>(s.raw[i / 2]) : lo16<kX>(s.raw[i / 2]);
       }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      // over the four lanes of a token, 16 and 32 apart
+      const auto p = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+      top = max(p[0], p[1]);
+      const auto o = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+      top = max(o[0], o[1]);
+      s.sx[0] = f8_scale(top);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        s.x[i / 4][0][i % 4] = f8_codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], s.sx[0]);
     }
     if constexpr (kY == GPTQ_F32) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) f8_wide_unit<kR, kT>(s.w[u], s.x[u], s.sw, s.sx, acc);
+      for (int u = 0; u < 2; ++u) f8_wide_unit<1, 1>(s.w[u], s.x[u], s.sw, s.sx, acc);
     } else {
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
-          acc[r][t] = f8_mfma(f8_frag(s.w[0][r], s.w[1][r]), f8_frag(s.x[0][t], s.x[1][t]), acc[r][t], s.sw[r], s.sx[t]);
+      acc[0][0] = f8_mfma(f8_frag(s.w[0][0], s.w[1][0]), f8_frag(s.x[0][0], s.x[1][0]), acc[0][0], s.sw[0], s.sx[0]);
     }
   };
-  // kU blocks' operands are asked for together
   int b = wave;
-  for (; b + (kU - 1) * kW < a.nb; b += kU * kW) {
+  for (; b + (kU - 1) * kF8FewWaves < a.nb; b += kU * kF8FewWaves) {
     Step s[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) read(b + u * kW, s[u]);
+    for (int u = 0; u < kU; ++u) read(b + u * kF8FewWaves, s[u]);
 #pragma unroll
     for (int u = 0; u < kU; ++u) multiply(s[u]);
   }
-  for (; b < a.nb; b += kW) {
+  for (; b < a.nb; b += kF8FewWaves) {
     Step s;
     read(b, s);
     multiply(s);
   }
-#pragma unroll
-  for (int r = 0; r < kR; ++r)
-#pragma unroll
-    for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4*>(&red[wave][t * 16 + c16][r * 16 + 4 * q]) = acc[r][t];
+  *reinterpret_cast<f32x4*>(&red[wave][c16][4 * q]) = acc[0][0];
   __syncthreads();
-  for (int i = threadIdx.x; i < kT * 16 * kR * 4; i += 512) {
-    const int m = i / (kR * 4), n = i % (kR * 4) * 4;
-    if (m >= a.M || n0 + n >= a.d_out) continue;
-    f32x4 v = *reinterpret_cast<const f32x4*>(&red[0][m][n]);
+  const int tok = threadIdx.x >> 2, n = threadIdx.x % 4 * 4;
+  if (tok >= a.M || tok >= 16 || n0 + n >= a.d_out) return;
+  f32x4 v = *reinterpret_cast<const f32x4*>(&red[0][tok][n]);
 #pragma unroll
-    for (int u = 1; u < kW; ++u) v += *reinterpret_cast<const f32x4*>(&red[u][m][n]);
-    f8_store4<kY>(a.Y, m * a.ld_y + n0 + n, a.d_out - n0 - n, v);
-  }
+  for (int u = 1; u < kF8FewWaves; ++u) v += *reinterpret_cast<const f32x4*>(&red[u][tok][n]);
+  f8_store4<kY>(a.Y, tok * a.ld_y + n0 + n, a.d_out - n0 - n, v);
 }
 
 // ---------------------------------------------------------------- many tokens
-// Workgroup number -> (token tile, weight tile, part).  Workgroups go to the
+// Number -> (token tile, weight tile, part).  Workgroups go to the
 // eight XCDs in turn; each gets a run of tiles, walked in bands of eight token
 // tiles, so that what runs on it at one time reads few panels through its L2.
-__device__ __forceinline__ void f8_place(const F8MmArgs& a, int& tm, int& tn, int& part) {
+__device__ __forceinline__ void f8_place(const F8MmArgs& a, int id, int& tm, int& tn, int& part) {
   const int total = a.tiles_m * a.tiles_n * a.splits;
   const int per = total / 8;
-  int id = blockIdx.x;
   if (id < per * 8) id = id % 8 * per + id / 8;
   const int tiles = a.tiles_m * a.tiles_n;
   part = id / tiles;
@@ -236,7 +220,7 @@ __device__ __forceinline__ void f8_place(const F8MmArgs& a, int& tm, int& tn, in
 // slot u ^ (r / 2 % 8): the sixteen rows of a fragment's unit then cover all banks
 // once.
 template <int kY, int kBM, int kBN, int kWM, int kWN>
-__global__ __launch_bounds__(64 * kWM * kWN) void fp8_tile_kernel(F8MmArgs a) {
+__global__ __launch_bounds__(64 * kWM * kWN, 2) void fp8_tile_kernel(F8MmArgs a) {
   constexpr int kWaves = kWM * kWN;
   constexpr int kRows = kBM + kBN;
   constexpr int kStage = kRows * kF8Block;
@@ -247,7 +231,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void fp8_tile_kernel(F8MmArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
   int tm, tn, part;
-  f8_place(a, tm, tn, part);
+  f8_place(a, blockIdx.x, tm, tn, part);
   const int64_t m0 = (int64_t)tm * kBM, n0 = (int64_t)tn * kBN;
   const int b0 = part * a.nb_split, b1 = min(b0 + a.nb_split, a.nb);
   // this lane's part of load i: row 8 (wave + i kWaves) + lane / 8 of the stage (tokens first), slot lane % 8
@@ -317,12 +301,22 @@ __global__ __launch_bounds__(64 * kWM * kWN) void fp8_tile_kernel(F8MmArgs a) {
 #pragma unroll
       for (int t = 0; t < kT; ++t) acc[r][t] = f8_mfma(wf, xf[t], acc[r][t], uw[r * 16 / kF8Block], ux[t]);
     }
+    // the tokens' operands and two of the weights' first, then every next one's beside
+    // the products of the one two before
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kT + 4, 0);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x8, kT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
   };
   fetch(b0, x0, bx[0], bw[0]);
 #define GQ_F8_STAGE(u, CUR, NEXT)                                         \
   {                                                                       \
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); \
+    __builtin_amdgcn_s_waitcnt(0x0F70);   /* vmcnt(0), known to the compiler */ \
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");       \
     fetch(b + (u) + 1, NEXT, bx[1 - (u)], bw[1 - (u)]);                   \
+    __builtin_amdgcn_sched_barrier(0);                                    \
     if (b + (u) < b1) multiply(CUR, bx[u], bw[u]);                        \
   }
   for (int b = b0; b < b1; b += 2) {
@@ -342,6 +336,192 @@ __global__ __launch_bounds__(64 * kWM * kWN) void fp8_tile_kernel(F8MmArgs a) {
       if (a.splits > 1) f8_store4<GPTQ_F32>(a.part, ((int64_t)part * a.M + m) * a.d_out + n, a.d_out - n, acc[r][t]);
       else f8_store4<kY>(a.Y, m * a.ld_y + n, a.d_out - n, acc[r][t]);
     }
+  }
+}
+
+// Large products with 16-bit outputs: 256 tokens by 256 rows, four waves of 128 x 128
+// each (one per SIMD, so that an operand read from LDS serves four products of
+// 32x32x64), the sum a block of 128 at a time in two buffers, whole 128-byte lines of
+// every row (half lines keep the L2s busy for twice as long).  A block's second half is
+// read while its first is multiplied, then its buffer is free for the block after the
+// next.  Unit u of row r lies at slot u ^ (r / 2 % 8): the sixteen rows that are read
+// together cover all banks once.
+constexpr int kF8Big = 256;
+constexpr int kF8BigStage = 2 * kF8Big * kF8Block;
+constexpr int kF8BigWords = 30;
+
+template <int kY>
+__global__ __launch_bounds__(256, 1) void fp8_big_kernel(F8MmArgs a) {
+  __shared__ __attribute__((aligned(1024))) char r0[kF8BigStage], r1[kF8BigStage];
+  __shared__ uint32_t scale_x[kF8BigWords][kF8Big], scale_w[kF8BigWords][2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c32 = lane & 31, h = lane >> 5;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t w_rows = (a.d_out + kF8Block - 1) / kF8Block;
+  int tm, tn, part;
+  f8_place(a, blockIdx.x, tm, tn, part);
+  const int64_t m0 = (int64_t)tm * kF8Big, n0 = (int64_t)tn * kF8Big;
+  uint32_t src[16];
+  // this lane's part of load i: row 8 (4 i + wave) + lane / 8 of the stage (tokens
+  // first), slot lane % 8; rows behind the end read the last one and are never stored
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int row = 8 * (4 * (i & 7) + wave) + (lane >> 3);
+    const int unit = (lane & 7) ^ ((row >> 1) & 7);
+    src[i] = unit * 16 + (i < 8 ? (uint32_t)min(row, (int)min(a.M - 1 - m0, (int64_t)kF8Big)) * (uint32_t)a.ld_x
+                                : (uint32_t)min(row, (int)min(a.d_out - 1 - n0, (int64_t)kF8Big)) * (uint32_t)a.ld_w);
+  }
+  const uint8_t* base_x = static_cast<const uint8_t*>(a.X) + m0 * a.ld_x;
+  const uint8_t* base_w = a.W + n0 * a.ld_w;
+  auto dma = [&](int block, char* to) {
+    const int at = min(block, a.nb - 1) * kF8Block;   // blocks behind the end read the last one, which nothing uses
+#pragma unroll
+    for (int i = 0; i < 16; ++i) lds_load16((i < 8 ? base_x : base_w) + at + src[i], to + (4 * i + wave) * 1024);
+  };
+  // Scales of four blocks in a word, one byte of which an instruction picks: up to 30
+  // words of every row in LDS.  Words that would end behind the array are read there
+  // and moved.
+  auto stage = [&](const uint8_t* array, int64_t rows, int64_t row, int b, int g0, int words, uint32_t (&v)[6]) {
+    const int64_t end = rows * a.nb - 4;
+    uint32_t move[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const int64_t at = row * a.nb + b + 4 * min(g0 + i, words - 1);
+      move[i] = at > end ? (uint32_t)min(at - end, (int64_t)3) * 8 : 0u;
+      __builtin_memcpy(&v[i], array + min(at, end), 4);
+    }
+    __builtin_amdgcn_sched_barrier(0);   // together
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] >>= move[i];
+  };
+  auto stage_scales = [&](int b) {
+    const int words = min((a.nb - b + 3) / 4, kF8BigWords);
+    const int64_t row = min(m0 + (int)threadIdx.x, a.M - 1), w_row = min(n0 / kF8Block + (lane & 1), w_rows - 1);
+#pragma unroll 1
+    for (int g = 0; g < words; g += 6) {
+      uint32_t v[6];
+      stage(a.xs, a.M, row, b, g, words, v);
+#pragma unroll
+      for (int i = 0; i < 6; ++i) scale_x[g + i][threadIdx.x] = v[i];
+      if (wave == 0) {
+        stage(a.ws, w_rows, w_row, b, g, words, v);
+        if (lane < 2) {
+#pragma unroll
+          for (int i = 0; i < 6; ++i) scale_w[g + i][lane] = v[i];
+        }
+      }
+    }
+  };
+  struct Frags {
+    i32x8 x[4], w[4];
+  };
+  const int swz = (c32 >> 1) & 7;
+  const int at_x = (wm * 128 + c32) * kF8Block, at_w = (kF8Big + wn * 128 + c32) * kF8Block;
+  auto read = [&](const char* from, int half, Frags& f) {
+    const int u0 = ((4 * half + 2 * h) ^ swz) * 16, u1 = u0 ^ 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const char* p = from + at_w + i * 32 * kF8Block;
+      const char* q = from + at_x + i * 32 * kF8Block;
+      f.w[i] = f8_frag(*reinterpret_cast<const u32x4*>(p + u0), *reinterpret_cast<const u32x4*>(p + u1));
+      f.x[i] = f8_frag(*reinterpret_cast<const u32x4*>(q + u0), *reinterpret_cast<const u32x4*>(q + u1));
+    }
+  };
+  f32x16 acc[4][4];
+  Frags fa, fb;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[r][t][i] = 0.f;
+  // Block b + k: its first half is in fa.  At the barrier its second half is read by
+  // every wave, so that its buffer is free, and the next block has landed.  No branch
+  // between two of them: the compiler's count of what is in flight would be lost.
+#define GQ_F8_MULTIPLY(F, k)                                                            \
+  _Pragma("unroll") for (int r = 0; r < 4; ++r)                                         \
+  _Pragma("unroll") for (int t = 0; t < 4; ++t)                                         \
+    acc[r][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[r], F.x[t], acc[r][t], 0, 0, (k), (int)now_w, (k), \
+                                                                (int)now_x[t]);
+#define GQ_F8_BLOCK(k, CUR, NXT)                                                        \
+  {                                                                                     \
+    read(CUR, 1, fb);                                                                   \
+    GQ_F8_MULTIPLY(fa, k)                                                               \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) {                                     \
+      __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);                                  \
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                                \
+    }                                                                                   \
+    __builtin_amdgcn_s_waitcnt(0x0070);   /* vmcnt(0) lgkmcnt(0) */                     \
+    asm volatile("s_barrier" ::: "memory");                                             \
+    dma(b + (k) + 2, CUR);                                                              \
+    read(NXT, 0, fa);                                                                   \
+    GQ_F8_MULTIPLY(fb, k)                                                               \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) {                                     \
+      if (i < 4) __builtin_amdgcn_sched_group_barrier(0x20, 4, 0);                      \
+      __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);                                  \
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                                \
+    }                                                                                   \
+  }
+  for (int first = 0; first < a.nb; first += 4 * kF8BigWords) {
+    const int end = min(first + 4 * kF8BigWords, a.nb);
+    // what was asked for behind the last block has landed, and every wave is done
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+    dma(first, r0);
+    dma(first + 1, r1);
+    stage_scales(first);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    asm volatile("s_barrier" ::: "memory");
+    read(r0, 0, fa);
+    uint32_t now_x[4], now_w;
+    auto scales = [&](int b) {
+      const int g = (b - first) / 4, move = b - first & 2 ? 16 : 0;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) now_x[t] = scale_x[g][wm * 128 + t * 32 + c32] >> move;
+      now_w = scale_w[g][wn] >> move;
+    };
+    int b = first;
+    for (; b + 2 <= end; b += 2) {
+      scales(b);
+      GQ_F8_BLOCK(0, r0, r1)
+      GQ_F8_BLOCK(1, r1, r0)
+    }
+    if (b < end) {
+      scales(b);
+      GQ_F8_BLOCK(0, r0, r1)
+    }
+  }
+#undef GQ_F8_BLOCK
+#undef GQ_F8_MULTIPLY
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no direct load ends after the workgroup
+  // eight consecutive outputs a lane: half of them from the lane 32 away
+  uint16_t* out = static_cast<uint16_t*>(a.Y) + (m0 + wm * 128) * a.ld_y + n0 + wn * 128;
+  const int left_m = (int)min(a.M - m0 - wm * 128, (int64_t)128), left_n = (int)min(a.d_out - n0 - wn * 128, (int64_t)128);
+  const bool full = left_m == 128 && left_n == 128;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t at = (uint32_t)(t * 32 + c32) * (uint32_t)a.ld_y + 8 * h;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = value_bits<kY>(acc[r][t][8 * i + 2 * j]) | value_bits<kY>(acc[r][t][8 * i + 2 * j + 1]) << 16;
+        // words 0, 1: rows 16 i + 4 h .., words 2, 3: rows 16 i + 8 + 4 h ..
+        const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+        const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
+        const int n = r * 32 + i * 16;
+        if (full) {
+          __builtin_memcpy(__builtin_assume_aligned(out + at + n, 2), &v, 16);
+        } else if (t * 32 + c32 < left_m) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + 8 * h + e < left_n) out[at + n + e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+        }
+      }
   }
 }
 
@@ -366,11 +546,22 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(F8MmArgs a) {
   f8_store4<kY>(a.Y, m * a.ld_y + n, left, v);
 }
 
-constexpr int kF8Few = 64;          // tokens up to which weights go straight to the matrix units
-constexpr int kF8Fused = 16;        // tokens up to which values are quantized beside the product
+// Up to 16 tokens on up to 8192 rows take one launch, whose every workgroup quantizes all
+// tokens; more rows make that the larger part.  bf16 in one launch, or quantized apart
+// and in tiles of 32 tokens, us:
+//   4096 -> 4096     1 to 8 tokens 8 and 13,   16 tokens 9 and 14,   32 (by the codes) 18 and 14
+//   11008 -> 4096    2 tokens 13 and 20,       16 tokens 20 and 21,  32 37 and 22
+//   8192 -> 28672    2 tokens 57 and 44,       16 tokens 102 and 45, 48 70 and 50
+constexpr int kF8Few = 16;
+constexpr int64_t kF8FewRows = 8192;
+// Tiles of 128 tokens if two of them for every CU remain, else 64 (or 32), bf16, us:
+// 300 x 4096 -> 14336 56 and 50, 2048 x 4096 -> 4096 61 and 69.  The sum is split until
+// every CU has a workgroup, into parts of four blocks or more: 65 x 4096 -> 4096 in 1, 4
+// and 8 parts 26, 16 and 20; 128 x 8192 -> 28672 in 1 and 2 parts 62 and 87.
+constexpr int64_t kF8Wide = 512;
 
 struct F8Plan {
-  bool few, fused;
+  bool few;
   int bm, bn, splits;
   size_t off_scales, off_part, total;
 };
@@ -378,9 +569,8 @@ struct F8Plan {
 static F8Plan f8_plan(int64_t M, int64_t d_in, int64_t d_out, bool codes) {
   F8Plan p{};
   const int64_t nb = cdiv(d_in, kF8Block);
-  p.few = M <= kF8Few;
-  p.fused = !codes && M <= kF8Fused;
-  if (!codes && !p.fused) {
+  p.few = M <= kF8Few && d_out <= kF8FewRows;
+  if (!codes && !p.few) {
     p.off_scales = align_up((size_t)M * nb * kF8Block, 256);
     p.total = align_up(p.off_scales + (size_t)M * nb, 256);
   }
@@ -388,8 +578,11 @@ static F8Plan f8_plan(int64_t M, int64_t d_in, int64_t d_out, bool codes) {
   if (!p.few) {
     p.bm = p.bn = cdiv(M, 256) * cdiv(d_out, 256) >= 256 ? 256 : 128;
     if (p.bm == 128) {
-      const int64_t tiles = cdiv(M, 128) * cdiv(d_out, 128);
-      while (p.splits < 8 && tiles * p.splits < 256 && nb / (p.splits * 2) >= 8) p.splits *= 2;
+      if (M <= 32) p.bm = 32;
+      else if (cdiv(M, 128) * cdiv(d_out, 128) < kF8Wide) p.bm = 64;
+      const int64_t tiles = cdiv(M, p.bm) * cdiv(d_out, 128);
+      while (tiles * p.splits < 256 && nb / (p.splits * 2) >= 4) p.splits *= 2;
+      p.splits = (int)cdiv(nb, cdiv(nb, p.splits));
     }
   }
   p.off_part = p.total;
@@ -401,20 +594,14 @@ size_t fp8_matmul_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out) {
   return f8_plan(M, d_in, d_out, false).total;
 }
 
-template <int kX, int kY, int kT, int kR, int kU>
-static void f8_launch_few(const F8MmArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((fp8_few_kernel<kX, kY, kT, kR, kU>), dim3((unsigned)cdiv(a.d_out, 16 * kR)), dim3(512), 0, st, a);
-}
-
 template <int kY>
 static void f8_run(F8MmArgs& a, int x_dtype, const F8Plan& p, hipStream_t st) {
   if (p.few) {
-    if (x_dtype == GPTQ_F32) f8_launch_few<GPTQ_F32, kY, 1, 1, 2>(a, st);
-    else if (x_dtype == GPTQ_F16) f8_launch_few<GPTQ_F16, kY, 1, 1, 2>(a, st);
-    else if (x_dtype == GPTQ_BF16) f8_launch_few<GPTQ_BF16, kY, 1, 1, 2>(a, st);
-    else if (a.M <= 16) f8_launch_few<GPTQ_E4M3, kY, 1, 1, 4>(a, st);
-    else if (a.M <= 32) f8_launch_few<GPTQ_E4M3, kY, 2, 2, 2>(a, st);
-    else f8_launch_few<GPTQ_E4M3, kY, 4, 2, 2>(a, st);
+    const dim3 grid((unsigned)cdiv(a.d_out, 16)), block(64 * kF8FewWaves);
+    if (x_dtype == GPTQ_F32) hipLaunchKernelGGL((fp8_few_kernel<GPTQ_F32, kY>), grid, block, 0, st, a);
+    else if (x_dtype == GPTQ_F16) hipLaunchKernelGGL((fp8_few_kernel<GPTQ_F16, kY>), grid, block, 0, st, a);
+    else if (x_dtype == GPTQ_BF16) hipLaunchKernelGGL((fp8_few_kernel<GPTQ_BF16, kY>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((fp8_few_kernel<GPTQ_E4M3, kY>), grid, block, 0, st, a);
     return;
   }
   a.tiles_m = (int)cdiv(a.M, p.bm);
@@ -422,8 +609,18 @@ static void f8_run(F8MmArgs& a, int x_dtype, const F8Plan& p, hipStream_t st) {
   a.splits = p.splits;
   a.nb_split = (int)cdiv(a.nb, p.splits);
   const dim3 grid((unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits));
+  if constexpr (kY != GPTQ_F32) {
+    // scales are read in words, a tile's rows by 32-bit offsets
+    if (p.bm == 256 && cdiv(a.d_out, kF8Block) * a.nb >= 4 && std::max(a.ld_x, a.ld_w) <= ((int64_t)1 << 23) &&
+        a.ld_y <= ((int64_t)1 << 23)) {
+      hipLaunchKernelGGL((fp8_big_kernel<kY>), grid, dim3(256), 0, st, a);
+      return;
+    }
+  }
   if (p.bm == 256) hipLaunchKernelGGL((fp8_tile_kernel<kY, 256, 256, 4, 2>), grid, dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((fp8_tile_kernel<kY, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else if (p.bm == 128) hipLaunchKernelGGL((fp8_tile_kernel<kY, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else if (p.bm == 64) hipLaunchKernelGGL((fp8_tile_kernel<kY, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((fp8_tile_kernel<kY, 32, 128, 1, 4>), grid, dim3(256), 0, st, a);
   if (a.splits > 1)
     hipLaunchKernelGGL((fp8_join_kernel<kY>), dim3((unsigned)cdiv(a.d_out, 1024), (unsigned)a.M), dim3(256), 0, st, a);
 }
@@ -469,7 +666,7 @@ extern "C" gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uin
   hipStream_t st = static_cast<hipStream_t>(stream);
   TimedScope ts(kTimeFp8Matmul, st);
   int kind = x_dtype;
-  if (!codes && !p.fused) {
+  if (!codes && !p.few) {
     f8_quantize_rows(X, x_dtype, M, d_in, ld_x, ws, (int64_t)a.nb * kF8Block, ws + p.off_scales, st);
     GQ_LAUNCHED();
     a.X = ws;
