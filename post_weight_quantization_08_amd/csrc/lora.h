@@ -151,12 +151,6 @@ __device__ __forceinline__ void lora_up_four(const LoraFew& a, int m, int64_t ro
   for (int r = 0; r < 4; ++r) y[r] = acts[r] ? y[r] + s[r] : y[r];
 }
 
-// Y[m] = base[m] + T[m] B_a^T for T made elsewhere (fp32 [M][rank padded to 8],
-// zeros behind the rank); dtype is B's; in lora.hip.
-void lora_up_run(int32_t dtype, const float* T, const int32_t* adapter, const uint16_t* B, int64_t n, int rank,
-                 const void* base, int64_t ld_b, void* Y, int32_t y_dtype, int64_t ld_y, int64_t M, int64_t d_out,
-                 hipStream_t st);
-
 // The 4-bit projection (arguments as gptq_w4a16_matmul's), with adapters when
 // `lora` is given; in w4a16.hip.
 gptq_status w4a16_run(const void* X, int32_t x_dtype, int64_t M, int64_t d_in, int64_t ld_x, const uint8_t* qweight,

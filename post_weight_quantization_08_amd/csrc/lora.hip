@@ -662,39 +662,6 @@ static void lora_launch(const LoraArgs& a, int32_t y_dtype, hipStream_t st) {
   else lora_up<kDt, kDt>(a, st);
 }
 
-template <int kDt>
-static void lora_up_any(const LoraArgs& a, int32_t y_dtype, hipStream_t st) {
-  if (a.M <= kLoraFew) {
-    if (y_dtype == GPTQ_F32) lora_up_few<kDt, GPTQ_F32>(a, st);
-    else lora_up_few<kDt, kDt>(a, st);
-  } else {
-    if (y_dtype == GPTQ_F32) lora_up<kDt, GPTQ_F32>(a, st);
-    else lora_up<kDt, kDt>(a, st);
-  }
-}
-
-void lora_up_run(int32_t dtype, const float* T, const int32_t* adapter, const uint16_t* B, int64_t n, int rank,
-                 const void* base, int64_t ld_b, void* Y, int32_t y_dtype, int64_t ld_y, int64_t M, int64_t d_out,
-                 hipStream_t st) {
-  LoraArgs a{};
-  a.B = B;
-  a.adapter = adapter;
-  a.base = base;
-  a.Y = Y;
-  a.T = const_cast<float*>(T);
-  a.ld_b = ld_b;
-  a.ld_y = ld_y;
-  a.M = M;
-  a.d_out = d_out;
-  a.rank = rank;
-  a.n = (int)n;
-  a.rp = (int)(cdiv(rank, 8) * 8);
-  a.splits = 1;
-  a.cols = lora_plan(M, 256, d_out, rank).cols;
-  if (dtype == GPTQ_F16) lora_up_any<GPTQ_F16>(a, y_dtype, st);
-  else lora_up_any<GPTQ_BF16>(a, y_dtype, st);
-}
-
 }  // namespace gq
 
 using namespace gq;

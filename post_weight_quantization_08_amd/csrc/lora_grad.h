@@ -3,10 +3,9 @@
 //   dA_a = sum_m U[m]^T X[m],  dB_a = sum_m dY[m]^T T[m],  dX[m] = base[m] + U[m] A_a
 // over the tokens of adapter a.
 //
-// Launches: parts of U and T, with the tokens sorted by adapter and A^T for dX beside
-// them (project); U and T added up and laid out for the sums over tokens (terms);
-// those sums (outer); their parts joined where an adapter has many tokens; dX by the
-// adapters' own second product.
+// Launches: parts of U and T, with the tokens sorted by adapter beside them (project);
+// U and T added up and laid out for what follows (terms); the sums over tokens (outer);
+// their parts joined where an adapter has many tokens; dX.
 //
 // Sums are fp32 and keep 24 bits of everything in them.  Where 16-bit numbers meet,
 // that is one product.  U, T and fp32 dY are three bf16 terms, fp16 beside them two,
@@ -33,10 +32,11 @@ struct GradChunk {
 };
 
 struct GradPlace {                  // what the sort writes
-  int32_t* order;                   // [P]: the token at a position; ~token where it fills a run up to 32
+  int32_t* order;                   // [P]: the token at a position; ~token where it fills a run up to 32;
+                                    // tokens without an adapter behind the runs
   GradChunk* chunks;
   int32_t* parts;                   // [n][2]: an adapter's first slot and its parts
-  int32_t* count;                   // [2]: chunks, positions
+  int32_t* count;                   // [3]: chunks, positions of the runs, of all
 };
 
 // One operand: rows of X with A, or rows of dY with B.
@@ -48,12 +48,12 @@ struct GradSide {
   const uint16_t* F;                // A [n][rank][K] or B [n][K][rank]
   int splits, per;                  // parts of the sum, and their blocks of 128
   float* sums;                      // [splits][M][rp]
-  float* full;                      // [M][rp], or null
+  uint16_t* flat;                   // bf16 [3][P][rk]: U for dX, or null
   uint16_t* turned;                 // bf16 [3][r16][P]: what this side's product gives
   const uint16_t* by;               // the other side's, which its sum over tokens takes
   float* grad;                      // [n][rank * K]
   float* part;                      // [slots][rank * K]
-  int blocks;                       // of 128 columns
+  int blocks;                       // of 256 columns
 };
 
 struct GradArgs {
@@ -61,13 +61,15 @@ struct GradArgs {
   GradPlace at;
   const int32_t* adapter;
   const float* scale;
-  const uint16_t* A;
-  uint16_t* a_turned;               // [n][d_in][rank], or null
+  const void* base;                 // dX = base + U A
+  void* dX;
+  int64_t ld_b, ld_dx;
+  int wide_dx;                      // dX and base are fp32
   int64_t M, P;
-  int n, rank, rp, r16;
+  int n, rank, rp, r16, rk;         // rank padded to 8, to tiles of 16, to steps of 32
   int chunk;
+  int input_tokens;                 // of a workgroup, for dX
   int groups;                       // of four token tiles
-  int a_tiles;                      // tiles of A to turn
   int halves;                       // of the ranks: more than 64 are taken 64 at a time
 };
 
@@ -170,9 +172,10 @@ __device__ __forceinline__ f32x4 grad_mfma(const u32x4 (&a)[kA], const u32x4 (&b
   return acc;
 }
 
-// Workgroups of the launches; in lora_grad_f16.hip and lora_grad_bf16.hip, for
-// factors of either type.  codes: X is e4m3; wide: dY is fp32.
-void grad_launch_f16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, bool outer, hipStream_t st);
-void grad_launch_bf16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, bool outer, hipStream_t st);
+// The launches that depend on the types; in lora_grad_f16.hip and lora_grad_bf16.hip,
+// for factors of either type.  codes: X is e4m3; wide: dY is fp32.
+enum GradStage { kGradProject, kGradOuter, kGradInput };
+void grad_launch_f16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, GradStage stage, hipStream_t st);
+void grad_launch_bf16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, GradStage stage, hipStream_t st);
 
 }  // namespace gq

@@ -4,7 +4,8 @@
 namespace gq {
 
 // U and T: the parts of their sums added up, scaled and laid out by position as three
-// bf16 terms, zero where a run is only filled up; and in fp32 by token for dX.
+// bf16 terms, zero where a run is only filled up: [rank][position] for the sums over
+// tokens, [position][rank] for dX.
 __global__ __launch_bounds__(256) void lora_grad_terms_kernel(GradArgs a) {
   const GradSide& s = a.side[blockIdx.y];
   const int pos = blockIdx.x * 64 + (threadIdx.x & 63);
@@ -28,18 +29,31 @@ __global__ __launch_bounds__(256) void lora_grad_terms_kernel(GradArgs a) {
       for (; p < s.splits; ++p) x += *reinterpret_cast<const f32x4*>(src + p * step);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] *= by;
-      if (s.full) *reinterpret_cast<f32x4*>(s.full + m * a.rp + r) = x;
     }
+    uint32_t h[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float left = x[i];
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
-        const uint32_t h = value_bits<GPTQ_BF16>(left);
-        s.turned[(int64_t)(t * a.r16 + r + i) * a.P + pos] = (uint16_t)h;
-        left -= bf16_bits_to_f32(h);
+        h[t][i] = value_bits<GPTQ_BF16>(left);
+        s.turned[(int64_t)(t * a.r16 + r + i) * a.P + pos] = (uint16_t)h[t][i];
+        left -= bf16_bits_to_f32(h[t][i]);
       }
     }
+    if (s.flat) {
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<uint2*>(s.flat + ((int64_t)t * a.P + pos) * a.rk + r) =
+            uint2{h[t][0] | h[t][1] << 16, h[t][2] | h[t][3] << 16};
+    }
+  }
+  // a step of 32 ranks may end behind the tiles of 16
+  if (s.flat && a.r16 < a.rk && threadIdx.x < 64) {
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+      for (int r = a.r16; r < a.rk; r += 4)
+        *reinterpret_cast<uint2*>(s.flat + ((int64_t)t * a.P + pos) * a.rk + r) = uint2{0u, 0u};
   }
 }
 
@@ -57,18 +71,20 @@ __global__ __launch_bounds__(256) void lora_grad_join_kernel(GradArgs a) {
 }
 
 struct GradPlan {
-  int rp, r16, chunk, splits[2], per[2];
+  int rp, r16, rk, chunk, splits[2], per[2];
   int64_t P, max_chunks, slots;
-  size_t order, chunks, parts, count, a_turned, full, sums[2], turned[2], part[2], total;
+  size_t order, chunks, parts, count, flat, sums[2], turned[2], part[2], total;
 };
 
 static GradPlan grad_plan(int64_t M, int64_t d_in, int64_t d_out, int64_t rank, int64_t n) {
   GradPlan p{};
   p.rp = (int)(cdiv(rank, 8) * 8);
   p.r16 = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
-  const int64_t blocks = cdiv(d_in, kF8Block) + cdiv(d_out, kF8Block);
-  // chunks: two workgroups per CU, of a step for every wave or more
-  const int64_t want = std::max<int64_t>(1, std::min(cdiv(512, blocks), M / 128));
+  p.rk = std::max(p.r16, 32);
+  const int64_t blocks = cdiv(d_in, 256) + cdiv(d_out, 256);
+  // chunks: a workgroup for every CU in one round, or two where registers and LDS have
+  // room for them, of a step for every wave or more
+  const int64_t want = std::max<int64_t>(1, std::min((p.r16 >= 64 ? 256 : 512) / blocks, M / 128));
   p.chunk = (int)(cdiv(cdiv(M, want), 32) * 32);
   p.P = align_up(M + 32 * n + 32, 64);
   p.max_chunks = cdiv(M, p.chunk) + n;
@@ -83,14 +99,16 @@ static GradPlan grad_plan(int64_t M, int64_t d_in, int64_t d_out, int64_t rank, 
   p.order = take((size_t)p.P * 4);
   p.chunks = take((size_t)p.max_chunks * sizeof(GradChunk));
   p.parts = take((size_t)n * 8);
-  p.count = take(8);
-  p.a_turned = take((size_t)n * rank * d_in * 2);
-  p.full = take((size_t)M * p.rp * 4);
+  p.count = take(12);
+  p.flat = take((size_t)3 * p.P * p.rk * 2);
+  // parts of the sums: as many as one round of two workgroups a CU takes, of both sides
+  const int64_t nb[2] = {cdiv(d_in, kF8Block), cdiv(d_out, kF8Block)};
+  const int64_t parts = std::max<int64_t>(2, 512 / (cdiv(M, 4 * kGradTile) * (p.r16 > 64 ? 2 : 1)));
+  int64_t per = cdiv(nb[0] + nb[1], parts);
+  while (cdiv(nb[0], per) + cdiv(nb[1], per) > parts) ++per;
   for (int i = 0; i < 2; ++i) {
-    // parts of the sum: 2048 waves a side
-    const int64_t nb = cdiv(widths[i], kF8Block);
-    p.per[i] = (int)cdiv(nb, std::min<int64_t>(nb, cdiv(2048, cdiv(M, kGradTile))));
-    p.splits[i] = (int)cdiv(nb, p.per[i]);
+    p.splits[i] = (int)cdiv(nb[i], per);
+    p.per[i] = (int)cdiv(nb[i], p.splits[i]);
     p.sums[i] = take((size_t)p.splits[i] * M * p.rp * 4);
     p.turned[i] = take((size_t)3 * p.r16 * p.P * 2);
     p.part[i] = take((size_t)p.slots * rank * widths[i] * 4);
@@ -153,18 +171,21 @@ extern "C" gptq_status gptq_lora_grad(const void* X, int32_t x_dtype, const uint
                    reinterpret_cast<int32_t*>(ws + p.parts), reinterpret_cast<int32_t*>(ws + p.count)};
   a.adapter = adapter;
   a.scale = scale;
-  a.A = static_cast<const uint16_t*>(A);
-  a.a_turned = dX ? reinterpret_cast<uint16_t*>(ws + p.a_turned) : nullptr;
+  a.base = base;
+  a.dX = dX;
+  a.ld_b = ld_b;
+  a.ld_dx = ld_dx;
+  a.wide_dx = dx_dtype == GPTQ_F32;
   a.M = M;
   a.P = p.P;
   a.n = (int)n_adapters;
   a.rank = rank;
   a.rp = p.rp;
   a.r16 = p.r16;
+  a.rk = p.rk;
   a.chunk = p.chunk;
   a.halves = p.r16 > 64 ? 2 : 1;
   a.groups = (int)cdiv(M, 4 * kGradTile);
-  a.a_tiles = dX ? (int)(cdiv(d_in, 32) * cdiv(rank, 32)) : 0;
   for (int i = 0; i < 2; ++i) {     // X with A, dY with B
     GradSide& s = a.side[i];
     s.D = i ? dY : X;
@@ -176,20 +197,20 @@ extern "C" gptq_status gptq_lora_grad(const void* X, int32_t x_dtype, const uint
     s.splits = p.splits[i];
     s.per = p.per[i];
     s.sums = reinterpret_cast<float*>(ws + p.sums[i]);
-    s.full = i && dX ? reinterpret_cast<float*>(ws + p.full) : nullptr;
+    s.flat = i && dX ? reinterpret_cast<uint16_t*>(ws + p.flat) : nullptr;
     s.turned = reinterpret_cast<uint16_t*>(ws + p.turned[i]);
     s.by = reinterpret_cast<uint16_t*>(ws + p.turned[1 - i]);
     s.grad = i ? dB : dA;
     s.part = reinterpret_cast<float*>(ws + p.part[i]);
-    s.blocks = s.nb;
+    s.blocks = (int)cdiv(s.K, 256);
   }
   const bool codes = x_dtype == GPTQ_E4M3, wide = dy_dtype == GPTQ_F32;
   const auto launch = dtype == GPTQ_F16 ? grad_launch_f16 : grad_launch_bf16;
-  launch(a, codes, wide, p.max_chunks, false, st);
+  launch(a, codes, wide, p.max_chunks, kGradProject, st);
   GQ_LAUNCHED();
   hipLaunchKernelGGL(lora_grad_terms_kernel, dim3((unsigned)cdiv(p.P, 64), 2), dim3(256), 0, st, a);
   GQ_LAUNCHED();
-  launch(a, codes, wide, p.max_chunks, true, st);
+  launch(a, codes, wide, p.max_chunks, kGradOuter, st);
   GQ_LAUNCHED();
   if (p.slots > 0) {
     const int64_t each = (int64_t)rank * std::max(d_in, d_out);
@@ -198,7 +219,7 @@ extern "C" gptq_status gptq_lora_grad(const void* X, int32_t x_dtype, const uint
     GQ_LAUNCHED();
   }
   if (dX && M > 0) {
-    lora_up_run(dtype, a.side[1].full, adapter, a.a_turned, n_adapters, rank, base, ld_b, dX, dx_dtype, ld_dx, M, d_in, st);
+    launch(a, codes, wide, p.max_chunks, kGradInput, st);
     GQ_LAUNCHED();
   }
   return GPTQ_OK;

@@ -3,8 +3,8 @@
 
 namespace gq {
 
-void grad_launch_f16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, bool outer, hipStream_t st) {
-  grad_launch<GPTQ_F16>(a, codes, wide, max_chunks, outer, st);
+void grad_launch_f16(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, GradStage stage, hipStream_t st) {
+  grad_launch<GPTQ_F16>(a, codes, wide, max_chunks, stage, st);
 }
 
 }  // namespace gq

@@ -11,7 +11,7 @@ namespace gq {
 // range of tokens, then places it.
 struct GradSortShared {
   uint32_t hist[4][kGradMaxAdapters];
-  uint32_t scan[4];
+  uint32_t scan[4], none[4];
 };
 
 __device__ inline void grad_sort(const GradArgs& a, GradSortShared& sh) {
@@ -30,13 +30,17 @@ __device__ inline void grad_sort(const GradArgs& a, GradSortShared& sh) {
       ad[u] = m < last && v >= 0 && v < a.n ? v : -1;
     }
   };
+  uint32_t none = 0;
   for (int64_t m0 = first; m0 < last; m0 += 64 * kU) {
     int ad[kU];
     read(m0, ad);
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < kU; ++u) {
       if (ad[u] >= 0) atomicAdd(&sh.hist[wave][ad[u]], 1u);   // counts: their order is nothing
+      none += __popcll(__ballot(ad[u] < 0 && m0 + u * 64 + lane < last));
+    }
   }
+  if (lane == 0) sh.none[wave] = none;
   __syncthreads();
   // thread t has adapters kE t .. kE t + kE - 1
   uint32_t count[kE], parts[kE], sum[3] = {0u, 0u, 0u};
@@ -90,9 +94,12 @@ __device__ inline void grad_sort(const GradArgs& a, GradSortShared& sh) {
     base[1] += parts[e];
     base[2] += parts[e] > 1 ? parts[e] : 0u;
   }
+  uint32_t outside = total[0];   // where this wave's tokens without an adapter go
+  for (int w = 0; w < wave; ++w) outside += sh.none[w];
   if (t == 0) {
     a.at.count[0] = (int)total[1];
     a.at.count[1] = (int)total[0];
+    a.at.count[2] = (int)(total[0] + sh.none[0] + sh.none[1] + sh.none[2] + sh.none[3]);
   }
   __syncthreads();
   for (int64_t m0 = first; m0 < last; m0 += 64 * kU) {
@@ -110,6 +117,10 @@ __device__ inline void grad_sort(const GradArgs& a, GradSortShared& sh) {
         if (ad[u] == one) mine = (int)(at + __popcll(same & ((1ull << lane) - 1)));
         if (lane == 0) sh.hist[wave][one] = at + __popcll(same);
       }
+      const bool lone = ad[u] < 0 && m0 + u * 64 + lane < last;
+      const uint64_t others = __ballot(lone);
+      if (lone) mine = (int)(outside + __popcll(others & ((1ull << lane) - 1)));
+      outside += __popcll(others);
       if (mine >= 0) a.at.order[mine] = (int32_t)(m0 + u * 64 + lane);
     }
   }
@@ -126,14 +137,22 @@ __device__ inline void grad_sort(const GradArgs& a, GradSortShared& sh) {
 }
 
 // ---------------------------------------------------------------- U and T
-// A wave takes 32 tokens, all ranks and one part of the sum, a block of 128 at a time.
-// Of a block lane (c16, q) has elements 64 u + 16 q + 8 h + 0..7 of its row in step
-// 2 u + h, so that codes come 16 bytes at a time.  D: rows = ranks, columns = tokens.
+// A workgroup takes 128 tokens, 32 a wave, up to 64 ranks and one part of the sum, a block
+// of 128 at a time; the factors' block is laid out in LDS as operands for all four waves
+// while the one before is multiplied.  Of a block lane (c16, q) has elements 64 u + 16 q +
+// 8 h + 0..7 of its row in step j = 2 u + h, so that codes come 16 bytes at a time.
+// D: rows = ranks, columns = tokens.
 //   kRows false: F is [rank][K]; D's row i of tile p is rank 16 p + i.
 //   kRows true: F is [K][rank]; a lane loads kR ranks of eight rows and turns them;
 //   row i of tile p is rank kR i + p.
+template <int kR>
+struct GradProjectShared {
+  u32x4 f[2][4 * kR][64];           // [buffer][step, rank tile][lane]
+  int adapter[128];
+};
+
 template <int kD, int kF, bool kRows, int kR>
-__device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& s, int id) {
+__device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& s, int id, GradProjectShared<kR>& sh) {
   const int group = id % a.groups, rank0 = id / a.groups % a.halves * 64, part = id / (a.groups * a.halves);
   const int rank = a.halves > 1 ? min(a.rank - rank0, 64) : a.rank;   // of this half
   constexpr int kT = Eight<kD>::kTerms;
@@ -141,11 +160,13 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
   constexpr bool kHalf = kF == GPTQ_F16 && kD != GPTQ_F32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
-  const int64_t m0 = ((int64_t)group * 4 + wave) * kGradTile;
-  if (m0 >= a.M) return;
-  const int64_t mine_at = m0 + (lane & 31);
-  int mine = mine_at < a.M ? a.adapter[mine_at] : -1;
-  if (mine < 0 || mine >= a.n) mine = -1;
+  const int64_t g0 = (int64_t)group * 128, m0 = g0 + wave * kGradTile;
+  if (threadIdx.x < 128) {
+    const int v = g0 + threadIdx.x < a.M ? a.adapter[g0 + threadIdx.x] : -1;
+    sh.adapter[threadIdx.x] = v >= 0 && v < a.n ? v : -1;
+  }
+  __syncthreads();
+  const int mine = sh.adapter[wave * kGradTile + (lane & 31)];
   const char* x[2];
   const uint8_t* sc[2];
 #pragma unroll
@@ -155,26 +176,75 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
     sc[t] = kD == GPTQ_E4M3 ? s.scales + m * s.nb : nullptr;
   }
   const int b0 = part * s.per, b1 = min(b0 + s.per, s.nb);
-  const bool even = a.rank % kR == 0;   // then a lane's ranks are there together, or none of them
-  uint32_t left = (uint32_t)__ballot(mine >= 0);
-  while (left) {
-    const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-    left &= ~(uint32_t)__ballot(mine == ad);
+  int ad = -1;
+  for (;;) {
+    // the next adapter among the 128 tokens, the same for all waves
+    const int v0 = sh.adapter[lane], v1 = sh.adapter[lane + 64];
+    constexpr float kNone = kGradMaxAdapters;
+    const float next = wave_reduce(min(v0 > ad ? (float)v0 : kNone, v1 > ad ? (float)v1 : kNone),
+                                   [](float p, float r) { return min(p, r); });
+    if (next == kNone) break;
+    ad = __builtin_amdgcn_readfirstlane((int)next);
+    const bool here = __ballot(mine == ad) != 0;
     const uint16_t* f = s.F + (int64_t)ad * a.rank * s.K + (kRows ? rank0 : (int64_t)rank0 * s.K);
-    f32x4 acc[kR][2];
+    // this wave's kR operands of a block: step `wave` of all rank tiles; rows of B are
+    // turned when they are there
+    struct Factor {
+      u32x4 w[kRows ? 1 : kR];
+      uint16_t v[kRows ? 8 : 1][kR];
+    };
+    auto read_factor = [&](int b, Factor& w, auto even, auto whole) {
+      const int k = b * kF8Block + wave / 2 * 64 + wave % 2 * 8, kq = q * 16;   // the wave's, the lane's
+      if constexpr (!kRows) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) acc[r][0] = acc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < kR; ++r) {
+          const uint32_t row = (uint32_t)min(r * 16 + c16, rank - 1) * (uint32_t)s.K;
+          if constexpr (whole) w.w[r] = load8(f + k + (row + kq));
+          else w.w[r] = load8_end(f + row, k + kq, s.K);
+        }
+      } else {
+        const uint32_t r0 = c16 * kR < rank ? c16 * kR : 0;   // rows of D behind the rank are not stored
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint16_t* row = whole ? f + (int64_t)(k + i) * a.rank + (uint32_t)(kq * a.rank + (even ? r0 : 0))
+                                      : f + (int64_t)min(k + kq + i, s.K - 1) * a.rank + (even ? r0 : 0);
+          if constexpr (even) {
+            __builtin_memcpy(w.v[i], __builtin_assume_aligned(row, 2), 2 * kR);
+          } else {
+#pragma unroll
+            for (int p = 0; p < kR; ++p) w.v[i][p] = row[min(c16 * kR + p, rank - 1)];
+          }
+          // zeros behind the last row: its infinity times the zeros of D would be a NaN
+          if constexpr (!whole) {
+#pragma unroll
+            for (int p = 0; p < kR; ++p) w.v[i][p] = k + kq + i < s.K ? w.v[i][p] : (uint16_t)0;
+          }
+        }
+      }
+    };
+    auto write_factor = [&](int buffer, const Factor& w) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if constexpr (kRows) {
+          u32x4 t;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = w.v[2 * i][r] | (uint32_t)w.v[2 * i + 1][r] << 16;
+          sh.f[buffer][wave * kR + r][lane] = t;
+        } else {
+          sh.f[buffer][wave * kR + r][lane] = w.w[r];
+        }
+      }
+    };
     struct Block {
       Eight<kD> d[4][2];
       uint32_t sb[2];
     };
-    auto read = [&](int b, Block& k) {
-      const bool whole = (b + 1) * kF8Block <= s.K;
+    auto read = [&](int b, Block& k, auto whole) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         k.sb[t] = 127u;
         if constexpr (kD == GPTQ_E4M3) k.sb[t] = sc[t][b];
-        if (whole || kD == GPTQ_E4M3) {   // codes are there up to the block's end
+        if constexpr (whole || kD == GPTQ_E4M3) {   // codes are there up to the block's end
 #pragma unroll
           for (int j = 0; j < 4; ++j) k.d[j][t].load(x[t], b * kF8Block + j / 2 * 64 + q * 16 + j % 2 * 8);
         } else {
@@ -183,36 +253,10 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
         }
       }
     };
-    // the factors' operand of step j
-    auto factor = [&](int b, int j, u32x4 (&w)[kR]) {
-      const int k = b * kF8Block + j / 2 * 64 + q * 16 + j % 2 * 8;
-      if constexpr (!kRows) {
+    f32x4 acc[kR][2];
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const uint16_t* row = f + (int64_t)min(r * 16 + c16, rank - 1) * s.K;
-          if ((b + 1) * kF8Block <= s.K) w[r] = load8(row + k);
-          else w[r] = load8_end(row, k, s.K);
-        }
-      } else {
-        uint16_t v[8][kR];
-        if (even) {
-          const int r0 = c16 * kR < rank ? c16 * kR : 0;   // rows of D behind the rank are not stored
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            __builtin_memcpy(v[i], __builtin_assume_aligned(f + (int64_t)min(k + i, s.K - 1) * a.rank + r0, 2), 2 * kR);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int p = 0; p < kR; ++p) v[i][p] = f[(int64_t)min(k + i, s.K - 1) * a.rank + min(c16 * kR + p, rank - 1)];
-        }
-#pragma unroll
-        for (int p = 0; p < kR; ++p)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[p][i] = v[2 * i][p] | (uint32_t)v[2 * i + 1][p] << 16;
-      }
-    };
-    auto multiply = [&](int b, const Block& k) {
+    for (int r = 0; r < kR; ++r) acc[r][0] = acc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](int buffer, const Block& k) {
       f32x4 one[kHalf && kD == GPTQ_E4M3 ? kR : 1][2];
       if constexpr (kHalf && kD == GPTQ_E4M3) {
 #pragma unroll
@@ -221,7 +265,9 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         u32x4 w[kR];
-        factor(b, j, w);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) w[r] = sh.f[buffer][j * kR + r][lane];
+        if constexpr (kR == 4) __builtin_amdgcn_sched_barrier(0);   // or all steps' operands are held at once
         if constexpr (kHalf) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -265,28 +311,54 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
         }
       }
     };
-    if constexpr (kD == GPTQ_F32) {
-      for (int b = b0; b < b1; ++b) {
-        Block k;
-        read(b, k);
-        multiply(b, k);
-      }
-    } else {
-      // a block's rows are asked for while the one before is multiplied
-      Block even_block, odd_block;
-      read(b0, even_block);
-      for (int b = b0; b < b1; b += 2) {
-        read(min(b + 1, b1 - 1), odd_block);
-        multiply(b, even_block);
-        if (b + 1 < b1) {
-          read(min(b + 2, b1 - 1), even_block);
-          multiply(b + 1, odd_block);
+    // A block's rows and factors are asked for while the one before is multiplied (rows
+    // of fp32 behind it: they are too many registers).  Nothing in the loop is asked for
+    // on a condition: where paths with and without loads meet, the compiler waits for all.
+    const int bw = min(b1, s.K / kF8Block);   // behind the whole blocks
+    constexpr std::true_type kWhole{};
+    constexpr bool kAhead = kD != GPTQ_F32;
+    // take: whether this wave has tokens of the adapter
+    auto sum = [&](auto take, auto even) {
+      Factor w;
+      Block k0, k1;
+      auto step = [&](int b, int buffer, const Block& now, Block& then) {
+        read_factor(b, w, even, kWhole);
+        if constexpr (take && kAhead) read(b, then, kWhole);
+        if constexpr (take) multiply(buffer, now);
+        write_factor(buffer ^ 1, w);
+        if constexpr (take && !kAhead) read(b, then, kWhole);
+        __syncthreads();
+      };
+      if (b0 < bw) {
+        read_factor(b0, w, even, kWhole);
+        if constexpr (take) read(b0, k0, kWhole);
+        write_factor(0, w);
+        __syncthreads();
+        for (int b = b0; b < bw; b += 2) {
+          step(min(b + 1, bw - 1), 0, k0, k1);
+          if (b + 1 >= bw) break;
+          step(min(b + 2, bw - 1), 1, k1, k0);
         }
       }
-    }
+      if (bw < b1) {   // nobody multiplies from the first buffer any more
+        read_factor(bw, w, even, std::false_type{});
+        write_factor(0, w);
+        if constexpr (take) read(bw, k0, std::false_type{});
+        __syncthreads();
+        if constexpr (take) multiply(0, k0);
+        __syncthreads();
+      }
+    };
+    // a barrier counts waves, wherever each of them meets it
+    auto any = [&](auto even) {
+      if (here) sum(std::true_type{}, even);
+      else sum(std::false_type{}, even);
+    };
+    if (!kRows || a.rank % kR == 0) any(std::true_type{});   // a lane's ranks are there together, or none of them
+    else any(std::false_type{});
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (__shfl(mine, t * 16 + c16) != ad) continue;
+      if (sh.adapter[wave * kGradTile + t * 16 + c16] != ad) continue;
       float* out = s.sums + ((int64_t)part * a.M + m0 + t * 16 + c16) * a.rp + rank0;
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
@@ -304,12 +376,12 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
   }
 }
 
-// Workgroups: the sort, then X's parts, dY's parts, and tiles of 32 x 32 of A to turn.
+// Workgroups: the sort, then X's parts and dY's parts.
 template <int kX, int kY, int kF, int kR>
-__global__ __launch_bounds__(256) void lora_grad_project_kernel(GradArgs a) {
+__global__ __launch_bounds__(256, kY == GPTQ_F32 ? 1 : 2) void lora_grad_project_kernel(GradArgs a) {
   __shared__ union {
     GradSortShared sort;
-    uint16_t tile[32][34];
+    GradProjectShared<kR> project;
   } sh;
   int id = blockIdx.x;
   if (id == 0) {
@@ -317,56 +389,51 @@ __global__ __launch_bounds__(256) void lora_grad_project_kernel(GradArgs a) {
     return;
   }
   id -= 1;
-  const int wgs = a.groups * a.halves;
-  if (id < wgs * a.side[0].splits) {
-    grad_project<kX, kF, false, kR>(a, a.side[0], id);
-    return;
-  }
-  id -= wgs * a.side[0].splits;
-  if (id < wgs * a.side[1].splits) {
-    grad_project<kY, kF, true, kR>(a, a.side[1], id);
-    return;
-  }
-  id -= wgs * a.side[1].splits;
-  const int ad = id / a.a_tiles, i = id % a.a_tiles, K = a.side[0].K;
-  const int rank_tiles = (a.rank + 31) / 32, r0 = i % rank_tiles * 32, k0 = i / rank_tiles * 32;
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-#pragma unroll
-  for (int j = 0; j < 32; j += 8)
-    sh.tile[y + j][x] = r0 + y + j < a.rank && k0 + x < K ? a.A[((int64_t)ad * a.rank + r0 + y + j) * K + k0 + x] : 0;
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 32; j += 8)
-    if (k0 + y + j < K && r0 + x < a.rank) a.a_turned[((int64_t)ad * K + k0 + y + j) * a.rank + r0 + x] = sh.tile[x][y + j];
+  const int x_parts = a.groups * a.halves * a.side[0].splits;
+  if (id < x_parts) grad_project<kX, kF, false, kR>(a, a.side[0], id, sh.project);
+  else grad_project<kY, kF, true, kR>(a, a.side[1], id - x_parts, sh.project);
 }
 
 // ---------------------------------------------------------------- sums over tokens
-// A workgroup sums a chunk of one adapter's tokens for 128 columns and all ranks; its
-// waves take the steps of 32 tokens in turn.  D: rows = ranks, columns = columns: lane
-// c16 holds columns 8 c16 .. 8 c16 + 7, column p of them in tile p.
-constexpr int kOuterWaves = 4;
+// A workgroup sums a chunk of one adapter's tokens for 256 columns and up to 64 ranks: two
+// waves side by side, four taking the steps of 32 tokens in turn.  U (or T) comes into
+// LDS by direct loads, as operands, a step ahead.  D: rows = ranks, columns = columns:
+// lane c16 holds columns 8 c16 .. 8 c16 + 7, column p of them in tile p.
+constexpr int kOuterSplit = 4;
+constexpr int kOuterWaves = 2 * kOuterSplit;
+
+template <int kR>
+struct GradOuterShared {
+  u32x4 u[kOuterSplit][3 * kR][64];   // [wave's tokens][term, rank tile][lane]
+};
 
 template <int kD, int kR, bool kRankFirst>
 __device__ __forceinline__ void grad_outer(const GradArgs& a, const GradSide& s, int block, int rank0,
-                                           const GradChunk& ch, f32x4 (*red)[64]) {
+                                           const GradChunk& ch, GradOuterShared<kR>& u0, GradOuterShared<kR>& u1) {
   constexpr int kT = Eight<kD>::kTerms;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c16 = lane & 15, q = lane >> 4;
-  const int col = block * kF8Block + c16 * 8;
-  const bool whole = (block + 1) * kF8Block <= s.K || kD == GPTQ_E4M3;
+  const int c16 = lane & 15, q = lane >> 4, beside = wave & 1, split = wave >> 1;
+  const int block128 = block * 2 + beside, col = block128 * kF8Block + c16 * 8;
+  // an odd number of 128s leaves a wave without columns, and an adapter may have no
+  // tokens: nothing need stand in the order at its place then
+  const bool some = block128 * kF8Block < s.K && ch.begin < ch.end;
+  const bool whole = (block128 + 1) * kF8Block <= s.K || kD == GPTQ_E4M3;
   const uint16_t* by = s.by + (int64_t)(rank0 + c16) * a.P + 8 * q;
   f32x4 acc[kR][8];
 #pragma unroll
   for (int r = 0; r < kR; ++r)
 #pragma unroll
     for (int p = 0; p < 8; ++p) acc[r][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kStep = kOuterSplit * kGradTile;
+  const int first = ch.begin + split * kGradTile, steps = (ch.end - ch.begin + kStep - 1) / kStep;
+  auto clamp = [&](int pos) { return pos < ch.end ? pos : ch.begin; };
   struct Step {
     Eight<kD> e[8];
     uint32_t sb[8];
   };
   // a run is filled up to the step's end with tokens that U and T have zeros for
   auto tokens = [&](int pos, int4 (&v)[2]) {
-    const int4* p = reinterpret_cast<const int4*>(a.at.order + pos + 8 * q);
+    const int4* p = reinterpret_cast<const int4*>(a.at.order + clamp(pos) + 8 * q);
     v[0] = p[0];
     v[1] = p[1];
   };
@@ -378,94 +445,317 @@ __device__ __forceinline__ void grad_outer(const GradArgs& a, const GradSide& s,
       if (whole) d.e[i].load(grad_row<kD>(s, tok), col);
       else d.e[i].load_end(grad_row<kD>(s, tok), col, s.K);
       d.sb[i] = 127u;
-      if constexpr (kD == GPTQ_E4M3) d.sb[i] = s.scales[tok * s.nb + block];
+      if constexpr (kD == GPTQ_E4M3) d.sb[i] = s.scales[tok * s.nb + block128];
     }
   };
-  constexpr int kStep = kOuterWaves * kGradTile;
-  const int first = ch.begin + wave * kGradTile;
-  if (first < ch.end) {
-    // rows are asked for a step ahead, as soon as the ones before are turned; their
-    // numbers two steps ahead
-    int4 next[2];
-    Step d;
-    auto clamp = [&](int pos) { return pos < ch.end ? pos : first; };
+  // a wave loads every other operand of its tokens
+  auto fetch = [&](int pos, GradOuterShared<kR>& to) {
+    const uint16_t* from = by + clamp(pos);
+#pragma unroll
+    for (int i = 0; i < 3 * kR; i += 2) {
+      const int o = min(i + beside, 3 * kR - 1);
+      lds_load16(from + (int64_t)(o / kR * a.r16 + o % kR * 16) * a.P, reinterpret_cast<char*>(to.u[split][o]));
+    }
+  };
+  // columns 2 i and 2 i + 1 of eight tokens as operands
+  auto turn = [&](const Step& d, int i, u32x4 (&c)[2][kT]) {
+    uint32_t x[8][kT];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d.e[j].pair(i, grad_scale(d.sb[j]), x[j]);
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c[0][t][j] = __builtin_amdgcn_perm(x[2 * j + 1][t], x[2 * j][t], 0x05040100u);
+        c[1][t][j] = __builtin_amdgcn_perm(x[2 * j + 1][t], x[2 * j][t], 0x07060302u);
+      }
+  };
+  auto operand = [&](const GradOuterShared<kR>& from, int r, u32x4 (&u)[3]) {
+#pragma unroll
+    for (int t = 0; t < 3; ++t) u[t] = from.u[split][t * kR + r][lane];
+  };
+  int4 next[2];
+  Step d;
+  if (some) {
     tokens(first, next);
     read(next, d);
-    tokens(clamp(first + kStep), next);
-    for (int pos = first; pos < ch.end; pos += kStep) {
-      u32x4 c[8][kT];
+    tokens(first + kStep, next);
+  }
+  fetch(first, u0);
+#define GQ_GRAD_STEP(i, CUR, NXT)                                                       \
+  {                                                                                     \
+    const int pos = first + (i) * kStep;                                                \
+    __builtin_amdgcn_s_waitcnt(0x0070);   /* vmcnt(0) lgkmcnt(0) */                     \
+    asm volatile("s_barrier" ::: "memory");                                             \
+    fetch(pos + kStep, NXT);                                                            \
+    if (some && pos < ch.end) {                                                         \
+      if constexpr (kT == 1) {                                                          \
+        /* all turned, so that the next rows can be asked for */                        \
+        u32x4 c[4][2][kT];                                                              \
+        _Pragma("unroll") for (int p = 0; p < 4; ++p) turn(d, p, c[p]);                 \
+        read(next, d);                                                                  \
+        tokens(pos + 2 * kStep, next);                                                  \
+        _Pragma("unroll") for (int r = 0; r < kR; ++r) {                                \
+          u32x4 u[3];                                                                   \
+          operand(CUR, r, u);                                                           \
+          _Pragma("unroll") for (int p = 0; p < 8; ++p) acc[r][p] = grad_mfma(u, c[p / 2][p % 2], acc[r][p]); \
+        }                                                                               \
+      } else {                                                                          \
+        _Pragma("unroll") for (int p = 0; p < 8; p += 2) {                              \
+          u32x4 c[2][kT];                                                               \
+          turn(d, p / 2, c);                                                            \
+          _Pragma("unroll") for (int r = 0; r < kR; ++r) {                              \
+            u32x4 u[3];                                                                 \
+            operand(CUR, r, u);                                                         \
+            acc[r][p] = grad_mfma(u, c[0], acc[r][p]);                                  \
+            acc[r][p + 1] = grad_mfma(u, c[1], acc[r][p + 1]);                          \
+          }                                                                             \
+          __builtin_amdgcn_sched_barrier(0);                                            \
+        }                                                                               \
+        read(next, d);                                                                  \
+        tokens(pos + 2 * kStep, next);                                                  \
+      }                                                                                 \
+    }                                                                                   \
+  }
+  for (int i = 0; i < steps; i += 2) {
+    GQ_GRAD_STEP(i, u0, u1)
+    GQ_GRAD_STEP(i + 1, u1, u0)
+  }
+#undef GQ_GRAD_STEP
+  // no direct load is in flight, and nobody reads, when the sums use the same memory:
+  // four columns of a lane at a time, the last waves' in what two buffers leave
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __syncthreads();
+  static_assert(kOuterSplit == 4 && sizeof(u0) == 12 * kR * 64 * sizeof(f32x4));
+  f32x4(*red0)[64] = reinterpret_cast<f32x4(*)[64]>(u0.u);
+  f32x4(*red1)[64] = reinterpret_cast<f32x4(*)[64]>(u1.u);
+  auto place = [&](int w, int r, int p) -> f32x4& {
+    if (w == 1) return red0[(r * 4 + p) * 2 + beside][lane];
+    if (w == 2) return red1[(r * 4 + p) * 2 + beside][lane];
+    return (p < 2 ? red0 : red1)[8 * kR + (r * 2 + p % 2) * 2 + beside][lane];
+  };
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t x[8][kT];
+  for (int half = 0; half < 2; ++half) {
+    if (half) __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d.e[j].pair(i, grad_scale(d.sb[j]), x[j]);
+    for (int w = 1; w < 4; ++w)
+      if (split == w) {
 #pragma unroll
-        for (int t = 0; t < kT; ++t)
+        for (int r = 0; r < kR; ++r)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            c[2 * i][t][j] = __builtin_amdgcn_perm(x[2 * j + 1][t], x[2 * j][t], 0x05040100u);
-            c[2 * i + 1][t][j] = __builtin_amdgcn_perm(x[2 * j + 1][t], x[2 * j][t], 0x07060302u);
-          }
+          for (int p = 0; p < 4; ++p) place(w, r, p) = acc[r][half * 4 + p];
       }
-      read(next, d);
-      tokens(clamp(pos + 2 * kStep), next);
+    __syncthreads();
+    if (split == 0) {
 #pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        u32x4 u[3];
+      for (int w = 1; w < 4; ++w)
 #pragma unroll
-        for (int t = 0; t < 3; ++t) u[t] = *reinterpret_cast<const u32x4*>(by + (int64_t)(t * a.r16 + r * 16) * a.P + pos);
+        for (int r = 0; r < kR; ++r)
 #pragma unroll
-        for (int p = 0; p < 8; ++p) acc[r][p] = grad_mfma(u, c[p], acc[r][p]);
-      }
+          for (int p = 0; p < 4; ++p) acc[r][half * 4 + p] += place(w, r, p);
     }
   }
-  // the waves' sums one after the other
-  for (int w = kOuterWaves - 1; w > 0; --w) {
-    if (wave == w) {
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int p = 0; p < 8; ++p) red[r * 8 + p][lane] = acc[r][p];
-    }
-    __syncthreads();
-    if (wave == w - 1) {
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int p = 0; p < 8; ++p) acc[r][p] += red[r * 8 + p][lane];
-    }
-    __syncthreads();
-  }
-  if (wave != 0) return;
+  if (split != 0) return;
   const int64_t each = (int64_t)a.rank * s.K;
   float* out = ch.slot < 0 ? s.grad + ch.adapter * each : s.part + ch.slot * each;
 #pragma unroll
-  for (int r = 0; r < kR; ++r)
+  for (int r = 0; r < kR; ++r) {
+    const int rank = rank0 + r * 16 + 4 * q;
+    if (rank + 4 <= a.rank && col + 8 <= s.K) {
+      if constexpr (kRankFirst) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rank = rank0 + r * 16 + 4 * q + i;
-      if (rank >= a.rank) continue;
+        for (int i = 0; i < 4; ++i) {
+          float v[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) v[p] = acc[r][p][i];
+          __builtin_memcpy(__builtin_assume_aligned(out + (int64_t)(rank + i) * s.K + col, 4), v, 32);
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          __builtin_memcpy(__builtin_assume_aligned(out + (int64_t)(col + p) * a.rank + rank, 4), &acc[r][p], 16);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int p = 0; p < 8; ++p)
-        if (col + p < s.K) out[kRankFirst ? (int64_t)rank * s.K + col + p : (int64_t)(col + p) * a.rank + rank] = acc[r][p][i];
-    }
+        if (rank + i < a.rank && col + p < s.K)
+          out[kRankFirst ? (int64_t)(rank + i) * s.K + col + p : (int64_t)(col + p) * a.rank + rank + i] = acc[r][p][i];
+  }
 }
 
 template <int kX, int kY, int kR>
 __global__ __launch_bounds__(64 * kOuterWaves) void lora_grad_outer_kernel(GradArgs a) {
-  __shared__ __align__(16) f32x4 red[kR * 8][64];
+  __shared__ GradOuterShared<kR> u0, u1;
   const int blocks = a.side[0].blocks + a.side[1].blocks;
   const int block = blockIdx.x % blocks, rank0 = blockIdx.x / blocks % a.halves * 64, ci = blockIdx.x / (blocks * a.halves);
   if (ci >= a.at.count[0]) return;
   const GradChunk ch = a.at.chunks[ci];
-  if (block < a.side[0].blocks) grad_outer<kX, kR, true>(a, a.side[0], block, rank0, ch, red);
-  else grad_outer<kY, kR, false>(a, a.side[1], block - a.side[0].blocks, rank0, ch, red);
+  if (block < a.side[0].blocks) grad_outer<kX, kR, true>(a, a.side[0], block, rank0, ch, u0, u1);
+  else grad_outer<kY, kR, false>(a, a.side[1], block - a.side[0].blocks, rank0, ch, u0, u1);
 }
 
+// ---------------------------------------------------------------- dX
+// A wave keeps A of 16 kC columns as operands (turned in registers) and takes 16 sorted
+// tokens at a time, which share an adapter; base and U of the next 16 are asked for
+// before.  D: rows = tokens, columns = columns: a lane has kC consecutive columns of four
+// tokens, so that base and dX move 16 bytes a lane.
+template <int kF, int kOut, int kS, int kC>
+__global__ __launch_bounds__(256, 2) void lora_grad_input_kernel(GradArgs a) {
+  constexpr int kA = kF == GPTQ_F16 ? 2 : 1;
+  constexpr int kE = kOut == GPTQ_F32 ? 4 : 2;
+  constexpr int kWords = kC * kE / 4;
+  constexpr bool kAhead = kS < 4;   // U of 128 ranks is too many registers
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, q = lane >> 4;
+  const int K = a.side[0].K, wide = 64 * kC, blocks = (K + wide - 1) / wide;
+  const int col = blockIdx.x % blocks * wide + wave * 16 * kC + c16 * kC;
+  const int runs = a.at.count[1], first = blockIdx.x / blocks * a.input_tokens;
+  const int end = min(first + a.input_tokens, a.at.count[2]);
+  const bool whole = col + kC <= K;
+  u32x4 f[kC][kS][kA];
+  int held = -1;
+  struct Tile {
+    int tok[4], adapter, pos;
+    uint32_t in[4][kWords];
+    u32x4 u[kAhead ? kS : 1][3];
+  };
+  auto read_u = [&](int pos, u32x4 (*u)[3]) {
+#pragma unroll
+    for (int k = 0; k < kS; ++k)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        u[k][i] = *reinterpret_cast<const u32x4*>(a.side[1].flat + ((int64_t)i * a.P + pos + c16) * a.rk + k * 32 + 8 * q);
+  };
+  auto tokens = [&](int pos, int (&tok)[4], int& lead) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tok[i] = pos + 4 * q + i < end ? a.at.order[pos + 4 * q + i] : -1;
+    lead = pos < min(end, runs) ? a.at.order[pos] : 0;
+  };
+  auto read = [&](int pos, const int (&tok)[4], int lead, Tile& t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.tok[i] = tok[i];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) t.in[i][w] = 0;
+      if (!a.base || tok[i] < 0) continue;
+      const char* p = static_cast<const char*>(a.base) + ((int64_t)tok[i] * a.ld_b + col) * kE;
+      if (whole) {
+        __builtin_memcpy(t.in[i], __builtin_assume_aligned(p, kE), kC * kE);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (col + c < K) {
+            if constexpr (kE == 4) t.in[i][c] = load_bits<kOut>(p, c);
+            else t.in[i][c / 2] |= load_bits<kOut>(p, c) << (16 * (c & 1));
+          }
+      }
+    }
+    t.adapter = -1;
+    if (pos >= min(end, runs)) return;
+    t.adapter = a.adapter[lead ^ (lead >> 31)];
+    t.pos = pos;
+    if constexpr (kAhead) read_u(pos, t.u);
+  };
+  auto hold = [&](int ad) {
+    held = ad;
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      Eight<kF> e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rank = k * 32 + 8 * q + i;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) e[i].w[w] = 0;
+        if (rank < a.rank) {
+          const uint16_t* row = a.side[0].F + ((int64_t)ad * a.rank + rank) * K;
+          if (whole) {
+            __builtin_memcpy(e[i].w, __builtin_assume_aligned(row + col, 2), 2 * kC);
+          } else {
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+              if (col + c < K) e[i].w[c / 2] |= (uint32_t)row[col + c] << (16 * (c & 1));
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kC; c += 2) {
+        uint32_t x[8][kA];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i].pair(c / 2, 1.f, x[i]);
+#pragma unroll
+        for (int t = 0; t < kA; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[c][k][t][j] = __builtin_amdgcn_perm(x[2 * j + 1][t], x[2 * j][t], 0x05040100u);
+            f[c + 1][k][t][j] = __builtin_amdgcn_perm(x[2 * j + 1][t], x[2 * j][t], 0x07060302u);
+          }
+      }
+    }
+  };
+  auto add = [&](const Tile& t) {
+    const bool some = t.adapter >= 0;   // else the base's bits stay
+    f32x4 acc[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (some) {
+      if (t.adapter != held) hold(t.adapter);
+      u32x4 now[kAhead ? 1 : kS][3];
+      if constexpr (!kAhead) read_u(t.pos, now);
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int k = 0; k < kS; ++k) {
+          if constexpr (kAhead) acc[c] = grad_mfma(t.u[k], f[c][k], acc[c]);
+          else acc[c] = grad_mfma(now[k], f[c][k], acc[c]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t.tok[i] < 0) continue;
+      uint32_t out[kWords];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        if constexpr (kE == 4) {
+          out[w] = __float_as_uint(__uint_as_float(t.in[i][w]) + acc[w][i]);
+        } else {
+          out[w] = value_bits<kOut>(lo16<kOut>(t.in[i][w]) + acc[2 * w][i]) |
+                   value_bits<kOut>(hi16<kOut>(t.in[i][w]) + acc[2 * w + 1][i]) << 16;
+        }
+        if (!some) out[w] = t.in[i][w];
+      }
+      char* p = static_cast<char*>(a.dX) + ((int64_t)t.tok[i] * a.ld_dx + col) * kE;
+      if (whole) {
+        __builtin_memcpy(__builtin_assume_aligned(p, kE), out, kC * kE);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (col + c < K) store_bits<kOut>(p, c, kE == 4 ? out[c * kE / 4] : out[c / 2] >> (16 * (c & 1)) & 0xFFFFu);
+      }
+    }
+  };
+  int tok[4], lead;
+  Tile t0, t1;
+  tokens(first, tok, lead);
+  read(first, tok, lead, t0);
+  tokens(first + 16, tok, lead);
+  for (int pos = first; pos < end; pos += 32) {
+    read(pos + 16, tok, lead, t1);
+    tokens(pos + 32, tok, lead);
+    add(t0);
+    read(pos + 32, tok, lead, t0);
+    tokens(pos + 48, tok, lead);
+    add(t1);
+  }
+}
+
+// ---------------------------------------------------------------- launches
 template <int kX, int kY, int kF, int kR>
-static void grad_launch_rank(const GradArgs& a, int64_t max_chunks, bool outer, hipStream_t st) {
-  if (!outer) {
-    const int64_t wgs = 1 + (int64_t)a.groups * a.halves * (a.side[0].splits + a.side[1].splits) + (int64_t)a.n * a.a_tiles;
+static void grad_launch_rank(const GradArgs& a, int64_t max_chunks, GradStage stage, hipStream_t st) {
+  if (stage == kGradProject) {
+    const int64_t wgs = 1 + (int64_t)a.groups * a.halves * (a.side[0].splits + a.side[1].splits);
     hipLaunchKernelGGL((lora_grad_project_kernel<kX, kY, kF, kR>), dim3((unsigned)wgs), dim3(256), 0, st, a);
   } else {
     const int64_t wgs = (a.side[0].blocks + a.side[1].blocks) * a.halves * max_chunks;
@@ -474,18 +764,45 @@ static void grad_launch_rank(const GradArgs& a, int64_t max_chunks, bool outer, 
 }
 
 template <int kX, int kY, int kF>
-static void grad_launch_types(const GradArgs& a, int64_t max_chunks, bool outer, hipStream_t st) {
-  if (a.r16 == 16) grad_launch_rank<kX, kY, kF, 1>(a, max_chunks, outer, st);
-  else if (a.r16 == 32) grad_launch_rank<kX, kY, kF, 2>(a, max_chunks, outer, st);
-  else grad_launch_rank<kX, kY, kF, 4>(a, max_chunks, outer, st);
+static void grad_launch_types(const GradArgs& a, int64_t max_chunks, GradStage stage, hipStream_t st) {
+  if (a.r16 == 16) grad_launch_rank<kX, kY, kF, 1>(a, max_chunks, stage, st);
+  else if (a.r16 == 32) grad_launch_rank<kX, kY, kF, 2>(a, max_chunks, stage, st);
+  else grad_launch_rank<kX, kY, kF, 4>(a, max_chunks, stage, st);
+}
+
+template <int kF, int kOut, int kS>
+static void grad_launch_input_rank(const GradArgs& a, hipStream_t st) {
+  // A takes 64 registers: 4 kS words a column, twice for fp16's two terms
+  constexpr int kC = std::min(kOut == GPTQ_F32 ? 4 : 8, 16 / (kS * (kF == GPTQ_F16 ? 2 : 1)));
+  // in one round of two workgroups a CU
+  const int64_t blocks = cdiv(a.side[0].K, 64 * kC);
+  GradArgs b = a;
+  b.input_tokens = (int)(cdiv(a.P, std::max<int64_t>(1, 512 / blocks) * 16) * 16);
+  const int64_t wgs = blocks * cdiv(a.P, b.input_tokens);
+  hipLaunchKernelGGL((lora_grad_input_kernel<kF, kOut, kS, kC>), dim3((unsigned)wgs), dim3(256), 0, st, b);
+}
+
+template <int kF, int kOut>
+static void grad_launch_input(const GradArgs& a, hipStream_t st) {
+  if (a.rk == 32) grad_launch_input_rank<kF, kOut, 1>(a, st);
+  else if (a.rk == 64) grad_launch_input_rank<kF, kOut, 2>(a, st);
+  else grad_launch_input_rank<kF, kOut, 4>(a, st);
 }
 
 template <int kF>
-static void grad_launch(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, bool outer, hipStream_t st) {
-  if (codes && wide) grad_launch_types<GPTQ_E4M3, GPTQ_F32, kF>(a, max_chunks, outer, st);
-  else if (codes) grad_launch_types<GPTQ_E4M3, kF, kF>(a, max_chunks, outer, st);
-  else if (wide) grad_launch_types<kF, GPTQ_F32, kF>(a, max_chunks, outer, st);
-  else grad_launch_types<kF, kF, kF>(a, max_chunks, outer, st);
+static void grad_launch(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, GradStage stage, hipStream_t st) {
+  if (stage == kGradInput) {
+    if (a.wide_dx) grad_launch_input<kF, GPTQ_F32>(a, st);
+    else grad_launch_input<kF, kF>(a, st);
+  } else if (codes && wide) {
+    grad_launch_types<GPTQ_E4M3, GPTQ_F32, kF>(a, max_chunks, stage, st);
+  } else if (codes) {
+    grad_launch_types<GPTQ_E4M3, kF, kF>(a, max_chunks, stage, st);
+  } else if (wide) {
+    grad_launch_types<kF, GPTQ_F32, kF>(a, max_chunks, stage, st);
+  } else {
+    grad_launch_types<kF, kF, kF>(a, max_chunks, stage, st);
+  }
 }
 
 }  // namespace gq
