@@ -4,8 +4,9 @@ A head W (vocabulary x hidden) is quantized once to int4.  Two teachers are
 fine-tuned versions of it, W + D_0 and W + D_1.  Their answers are kept as the
 top lists of token_logprobs; low-rank adapters beside the quantized head are
 trained on them with distill_topk (lora_add makes the student's logits and
-distill_topk turns them into their gradient in place); then tokens that want
-the one or the other are served together by w4a16_lora_matmul and scored.
+distill_topk turns them into their gradient in place, which lora_grad takes to
+the adapters with the hidden states kept in 8 bits); then tokens that want the
+one or the other are served together by w4a16_lora_matmul and scored.
 
     python examples/recover_head.py [--steps 60]
 """
@@ -30,15 +31,10 @@ def quantize_head(W, X, group_size=128):
                 group_size=group_size), q["Q"][0]
 
 
-def gradients(X, A, B, adapter, scale, dlogits):
-    """Gradients of every adapter's factors from the logits'."""
-    dA, dB = torch.zeros_like(A), torch.zeros_like(B)
-    for i in range(A.shape[0]):
-        rows = adapter == i
-        x, g = X[rows].float(), dlogits[rows].float()
-        dB[i] = scale[i] * g.t() @ (x @ A[i].t())
-        dA[i] = scale[i] * (g @ B[i]).t() @ x
-    return dA, dB
+def gradients(kept, A, B, adapter, scale, dlogits, out=None, ws=None):
+    """Gradients of every adapter's factors from the logits' and the hidden states as fp8_quantize keeps them."""
+    g = P.lora_grad(kept["codes"], dlogits, A, B, adapter, scale, x_scales=kept["scales"], out=out, ws=ws)
+    return g["dA"], g["dB"]
 
 
 def run(steps=60, hidden=512, vocab=8192, tokens=2048, rank=16, k=32, temperature=1.0, seed=0, show=print):
@@ -74,15 +70,18 @@ def run(steps=60, hidden=512, vocab=8192, tokens=2048, rank=16, k=32, temperatur
     loss, ws = P.distill_topk_buffers(logits, k, want_grad=False)
     loss["grad"] = logits                                                    # the gradient replaces the logits
     weight = torch.full((tokens,), 1.0 / tokens, device="cuda")
+    kept = P.fp8_quantize(X)
+    grads, ws_grad = P.lora_grad_buffers(X, logits, A, B)
     history = []
     for step in range(steps + 1):
-        P.lora_add(X, A.bfloat16(), B.bfloat16(), adapter, scale, base=base, Y=logits, ws=ws_lora)
+        Ab, Bb = A.bfloat16(), B.bfloat16()
+        P.lora_add(X, Ab, Bb, adapter, scale, base=base, Y=logits, ws=ws_lora)
         P.distill_topk(logits, top_id, top_lp, temperature, weight=weight, out=loss, ws=ws)
         history.append(float(loss["loss"].mean()))
         if step % 20 == 0 or step == steps:
             show(f"step {step:3d}: loss {history[-1]:.4f}")
         if step < steps:
-            A.grad, B.grad = gradients(X, A, B, adapter, scale, logits)
+            A.grad, B.grad = gradients(kept, Ab, Bb, adapter, scale, logits, grads, ws_grad)
             opt.step()
 
     # tokens of both kinds, and some that want the quantized head itself, in one call

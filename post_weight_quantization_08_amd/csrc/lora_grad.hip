@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void lora_grad_terms_kernel(GradArgs a) {
       for (int t = 0; t < 3; ++t) {
         h[t][i] = value_bits<GPTQ_BF16>(left);
         s.turned[(int64_t)(t * a.r16 + r + i) * a.P + pos] = (uint16_t)h[t][i];
-        left -= bf16_bits_to_f32(h[t][i]);
+        left = isinf(bf16_bits_to_f32(h[t][i])) ? 0.f : left - bf16_bits_to_f32(h[t][i]);   // an infinity is one term
       }
     }
     if (s.flat) {
