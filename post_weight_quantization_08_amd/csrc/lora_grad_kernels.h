@@ -599,65 +599,72 @@ __global__ __launch_bounds__(64 * kOuterWaves) void lora_grad_outer_kernel(GradA
 
 // ---------------------------------------------------------------- dX
 // A wave keeps A of 16 kC columns as operands (turned in registers) and takes 16 sorted
-// tokens at a time, which share an adapter; base and U of the next 16 are asked for
-// before.  D: rows = tokens, columns = columns: a lane has kC consecutive columns of four
-// tokens, so that base and dX move 16 bytes a lane.
-template <int kF, int kOut, int kS, int kC>
+// tokens at a time, which share an adapter.  D: rows = tokens, columns = columns: a lane
+// has kC consecutive columns of four tokens, so that base and dX move 16 bytes a lane.
+// base is asked for three tiles before its turn and U one, whether they are wanted or
+// not: a load on a condition would have the compiler wait for all that are in flight.
+template <int kF, int kOut, bool kBase, int kS, int kC>
 __global__ __launch_bounds__(256, 2) void lora_grad_input_kernel(GradArgs a) {
   constexpr int kA = kF == GPTQ_F16 ? 2 : 1;
   constexpr int kE = kOut == GPTQ_F32 ? 4 : 2;
   constexpr int kWords = kC * kE / 4;
-  constexpr bool kAhead = kS < 4;   // U of 128 ranks is too many registers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, q = lane >> 4;
   const int K = a.side[0].K, wide = 64 * kC, blocks = (K + wide - 1) / wide;
   const int col = blockIdx.x % blocks * wide + wave * 16 * kC + c16 * kC;
-  const int runs = a.at.count[1], first = blockIdx.x / blocks * a.input_tokens;
-  const int end = min(first + a.input_tokens, a.at.count[2]);
+  const int first = blockIdx.x / blocks * a.input_tokens, end = min(first + a.input_tokens, a.at.count[2]);
+  const int runs = min(end, a.at.count[1]);
+  if (first >= end) return;
   const bool whole = col + kC <= K;
   u32x4 f[kC][kS][kA];
   int held = -1;
-  struct Tile {
-    int tok[4], adapter, pos;
-    uint32_t in[4][kWords];
-    u32x4 u[kAhead ? kS : 1][3];
+  struct Place {
+    int tok[4], lead;
   };
-  auto read_u = [&](int pos, u32x4 (*u)[3]) {
+  struct Tile {
+    int tok[4];                       // ~token: not stored
+    uint32_t in[4][kBase ? kWords : 1];
+  };
+  auto tokens = [&](int pos, Place& t) {
+    const int at = min(pos, end - 1) & ~15;
+    const int4 v = *reinterpret_cast<const int4*>(a.at.order + at + 4 * q);   // [P], a multiple of 64
+    const int lead = a.at.order[at], one = lead ^ (lead >> 31), left = end - pos - 4 * q;
+    t.tok[0] = left > 0 ? v.x : ~one;
+    t.tok[1] = left > 1 ? v.y : ~one;
+    t.tok[2] = left > 2 ? v.z : ~one;
+    t.tok[3] = left > 3 ? v.w : ~one;
+    t.lead = one;
+  };
+  auto read = [&](const Place& p, Tile& t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.tok[i] = p.tok[i];
+      if constexpr (kBase) {
+        const int64_t tok = p.tok[i] ^ (p.tok[i] >> 31);
+        const char* row = static_cast<const char*>(a.base) + tok * a.ld_b * kE;
+        if (whole) {
+          __builtin_memcpy(t.in[i], __builtin_assume_aligned(row + (int64_t)col * kE, kE), kC * kE);
+        } else {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) t.in[i][w] = 0;
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            if (col + c < K) {
+              if constexpr (kE == 4) t.in[i][c] = load_bits<kOut>(row, col + c);
+              else t.in[i][c / 2] |= load_bits<kOut>(row, col + c) << (16 * (c & 1));
+            }
+        }
+      }
+    }
+  };
+  u32x4 u[kS][3];
+  auto read_u = [&](int pos) {
+    const int at = min(pos, end - 1) & ~15;
 #pragma unroll
     for (int k = 0; k < kS; ++k)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        u[k][i] = *reinterpret_cast<const u32x4*>(a.side[1].flat + ((int64_t)i * a.P + pos + c16) * a.rk + k * 32 + 8 * q);
-  };
-  auto tokens = [&](int pos, int (&tok)[4], int& lead) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tok[i] = pos + 4 * q + i < end ? a.at.order[pos + 4 * q + i] : -1;
-    lead = pos < min(end, runs) ? a.at.order[pos] : 0;
-  };
-  auto read = [&](int pos, const int (&tok)[4], int lead, Tile& t) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t.tok[i] = tok[i];
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) t.in[i][w] = 0;
-      if (!a.base || tok[i] < 0) continue;
-      const char* p = static_cast<const char*>(a.base) + ((int64_t)tok[i] * a.ld_b + col) * kE;
-      if (whole) {
-        __builtin_memcpy(t.in[i], __builtin_assume_aligned(p, kE), kC * kE);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          if (col + c < K) {
-            if constexpr (kE == 4) t.in[i][c] = load_bits<kOut>(p, c);
-            else t.in[i][c / 2] |= load_bits<kOut>(p, c) << (16 * (c & 1));
-          }
-      }
-    }
-    t.adapter = -1;
-    if (pos >= min(end, runs)) return;
-    t.adapter = a.adapter[lead ^ (lead >> 31)];
-    t.pos = pos;
-    if constexpr (kAhead) read_u(pos, t.u);
+        u[k][i] = *reinterpret_cast<const u32x4*>(a.side[1].flat + ((int64_t)i * a.P + at + c16) * a.rk + k * 32 + 8 * q);
   };
   auto hold = [&](int ad) {
     held = ad;
@@ -695,59 +702,66 @@ __global__ __launch_bounds__(256, 2) void lora_grad_input_kernel(GradArgs a) {
       }
     }
   };
-  auto add = [&](const Tile& t) {
-    const bool some = t.adapter >= 0;   // else the base's bits stay
+  auto add = [&](int pos, int lead, const Tile& t) {
+    const bool some = pos < runs;   // else the base's bits stay
     f32x4 acc[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (some) {
-      if (t.adapter != held) hold(t.adapter);
-      u32x4 now[kAhead ? 1 : kS][3];
-      if constexpr (!kAhead) read_u(t.pos, now);
+      const int ad = __builtin_amdgcn_readfirstlane(a.adapter[lead]);
+      if (ad != held) hold(ad);
 #pragma unroll
       for (int c = 0; c < kC; ++c)
 #pragma unroll
-        for (int k = 0; k < kS; ++k) {
-          if constexpr (kAhead) acc[c] = grad_mfma(t.u[k], f[c][k], acc[c]);
-          else acc[c] = grad_mfma(now[k], f[c][k], acc[c]);
-        }
+        for (int k = 0; k < kS; ++k) acc[c] = grad_mfma(u[k], f[c][k], acc[c]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (t.tok[i] < 0) continue;
       uint32_t out[kWords];
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
+        const uint32_t in = kBase ? t.in[i][w] : 0u;
         if constexpr (kE == 4) {
-          out[w] = __float_as_uint(__uint_as_float(t.in[i][w]) + acc[w][i]);
+          out[w] = __float_as_uint(__uint_as_float(in) + acc[w][i]);
         } else {
-          out[w] = value_bits<kOut>(lo16<kOut>(t.in[i][w]) + acc[2 * w][i]) |
-                   value_bits<kOut>(hi16<kOut>(t.in[i][w]) + acc[2 * w + 1][i]) << 16;
+          out[w] = value_bits<kOut>(lo16<kOut>(in) + acc[2 * w][i]) | value_bits<kOut>(hi16<kOut>(in) + acc[2 * w + 1][i]) << 16;
         }
-        if (!some) out[w] = t.in[i][w];
+        if (!some) out[w] = in;
       }
-      char* p = static_cast<char*>(a.dX) + ((int64_t)t.tok[i] * a.ld_dx + col) * kE;
+      if (t.tok[i] < 0) continue;
+      char* row = static_cast<char*>(a.dX) + (int64_t)t.tok[i] * a.ld_dx * kE;
       if (whole) {
-        __builtin_memcpy(__builtin_assume_aligned(p, kE), out, kC * kE);
+        __builtin_memcpy(__builtin_assume_aligned(row + (int64_t)col * kE, kE), out, kC * kE);
       } else {
 #pragma unroll
         for (int c = 0; c < kC; ++c)
-          if (col + c < K) store_bits<kOut>(p, c, kE == 4 ? out[c * kE / 4] : out[c / 2] >> (16 * (c & 1)) & 0xFFFFu);
+          if (col + c < K) store_bits<kOut>(row, col + c, kE == 4 ? out[c * kE / 4] : out[c / 2] >> (16 * (c & 1)) & 0xFFFFu);
       }
     }
   };
-  int tok[4], lead;
-  Tile t0, t1;
-  tokens(first, tok, lead);
-  read(first, tok, lead, t0);
-  tokens(first + 16, tok, lead);
-  for (int pos = first; pos < end; pos += 32) {
-    read(pos + 16, tok, lead, t1);
-    tokens(pos + 32, tok, lead);
-    add(t0);
-    read(pos + 32, tok, lead, t0);
-    tokens(pos + 48, tok, lead);
-    add(t1);
+  Place p[3];
+  Tile t[3];
+  int leads[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) tokens(first + 16 * i, p[i]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    read(p[i], t[i]);
+    leads[i] = p[i].lead;
+  }
+  Place next;
+  tokens(first + 48, next);
+  read_u(first);
+  for (int pos = first; pos < end;) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i, pos += 16) {
+      // behind the end nothing is stored
+      add(pos, leads[i], t[i]);
+      read_u(pos + 16);
+      read(next, t[i]);
+      leads[i] = next.lead;
+      tokens(pos + 64, next);
+    }
   }
 }
 
@@ -770,30 +784,33 @@ static void grad_launch_types(const GradArgs& a, int64_t max_chunks, GradStage s
   else grad_launch_rank<kX, kY, kF, 4>(a, max_chunks, stage, st);
 }
 
-template <int kF, int kOut, int kS>
+template <int kF, int kOut, bool kBase, int kS>
 static void grad_launch_input_rank(const GradArgs& a, hipStream_t st) {
-  // A takes 64 registers: 4 kS words a column, twice for fp16's two terms
-  constexpr int kC = std::min(kOut == GPTQ_F32 ? 4 : 8, 16 / (kS * (kF == GPTQ_F16 ? 2 : 1)));
+  // A takes up to 64 registers: 4 kS words a column, twice for fp16's two terms; three
+  // tiles of fp32 base up to 48, of 128 ranks 24
+  constexpr int kC = std::min(kOut == GPTQ_F32 ? kS == 4 ? 2 : 4 : 8, 16 / (kS * (kF == GPTQ_F16 ? 2 : 1)));
   // in one round of two workgroups a CU
   const int64_t blocks = cdiv(a.side[0].K, 64 * kC);
   GradArgs b = a;
   b.input_tokens = (int)(cdiv(a.P, std::max<int64_t>(1, 512 / blocks) * 16) * 16);
   const int64_t wgs = blocks * cdiv(a.P, b.input_tokens);
-  hipLaunchKernelGGL((lora_grad_input_kernel<kF, kOut, kS, kC>), dim3((unsigned)wgs), dim3(256), 0, st, b);
+  hipLaunchKernelGGL((lora_grad_input_kernel<kF, kOut, kBase, kS, kC>), dim3((unsigned)wgs), dim3(256), 0, st, b);
 }
 
-template <int kF, int kOut>
+template <int kF, int kOut, bool kBase>
 static void grad_launch_input(const GradArgs& a, hipStream_t st) {
-  if (a.rk == 32) grad_launch_input_rank<kF, kOut, 1>(a, st);
-  else if (a.rk == 64) grad_launch_input_rank<kF, kOut, 2>(a, st);
-  else grad_launch_input_rank<kF, kOut, 4>(a, st);
+  if (a.rk == 32) grad_launch_input_rank<kF, kOut, kBase, 1>(a, st);
+  else if (a.rk == 64) grad_launch_input_rank<kF, kOut, kBase, 2>(a, st);
+  else grad_launch_input_rank<kF, kOut, kBase, 4>(a, st);
 }
 
 template <int kF>
 static void grad_launch(const GradArgs& a, bool codes, bool wide, int64_t max_chunks, GradStage stage, hipStream_t st) {
   if (stage == kGradInput) {
-    if (a.wide_dx) grad_launch_input<kF, GPTQ_F32>(a, st);
-    else grad_launch_input<kF, kF>(a, st);
+    if (a.wide_dx && a.base) grad_launch_input<kF, GPTQ_F32, true>(a, st);
+    else if (a.wide_dx) grad_launch_input<kF, GPTQ_F32, false>(a, st);
+    else if (a.base) grad_launch_input<kF, kF, true>(a, st);
+    else grad_launch_input<kF, kF, false>(a, st);
   } else if (codes && wide) {
     grad_launch_types<GPTQ_E4M3, GPTQ_F32, kF>(a, max_chunks, stage, st);
   } else if (codes) {
