@@ -10,6 +10,12 @@
 // fp32 outputs promise more than that: their codes become bf16 together with the
 // scales, exactly, and go through 16x16x32 bf16 products at half the rate.
 //
+// 8192 x 8192 -> 28672 in codes 1.66 ms, 2.3 PFLOP/s (a large product of the library
+// 3.25): direct loads of a block take as long as its products, and with two buffers
+// of 64 KB little of either is hidden behind the other's end.  48 x 8192 -> 28672 60 us,
+// 4.0 TB/s of weights; one token 4096 -> 4096 8 us, one launch; fp32 outputs 777 x 11000
+// -> 4001 99 us: 9 to quantize the tokens, the rest to turn codes into bf16 and multiply.
+//
 // A lane holds 32 codes of one row; which 32 of the block's 128 does not matter as
 // long as both operands agree (here units q and q + 4 of 16 bytes, q = lane / 16).
 // The weights are the rows of the result, so that a lane ends up with four
