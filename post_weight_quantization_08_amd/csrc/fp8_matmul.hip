@@ -560,6 +560,9 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(F8MmArgs a) {
 //   8192 -> 28672    2 tokens 57 and 44,       16 tokens 102 and 45, 48 70 and 50
 constexpr int kF8Few = 16;
 constexpr int64_t kF8FewRows = 8192;
+// Tiles of 256 by 256 if every CU gets one and they are more than half full: 4096 ->
+// 131072, bf16 (and fp32) in tiles of 256 and in the smaller ones, us: 16 tokens 153 (221)
+// and 126 (129), 100 tokens 183 (231) and 146 (165), 200 tokens 185 (247) and 221 (284).
 // Tiles of 128 tokens if two of them for every CU remain, else 64 (or 32), bf16, us:
 // 300 x 4096 -> 14336 56 and 50, 2048 x 4096 -> 4096 61 and 69.  The sum is split until
 // every CU has a workgroup, into parts of four blocks or more: 65 x 4096 -> 4096 in 1, 4
@@ -582,10 +585,10 @@ static F8Plan f8_plan(int64_t M, int64_t d_in, int64_t d_out, bool codes) {
   }
   p.splits = 1;
   if (!p.few) {
-    p.bm = p.bn = cdiv(M, 256) * cdiv(d_out, 256) >= 256 ? 256 : 128;
+    p.bm = p.bn = M > 128 && cdiv(M, 256) * cdiv(d_out, 256) >= 256 ? 256 : 128;
     if (p.bm == 128) {
       if (M <= 32) p.bm = 32;
-      else if (cdiv(M, 128) * cdiv(d_out, 128) < kF8Wide) p.bm = 64;
+      else if (M <= 64 || cdiv(M, 128) * cdiv(d_out, 128) < kF8Wide) p.bm = 64;
       const int64_t tiles = cdiv(M, p.bm) * cdiv(d_out, 128);
       while (tiles * p.splits < 256 && nb / (p.splits * 2) >= 4) p.splits *= 2;
       p.splits = (int)cdiv(nb, cdiv(nb, p.splits));
