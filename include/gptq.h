@@ -603,7 +603,8 @@ gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_sca
  *   dY        device, M x d_out of `dtype` or GPTQ_F32, row stride ld_dy.
  *   A, B      device, [n_adapters][rank][d_in] and [n_adapters][d_out][rank] of
  *             `dtype` (GPTQ_F16 or GPTQ_BF16), dense; rank <= 128, n_adapters <= 1024,
- *             M, d_in, d_out <= 2^22 (more: GPTQ_EUNSUPPORTED).
+ *             M, d_in, d_out <= 2^22 and n_adapters * (d_in + d_out) <= 2^29 (more:
+ *             GPTQ_EUNSUPPORTED).
  *   scale     device fp32 [n_adapters], or NULL (all 1); adapter device int32 [M],
  *             outside [0, n_adapters): no adapter, the token counts nowhere and
  *             dX = base.

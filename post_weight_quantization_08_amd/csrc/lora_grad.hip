@@ -76,6 +76,14 @@ struct GradPlan {
   size_t order, chunks, parts, count, flat, sums[2], turned[2], part[2], total;
 };
 
+// The last: a launch has fewer than 2^32 threads, and the sums over tokens 512 for every 256
+// columns, 64 ranks and chunk, of which an adapter has one whether it has tokens or not.
+static bool grad_supported(int64_t M, int64_t d_in, int64_t d_out, int64_t rank, int64_t n) {
+  const int64_t most = (int64_t)1 << 22;
+  return rank <= kGradMaxRank && n <= kGradMaxAdapters && M <= most && d_in <= most && d_out <= most &&
+         n * (d_in + d_out) <= ((int64_t)1 << 29);
+}
+
 static GradPlan grad_plan(int64_t M, int64_t d_in, int64_t d_out, int64_t rank, int64_t n) {
   GradPlan p{};
   p.rp = (int)(cdiv(rank, 8) * 8);
@@ -124,9 +132,7 @@ using namespace gq;
 extern "C" gptq_status gptq_lora_grad_workspace_size(int64_t M, int64_t d_in, int64_t d_out, int32_t rank,
                                                      int64_t n_adapters, size_t* bytes_out) {
   GQ_CHECK_ARG(bytes_out && M >= 0 && d_in >= 1 && d_out >= 1 && rank >= 1 && n_adapters >= 1);
-  if (rank > kGradMaxRank || n_adapters > kGradMaxAdapters || M > ((int64_t)1 << 22) || d_in > ((int64_t)1 << 22) ||
-      d_out > ((int64_t)1 << 22))
-    return GPTQ_EUNSUPPORTED;
+  if (!grad_supported(M, d_in, d_out, rank, n_adapters)) return GPTQ_EUNSUPPORTED;
   *bytes_out = grad_plan(std::max<int64_t>(M, 1), d_in, d_out, rank, n_adapters).total;
   return GPTQ_OK;
 }
@@ -147,9 +153,7 @@ extern "C" gptq_status gptq_lora_grad(const void* X, int32_t x_dtype, const uint
   GQ_CHECK_ARG(dX == nullptr || (ld_dx >= d_in && ld_dx <= ((int64_t)1 << 32)));
   GQ_CHECK_ARG(base == nullptr || (dX != nullptr && ld_b >= d_in && ld_b <= ((int64_t)1 << 32)));
   GQ_CHECK_ARG(base == nullptr || base != dX || ld_b == ld_dx);
-  if (rank > kGradMaxRank || n_adapters > kGradMaxAdapters || M > ((int64_t)1 << 22) || d_in > ((int64_t)1 << 22) ||
-      d_out > ((int64_t)1 << 22))
-    return GPTQ_EUNSUPPORTED;
+  if (!grad_supported(M, d_in, d_out, rank, n_adapters)) return GPTQ_EUNSUPPORTED;
   GQ_CHECK_ARG(dA && dB && A && B);
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(A) % 2 == 0 && reinterpret_cast<uintptr_t>(B) % 2 == 0 &&
                reinterpret_cast<uintptr_t>(dA) % 4 == 0 && reinterpret_cast<uintptr_t>(dB) % 4 == 0);
