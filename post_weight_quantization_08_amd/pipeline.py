@@ -653,6 +653,8 @@ def lora_grad(X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor, B: torch.Tenso
     has_dx = "dX" in out
     if has_dx:
         dx = out["dX"].dtype
+    elif want_dx:
+        raise ValueError("want_dx: out has no dX")
     if type(out) is Buffers and out.key == ("lora_grad", n, r, d_in, d_out, M if has_dx else -1, dx if has_dx else None,
                                             device):
         pda, pdb = out.addresses[:2]

@@ -234,3 +234,15 @@ def test_nothing_stands_where_the_last_adapters_have_no_tokens(M, n):
     for k in ("dA", "dB"):
         assert torch.equal(out[k][:1], one[k]), k
     assert torch.equal(out["dX"], one["dX"])
+
+
+def test_a_wanted_dx_needs_a_place():
+    import torch
+    from post_weight_quantization_08_amd import pipeline as P
+    X, g = torch.zeros(4, 64, device="cuda").bfloat16(), torch.zeros(4, 32, device="cuda").bfloat16()
+    A, B = torch.zeros(1, 8, 64, device="cuda").bfloat16(), torch.zeros(1, 32, 8, device="cuda").bfloat16()
+    out, ws = P.lora_grad_buffers(X, g, A, B)
+    ad = torch.zeros(4, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="want_dx"):
+        P.lora_grad(X, g, A, B, ad, want_dx=True, out=out, ws=ws)
+    assert "dX" not in P.lora_grad(X, g, A, B, ad, out=out, ws=ws)
