@@ -4,8 +4,7 @@
 // Bound by memory: every element is read once, kept in registers between the
 // maximum and the rounding, and leaves as one byte (two with the transpose).
 // 8192 x 11008 bf16 in rows 52 us (5.2 TB/s; a large copy runs at 5.0); 28672 x 8192
-// in tiles with the transpose 249 us (3.8 TB/s: of a wave's time four fifths are waits
-// for loads and for the exchange in LDS).
+// in tiles with the transpose 188 us (5.0 TB/s).
 #include "fp8.h"
 
 namespace gq {
@@ -57,13 +56,21 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(F8Args a) {
 // One workgroup per 128 x 128 tile: a thread holds eight rows of eight columns.
 // The transpose goes through LDS, 16 bytes behind every 128 so that the columns
 // of a store fall into different banks.
+// Tiles are taken in bands of eight row tiles, so that what runs at one time reads and
+// writes several lines next to each other of every row, of the transpose's too: 28672 x
+// 8192 bf16 in one column of tiles after another 241 us, in bands of 8, 16, 32, 64 rows of
+// tiles 189, 195, 197, 213; 131072 x 4096 528, and 422, 428, 451, 478.
+constexpr int kF8Band = 8;
+
 template <int kDt>
 __global__ __launch_bounds__(256) void fp8_tiles_kernel(F8Args a) {
   constexpr int kPitch = kF8Block + 8;
   __shared__ uint32_t tops[4];
   __shared__ __align__(16) uint8_t turned[kF8Block * kPitch];
   const int t = threadIdx.x, group = t >> 4, k = (t & 15) * 8;
-  const int row_tile = blockIdx.x % a.row_tiles, col_tile = blockIdx.x / a.row_tiles;
+  const int band = blockIdx.x / (kF8Band * a.blocks), first = band * kF8Band, in = blockIdx.x - first * a.blocks;
+  const int height = min(kF8Band, a.row_tiles - first);
+  const int row_tile = first + in % height, col_tile = in / height;
   const int64_t r0 = (int64_t)row_tile * kF8Block + group * 8;
   const int c0 = col_tile * kF8Block;
   float v[8][8];
