@@ -142,7 +142,8 @@ __device__ inline void grad_sort(const GradArgs& a, GradSortShared& sh) {
 // while the one before is multiplied.  Of a block lane (c16, q) has elements 64 u + 16 q +
 // 8 h + 0..7 of its row in step j = 2 u + h, so that codes come 16 bytes at a time.
 // D: rows = ranks, columns = tokens.  (8192 tokens, 64 ranks: every wave loading the
-// factors for itself 91 us, through LDS 76, and without a condition between loads 64.)
+// factors for itself 91 us, through LDS 76, and without a condition between loads 64; the parts
+// taking the blocks in turn the same.)
 //   kRows false: F is [rank][K]; D's row i of tile p is rank 16 p + i.
 //   kRows true: F is [K][rank]; a lane loads kR ranks of eight rows and turns them;
 //   row i of tile p is rank kR i + p.
@@ -318,35 +319,41 @@ __device__ __forceinline__ void grad_project(const GradArgs& a, const GradSide& 
     const int bw = min(b1, s.K / kF8Block);   // behind the whole blocks
     constexpr std::true_type kWhole{};
     constexpr bool kAhead = kD != GPTQ_F32;
+    constexpr int kDeep = 2;   // blocks of rows in registers (three of codes: 67 us for 65)
     // take: whether this wave has tokens of the adapter
     auto sum = [&](auto take, auto even) {
       Factor w;
-      Block k0, k1;
-      auto step = [&](int b, int buffer, const Block& now, Block& then) {
-        read_factor(b, w, even, kWhole);
-        if constexpr (take && kAhead) read(b, then, kWhole);
-        if constexpr (take) multiply(buffer, now);
-        write_factor(buffer ^ 1, w);
-        if constexpr (take && !kAhead) read(b, then, kWhole);
-        __syncthreads();
-      };
+      Block k[kDeep];
       if (b0 < bw) {
         read_factor(b0, w, even, kWhole);
-        if constexpr (take) read(b0, k0, kWhole);
+        if constexpr (take) {
+#pragma unroll
+          for (int i = 0; i + 1 < kDeep; ++i) read(min(b0 + i, bw - 1), k[i], kWhole);
+        }
         write_factor(0, w);
         __syncthreads();
-        for (int b = b0; b < bw; b += 2) {
-          step(min(b + 1, bw - 1), 0, k0, k1);
-          if (b + 1 >= bw) break;
-          step(min(b + 2, bw - 1), 1, k1, k0);
+        for (int b = b0; b < bw;) {
+#pragma unroll
+          for (int i = 0; i < kDeep; ++i) {
+            constexpr int kLast = kDeep - 1;
+            Block& then = k[(i + kLast) % kDeep];
+            const int ahead = min(b + kLast, bw - 1);
+            read_factor(min(b + 1, bw - 1), w, even, kWhole);
+            if constexpr (take && kAhead) read(ahead, then, kWhole);
+            if constexpr (take) multiply(i, k[i]);
+            write_factor((i + 1) % kDeep, w);
+            if constexpr (take && !kAhead) read(ahead, then, kWhole);
+            __syncthreads();
+            if (++b >= bw) break;
+          }
         }
       }
       if (bw < b1) {   // nobody multiplies from the first buffer any more
         read_factor(bw, w, even, std::false_type{});
         write_factor(0, w);
-        if constexpr (take) read(bw, k0, std::false_type{});
+        if constexpr (take) read(bw, k[0], std::false_type{});
         __syncthreads();
-        if constexpr (take) multiply(0, k0);
+        if constexpr (take) multiply(0, k[0]);
         __syncthreads();
       }
     };
