@@ -12,8 +12,8 @@
 // e4m3 with its scale one (exact); of their products those are taken whose size is
 // 2^-16 of the largest or more.
 //
-// 8192 tokens, 11008 -> 4096, 64 ranks, codes and bf16, with dX: 233 us, of them project
-// 64 (2.5 TB/s), terms 14, outer 67, join 6, dX 97 (3.7 TB/s).  2048 tokens of eight
+// 8192 tokens, 11008 -> 4096, 64 ranks, codes and bf16, with dX: 235 us, of them project
+// 65 (2.4 TB/s), terms 14, outer 67, join 6, dX 97 (3.7 TB/s).  2048 tokens of eight
 // adapters of 16 ranks, 4096 -> 14336, fp16: 91 us (29, 8, 30, 5, 15).  96 tokens, 8 ranks:
 // 17 us in three launches, each a chain of a few loads.
 //
