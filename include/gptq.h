@@ -488,8 +488,12 @@ gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, int64_t n_row
  *   workspace   GPTQ_OP_POLICY bytes, 256-byte aligned; may be NULL when that size is
  *               0; calls sharing one workspace must be stream-ordered.
  * Masked logits may be -inf or the type's lowest value.  A masked target (l = -inf)
- * has ratio 0, with a reference kl +inf, and gradient 0.  A scored row that holds a
- * NaN or +inf, or nothing above -inf, has NaN for every output (weight 0: gradient 0).
+ * has ratio 0, with a reference kl +inf, and gradient 0, also if old or ref is infinite.
+ * A scored row that holds a NaN or +inf, or nothing above -inf, has NaN for every output
+ * (weight 0: gradient 0).  A NaN in old, advantage or, with kl_coef > 0, ref gives a NaN
+ * loss and a row of NaN for its gradient (weight 0: 0); ratio and kl are NaN where they
+ * are made of it.  Infinite ones go by the formulas, with 0 for advantage 0 times an
+ * infinite ratio; where dloss/dl is infinite the gradient is infinite or NaN.
  * fp32 sums, the row's own numbers in 64 bits; no floating-point atomics. */
 gptq_status gptq_policy_loss(const void* logits, int32_t x_dtype, int64_t n_rows, int64_t vocab, int64_t ld_x,
                              const int32_t* targets, const float* old_logprob, const float* advantage,

@@ -39,18 +39,19 @@ def policy_loss(logits, targets, old, advantage, ref=None, clip_low=0.2, clip_hi
         lp = -np.log1p(others) if z[t] == m else (z[t] - m) - np.log(total)   # a sure token's is not rounded away
         a = float(advantage[i])
         with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
-            r = np.exp(lp - float(old[i]))
+            gone, o = lp == -np.inf, float(old[i])            # a masked token: ratio 0, whatever the behaviour's was
+            r = 0.0 if gone and o == o else np.exp(lp - o)
             free, held = r * a, min(max(r, 1.0 - clip_low), 1.0 + clip_high) * a
-            loss, c = (-free, -r * a) if free <= held else (-held, 0.0)
+            loss, c = (-held, 0.0) if free > held else (-free, -free)
             kl = 0.0
             if ref is not None:
-                d = float(ref[i]) - lp
+                d = np.inf if gone and ref[i] == ref[i] else float(ref[i]) - lp
                 kl = np.inf if d == np.inf else np.expm1(d) - d
                 if kl_coef > 0:
                     loss = loss + kl_coef * kl
                     c = c - kl_coef * np.expm1(d)
         out["loss"][i], out["logprob"][i], out["ratio"][i], out["kl"][i] = loss, lp, r, kl
-        if lp == -np.inf:                      # a masked token has no gradient
+        if gone and c == c:                    # nor has it a gradient; a NaN stays
             c = 0.0
         g = -e / total
         g[t] = others / total

@@ -112,25 +112,29 @@ __device__ __forceinline__ PlFinal pl_final(const PlArgs& a, int64_t row, const 
       loss = lp = ratio = kl = NAN;
     } else {
       lp = xt == m ? -(double)log1pf(mass) : ((double)xt - m) * a.inv_td - ln_wide(total);
-      const double adv = a.adv[row];
-      ratio = pl_exp(lp - (double)a.old[row]);
-      const double open = ratio * adv, held = fmin(fmax(ratio, a.low), a.high) * adv;
-      loss = open <= held ? -open : -held;
-      coef = open <= held ? -open : 0.0;
+      const double adv = a.adv[row], old = a.old[row];
+      // a masked token has ratio 0 and no gradient, whatever the others' finite or infinite
+      // numbers are; comparisons let a NaN through
+      const bool gone = lp == -INFINITY;
+      ratio = gone && old == old ? 0.0 : pl_exp(lp - old);
+      const double open = adv == 0.0 && ratio == INFINITY ? 0.0 : ratio * adv;   // 0 times what fp32 cannot hold
+      const double held = (ratio < a.low ? a.low : ratio > a.high ? a.high : ratio) * adv;
+      loss = open > held ? -held : -open;
+      coef = open > held ? 0.0 : -open;
       if (a.ref) {
-        const double d = (double)a.ref[row] - lp, up1 = expm1f((float)d);
+        const double ref = a.ref[row], d = gone && ref == ref ? INFINITY : ref - lp, up1 = expm1f((float)d);
         kl = pl_kl(d, up1);
         if (a.beta > 0.f) {                // 0 times an infinite kl is nothing
           loss += a.beta * kl;
           coef -= a.beta * up1;
         }
       }
-      if (lp == -INFINITY) coef = 0.0;   // a masked token has no gradient
+      if (gone && coef == coef) coef = 0.0;
     }
     const float w = p.weight * a.inv_t;
     f.zero = w == 0.f;
-    f.nan = bad && !f.zero;
     const float cf = f.zero ? 0.f : (float)(coef * w), inv_s = 1.f / total;
+    f.nan = !f.zero && (bad || cf != cf);
     f.rest = s > 0.f ? -cf * (up * inv_s) : 0.f;
     f.at = cf * (mass * inv_s);
   }
