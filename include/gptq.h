@@ -481,10 +481,10 @@ gptq_status gptq_distill_topk(const void* logits, int32_t x_dtype, int64_t n_row
  *               0, whatever it holds.
  *   loss        device fp32 [n_rows], not multiplied by weight.  logprob, ratio, kl:
  *               device fp32 [n_rows]; any of them may be NULL.
- *   grad        device, n_rows x vocab of x_dtype, row stride ld_g, each element
- *               rounded once to x_dtype (nearest even); NULL = no gradient.  It may be
- *               the logits' own buffer (grad == logits with ld_g == ld_x); otherwise it
- *               must not overlap them.
+ *   grad        device, n_rows x vocab of x_dtype, row stride ld_g, each element a
+ *               product in fp32 and rounded to x_dtype (nearest even); NULL = no
+ *               gradient.  It may be the logits' own buffer (grad == logits with
+ *               ld_g == ld_x); otherwise it must not overlap them.
  *   workspace   GPTQ_OP_POLICY bytes, 256-byte aligned; may be NULL when that size is
  *               0; calls sharing one workspace must be stream-ordered.
  * Masked logits may be -inf or the type's lowest value.  A masked target (l = -inf)

@@ -7,16 +7,15 @@
 //   l = (x_t - m) / T - ln S, or -log1p(s 2^((r - x_t) c)) where x_t is the maximum,
 //   dl/dx_t = s 2^((r - m) c) / (S T),   dl/dx_j = -2^((x_j - m) c) / (S T),
 // so neither l near 0 nor 1 - q_t is a difference of nearly equal numbers.  The row's
-// few other numbers (ratio, clipping, KL) are made by one wave; l and differences with it
-// are 64-bit numbers, the functions of them 32-bit ones (64-bit functions take so many
-// registers that the held blocks were spilled).
+// few other numbers (l, ratio, clipping, KL) are made by one wave in 64 bits, by functions
+// of their own that leave the held blocks in their registers.
 //
 // The row kernel holds a row in registers (16-byte blocks as loaded), so a logit is
 // read once and its gradient written once; the registers are refilled with the
 // next row's as soon as a block's gradient is stored.  Few rows are split over
 // workgroups, and rows too long for the registers of one, in two launches.
 //
-// 4096 x 131072 bf16 425 us (5.05 TB/s read and written, as a large copy); 777 x 50021
+// 4096 x 131072 bf16 428 us (5.02 TB/s read and written, as a large copy); 777 x 50021
 // fp16 51 us (512 workgroups have a row each, half of them a second); 8 x 32000 fp32 11 us,
 // two launches of 3.5 and 4.6.
 #include "rows.h"
@@ -78,22 +77,63 @@ struct PlFinal {
   int zero, nan;
 };
 
-// e^d of a 64-bit d, and e^d - 1, to 32 bits.
-__device__ __forceinline__ double pl_exp(double d) {
-  const float h = (float)d;
-  return (double)expf(h) * (fabsf(h) < INFINITY ? 1.0 + (d - (double)h) : 1.0);
+// A constant made where it is used: kept in registers from row to row, those of the functions
+// below spill held blocks.
+template <uint64_t kBits>
+__device__ __forceinline__ double pl_const() {
+  uint32_t lo, hi;
+  asm volatile("v_mov_b32 %0, %2\n\tv_mov_b32 %1, %3" : "=&v"(lo), "=v"(hi) : "n"((int)(uint32_t)kBits), "n"((int)(uint32_t)(kBits >> 32)));
+  return __hiloint2double((int)hi, (int)lo);
 }
-// e^d - 1 - d: the series where the difference would lose digits (|d| < 1/2: the
-// term behind the last is below 2^-12 d^11 / 11! / 2 of it).
-__device__ __forceinline__ double pl_kl(double d, double up1) {
-  if (fabs(d) >= 0.5) return d == INFINITY ? d : up1 - d;
-  float t = 1.f / 39916800.f;
-  const float h = (float)d;
-  constexpr float kInv[9] = {1.f / 3628800.f, 1.f / 362880.f, 1.f / 40320.f, 1.f / 5040.f, 1.f / 720.f,
-                             1.f / 120.f,     1.f / 24.f,     1.f / 6.f,     1.f / 2.f};
+#define PL_CONST(x) pl_const<__builtin_bit_cast(uint64_t, (double)(x))>()
+
+// e^d, e^d - 1 and e^d - 1 - d of a 64-bit d.  d = n ln 2 + f with |f| <= ln 2 / 2; at x =
+// f / 8 the series of e^x - 1 - x, whose first term left out, x^9 / 9!, is 2^-49 of it; then
+// three times from x to 2 x by e^(2 x) - 1 - 2 x = p^2 + 2 (p - x) with p = e^x - 1, in which
+// nothing cancels.  A NaN stays one.
+struct PlExp {
+  double p, over, e;          // e^f - 1, e^f - 1 - f, e^d
+  bool near;                  // n = 0: d = f
+  __device__ __forceinline__ explicit PlExp(double d) {
+    // beyond, e^d is 0 or infinite in 64 bits
+    d = d > 720.0 ? 720.0 : d < -760.0 ? -760.0 : d;
+    const double n = rint(d * PL_CONST(1.4426950408889634));
+    // ln 2 in two parts, the first of 24 bits, so that n times it is exact
+    double x = 0.125 * fma(n, PL_CONST(1.904654299957768e-09), fma(-n, PL_CONST(0.6931471824645996), d));
+    double q = fma(PL_CONST(1.0 / 40320), x, PL_CONST(1.0 / 5040));
+    q = fma(q, x, PL_CONST(1.0 / 720));
+    q = fma(q, x, PL_CONST(1.0 / 120));
+    q = fma(q, x, PL_CONST(1.0 / 24));
+    q = fma(q, x, PL_CONST(1.0 / 6));
+    q = fma(q, x, 0.5);
+    over = x * x * q;
+    p = x + over;
 #pragma unroll
-  for (int i = 0; i < 9; ++i) t = fmaf(t, h, kInv[i]);
-  return d * d * (double)t;
+    for (int i = 0; i < 3; ++i) {
+      over = fma(p, p, 2.0 * over);
+      x *= 2.0;
+      p = x + over;
+    }
+    e = ldexp(1.0 + p, (int)n);
+    near = n == 0.0;
+  }
+  __device__ __forceinline__ double less_one() const { return near ? p : e - 1.0; }
+  __device__ __forceinline__ double less_line(double d) const {   // e^d - 1 - d
+    return near ? over : d == INFINITY ? d : less_one() - d;
+  }
+};
+
+// ln x and ln(1 + x) of fp32 numbers, x > 0 and x >= 0: the 32-bit function and one step of
+// Newton's, which leaves the square of its error.
+__device__ __forceinline__ double pl_ln(float x) {
+  int e;
+  const float m = frexpf(x, &e), y = logf(m);
+  return fma((double)e, PL_CONST(0.69314718055994530942), (double)y + fma((double)m, PlExp(-(double)y).e, -1.0));
+}
+__device__ __forceinline__ double pl_ln1p(float x) {
+  const float y = log1pf(x);
+  const float left = (float)((double)x - PlExp(y).less_one());
+  return (double)y + (double)(left / (1.f + x));
 }
 
 // The row's outputs and what its gradient is made of, from the rest's sum and the
@@ -111,22 +151,25 @@ __device__ __forceinline__ PlFinal pl_final(const PlArgs& a, int64_t row, const 
     if (bad) {
       loss = lp = ratio = kl = NAN;
     } else {
-      lp = xt == m ? -(double)log1pf(mass) : ((double)xt - m) * a.inv_td - ln_wide(total);
+      lp = xt == m ? -pl_ln1p(mass) : ((double)xt - m) * a.inv_td - pl_ln(total);
       const double adv = a.adv[row], old = a.old[row];
       // a masked token has ratio 0 and no gradient, whatever the others' finite or infinite
       // numbers are; comparisons let a NaN through
       const bool gone = lp == -INFINITY;
-      ratio = gone && old == old ? 0.0 : pl_exp(lp - old);
-      const double open = adv == 0.0 && ratio == INFINITY ? 0.0 : ratio * adv;   // 0 times what fp32 cannot hold
+      ratio = gone && old == old ? 0.0 : PlExp(lp - old).e;
+      const double open = adv == 0.0 && ratio == INFINITY ? 0.0 : ratio * adv;
       const double held = (ratio < a.low ? a.low : ratio > a.high ? a.high : ratio) * adv;
       loss = open > held ? -held : -open;
       coef = open > held ? 0.0 : -open;
       if (a.ref) {
-        const double ref = a.ref[row], d = gone && ref == ref ? INFINITY : ref - lp, up1 = expm1f((float)d);
-        kl = pl_kl(d, up1);
-        if (a.beta > 0.f) {                // 0 times an infinite kl is nothing
-          loss += a.beta * kl;
-          coef -= a.beta * up1;
+        const double ref = a.ref[row], d = gone && ref == ref ? INFINITY : ref - lp;
+        const PlExp up(d);
+        kl = up.less_line(d);
+        float beta = a.beta;
+        asm volatile("" : "+v"(beta));     // nor its 64 bits
+        if (beta > 0.f) {                  // 0 times an infinite kl is nothing
+          loss += beta * kl;
+          coef -= beta * up.less_one();
         }
       }
       if (gone && coef == coef) coef = 0.0;
