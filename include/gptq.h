@@ -562,7 +562,7 @@ gptq_status gptq_w4a16_lora_matmul(const void* X, int32_t x_dtype, int64_t M, in
  *             codes cols x ld_ct (rows rounded up to whole blocks, written as 0 behind
  *             rows), scales [blocks][ceil(rows / 128)].  A tile has one scale both
  *             ways, so these are the same numbers.
- * rows * blocks < 2^30 (else GPTQ_EUNSUPPORTED).  rows = 0 does nothing. */
+ * rows * blocks <= 2^30 - 64 (more: GPTQ_EUNSUPPORTED).  rows = 0 does nothing. */
 gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
                               int32_t block_rows, uint8_t* codes, int64_t ld_c, uint8_t* scales, uint8_t* codes_t,
                               int64_t ld_ct, uint8_t* scales_t, void* stream);
@@ -587,8 +587,8 @@ gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t rows, int6
  * 3e-5 of a result, half a step of fp16 5e-4).  Scale bytes are those that
  * gptq_fp8_quantize writes, and no |x| or |w| above 2^127.  A token's outputs are NaN where its codes or
  * a row of weights hold a NaN; others do not see it.  Results are bitwise reproducible
- * for given sizes.  M, d_in, d_out <= 2^22 (more: GPTQ_EUNSUPPORTED).  M = 0 does
- * nothing.  The input's gradient is the same call on the output's gradient with
+ * for given sizes.  M, d_in, d_out <= 2^22, and of values M * blocks <= 2^30 - 64 (more:
+ * GPTQ_EUNSUPPORTED).  M = 0 does nothing.  The input's gradient is the same call on the output's gradient with
  * the transpose of the weights. */
 gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_scales, int64_t M, int64_t d_in,
                             int64_t ld_x, const uint8_t* W, int64_t ld_w, const uint8_t* w_scales, int64_t d_out,

@@ -64,7 +64,10 @@ __device__ __forceinline__ uint32_t f8_top8(const float (&v)[8]) {
 
 inline size_t f8_elem(int dtype) { return dtype == GPTQ_F32 ? 4 : dtype == GPTQ_E4M3 ? 1 : 2; }
 
-// Rows into codes of `cols` padded to whole blocks and scales [rows][blocks];
+// A launch has fewer than 2^32 threads, the quantizing one 256 for every 64 blocks.
+constexpr int64_t kF8MostBlocks = ((int64_t)1 << 30) - 64;
+
+// Rows, of kF8MostBlocks blocks at most, into codes of `cols` padded to whole blocks and scales [rows][blocks];
 // in fp8_quantize.hip.
 void f8_quantize_rows(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* codes,
                       int64_t ld_c, uint8_t* scales, hipStream_t st);

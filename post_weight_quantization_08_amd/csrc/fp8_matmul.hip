@@ -650,6 +650,7 @@ extern "C" gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uin
   GQ_CHECK_ARG(ld_w >= cdiv(d_in, kF8Block) * kF8Block && ld_w % 16 == 0 && ld_w <= ((int64_t)1 << 36));
   GQ_CHECK_ARG(ld_y >= d_out && ld_y <= ((int64_t)1 << 36));
   if (M > ((int64_t)1 << 22) || d_in > ((int64_t)1 << 22) || d_out > ((int64_t)1 << 22)) return GPTQ_EUNSUPPORTED;
+  if (!codes && M * cdiv(d_in, kF8Block) > kF8MostBlocks) return GPTQ_EUNSUPPORTED;
   if (M == 0) return GPTQ_OK;
   GQ_CHECK_ARG(X && W && w_scales && Y && (x_scales || !codes));
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(X) % (codes ? 16 : f8_elem(x_dtype)) == 0);

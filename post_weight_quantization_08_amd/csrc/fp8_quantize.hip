@@ -171,7 +171,7 @@ extern "C" gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t
   const bool turn = codes_t != nullptr || scales_t != nullptr;
   GQ_CHECK_ARG(!turn || (block_rows == kF8Block && codes_t && scales_t && ld_ct >= row_tiles * kF8Block &&
                          ld_ct % 16 == 0 && ld_ct <= ((int64_t)1 << 36)));
-  if (rows * blocks >= ((int64_t)1 << 30)) return GPTQ_EUNSUPPORTED;
+  if (rows * blocks > kF8MostBlocks) return GPTQ_EUNSUPPORTED;
   if (rows == 0) return GPTQ_OK;
   GQ_CHECK_ARG(X && codes && scales && reinterpret_cast<uintptr_t>(X) % f8_elem(x_dtype) == 0);
   GQ_CHECK_ARG(reinterpret_cast<uintptr_t>(codes) % 16 == 0 && reinterpret_cast<uintptr_t>(codes_t) % 16 == 0);
