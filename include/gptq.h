@@ -581,14 +581,17 @@ gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t rows, int6
  *             ld_y; must not overlap the inputs or the workspace.
  *   workspace GPTQ_OP_FP8_MATMUL bytes, 256-byte aligned; may be NULL when that size
  *             is 0; calls sharing one workspace must be stream-ordered.
- * Y in fp32: products exact, fp32 accumulation.  Y in 16 bits: the matrix unit's 8-bit
- * products, which are added up eight at a time with every product cut off below 2^-13
- * of the largest of the eight, then in fp32; Y is rounded once (the cutting is about
- * 3e-5 of a result, half a step of fp16 5e-4).  Scale bytes are those that
- * gptq_fp8_quantize writes, and no |x| or |w| above 2^127.  A token's outputs are NaN where its codes or
- * a row of weights hold a NaN; others do not see it.  Results are bitwise reproducible
- * for given sizes.  M, d_in, d_out <= 2^22, and of values M * blocks <= 2^30 - 64 (more:
- * GPTQ_EUNSUPPORTED).  M = 0 does nothing.  The input's gradient is the same call on the output's gradient with
+ * Y in fp32, or of up to 128 tokens: products exact, fp32 accumulation.  Y in 16 bits of
+ * more tokens: the matrix unit's 8-bit products, which are added up eight at a time with
+ * every product cut off below 2^-13 of the largest of the eight, then in fp32.  Before Y's
+ * own rounding an output is then off by at most 7 * 2^-13 of the sum, over the eights, of
+ * their largest products: 3e-5 of a result for random operands (half a step of fp16 is
+ * 5e-4), but no share of a result whose terms cancel; Y in fp32 is the call for those.
+ * Scale bytes are those that gptq_fp8_quantize writes, and no |x| or |w| above 2^127.
+ * A token's outputs are NaN where its codes or a row of weights hold a NaN; others do not
+ * see it.  Results are bitwise reproducible for given sizes.  M, d_in, d_out <= 2^22, and
+ * of values M * blocks <= 2^30 - 64 (more: GPTQ_EUNSUPPORTED).  M = 0 does nothing.
+ * The input's gradient is the same call on the output's gradient with
  * the transpose of the weights. */
 gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_scales, int64_t M, int64_t d_in,
                             int64_t ld_x, const uint8_t* W, int64_t ld_w, const uint8_t* w_scales, int64_t d_out,

@@ -1,20 +1,24 @@
 // Product of 8-bit operands with a power-of-two scale for each block of 128:
 //   Y[m][n] = sum_b 2^(sx[m][b] - 127) 2^(sw[n / 128][b] - 127) sum_{k in b} x[m][k] w[n][k].
 //
-// 16-bit outputs: one instruction, 16x16x128 on e4m3 with a scale byte per lane and
-// operand, does a block of 16 x 16 outputs: the scales cost nothing and the sums
-// stay in its fp32 accumulators from the first block to the last.  It adds the
-// products of eight consecutive codes after cutting each off at 2^-13 of the largest
-// one's exponent (measured with single products; sums across eights keep 24 bits), an
-// error of about 3e-5 of a result, far below half a step of a 16-bit output.
-// fp32 outputs promise more than that: their codes become bf16 together with the
-// scales, exactly, and go through 16x16x32 bf16 products at half the rate.
+// Two ways to multiply a block.  The codes become bf16 together with the scales, exactly,
+// and go through 16x16x32 bf16 products.  Or one instruction, 16x16x128 (32x32x64 in large
+// tiles) on e4m3 with a scale byte per lane and operand, does the block: no conversions and
+// twice the rate, but it adds the products of eight consecutive codes after cutting each off
+// at 2^-13 of the largest one's exponent (measured with single products; sums across eights
+// keep 24 bits).  That is up to 7 * 2^-13 of the largest product of each eight: 3e-5 of a
+// result for random operands, a tenth of half a step of fp16, but where terms cancel (1, -1
+// and six of 2^-14) they are lost.  So the second way is taken for 16-bit outputs alone, and
+// there only for more than 128 tokens, which products bound; fewer wait for the weights.  The
+// two ways, bf16 outputs, us: 1 x 4096 -> 4096 8.1 and 8.0, 16 x 11008 -> 4096
+// 21.2 and 21.5, 48 x 8192 -> 28672 72 and 72, 128 x 4096 -> 14336 34.3 and 34.2; 300 x
+// 4096 -> 14336 61.0 and 58.6, 1024 x 4096 -> 4096 44.8 and 40.8, 2048 x 4096 -> 4096 72 and 65.
 //
-// 8192 x 8192 -> 28672 in codes 1.66 ms, 2.3 PFLOP/s (a large product of the library
+// 8192 x 8192 -> 28672 in codes 1.68 ms, 2.3 PFLOP/s (a large product of the library
 // 3.25): direct loads of a block take as long as its products, and with two buffers
-// of 64 KB little of either is hidden behind the other's end.  48 x 8192 -> 28672 60 us,
-// 4.0 TB/s of weights; one token 4096 -> 4096 8 us, one launch; fp32 outputs 777 x 11000
-// -> 4001 99 us: 9 to quantize the tokens, the rest to turn codes into bf16 and multiply.
+// of 64 KB little of either is hidden behind the other's end.  48 x 8192 -> 28672 62 us,
+// 3.8 TB/s of weights; one token 4096 -> 4096 8 us, one launch; fp32 outputs 777 x 11000
+// -> 4001 98 us: 9 to quantize the tokens, the rest to turn codes into bf16 and multiply.
 //
 // A lane holds 32 codes of one row; which 32 of the block's 128 does not matter as
 // long as both operands agree (here units q and q + 4 of 16 bytes, q = lane / 16).
@@ -173,12 +177,8 @@ __global__ __launch_bounds__(64 * kF8FewWaves) void fp8_few_kernel(F8MmArgs a) {
       for (int i = 0; i < 8; ++i)
         s.x[i / 4][0][i % 4] = f8_codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], s.sx[0]);
     }
-    if constexpr (kY == GPTQ_F32) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) f8_wide_unit<1, 1>(s.w[u], s.x[u], s.sw, s.sx, acc);
-    } else {
-      acc[0][0] = f8_mfma(f8_frag(s.w[0][0], s.w[1][0]), f8_frag(s.x[0][0], s.x[1][0]), acc[0][0], s.sw[0], s.sx[0]);
-    }
+    for (int u = 0; u < 2; ++u) f8_wide_unit<1, 1>(s.w[u], s.x[u], s.sw, s.sx, acc);
   };
   int b = wave;
   for (; b + (kU - 1) * kF8FewWaves < a.nb; b += kU * kF8FewWaves) {
@@ -225,7 +225,7 @@ __device__ __forceinline__ void f8_place(const F8MmArgs& a, int id, int& tm, int
 // 128 of every row, straight from memory into LDS.  Unit u (16 bytes) of row r lies at
 // slot u ^ (r / 2 % 8): the sixteen rows of a fragment's unit then cover all banks
 // once.
-template <int kY, int kBM, int kBN, int kWM, int kWN>
+template <int kY, bool kExact, int kBM, int kBN, int kWM, int kWN>
 __global__ __launch_bounds__(64 * kWM * kWN, 2) void fp8_tile_kernel(F8MmArgs a) {
   constexpr int kWaves = kWM * kWN;
   constexpr int kRows = kBM + kBN;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void fp8_tile_kernel(F8MmArgs a)
   const int slot0 = (q ^ ((c16 >> 1) & 7)) * 16, slot1 = slot0 ^ 64;   // unit q + 4 = q ^ 4
   const int at_x = (wm * (kT * 16) + c16) * kF8Block, at_w = (kBM + wn * (kR * 16) + c16) * kF8Block;
   auto multiply = [&](const char* from, const uint32_t (&ux)[kT], const uint32_t (&uw)[kWide]) {
-    if constexpr (kY == GPTQ_F32) {
+    if constexpr (kExact) {
       uint32_t us[kR];
 #pragma unroll
       for (int r = 0; r < kR; ++r) us[r] = uw[r * 16 / kF8Block];
@@ -568,6 +568,8 @@ constexpr int64_t kF8FewRows = 8192;
 // every CU has a workgroup, into parts of four blocks or more: 65 x 4096 -> 4096 in 1, 4
 // and 8 parts 26, 16 and 20; 128 x 8192 -> 28672 in 1 and 2 parts 62 and 87.
 constexpr int64_t kF8Wide = 512;
+// Tokens whose 16-bit outputs are of exact products, too.
+constexpr int64_t kF8Exact = 128;
 
 struct F8Plan {
   bool few;
@@ -626,10 +628,14 @@ static void f8_run(F8MmArgs& a, int x_dtype, const F8Plan& p, hipStream_t st) {
       return;
     }
   }
-  if (p.bm == 256) hipLaunchKernelGGL((fp8_tile_kernel<kY, 256, 256, 4, 2>), grid, dim3(512), 0, st, a);
-  else if (p.bm == 128) hipLaunchKernelGGL((fp8_tile_kernel<kY, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
-  else if (p.bm == 64) hipLaunchKernelGGL((fp8_tile_kernel<kY, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((fp8_tile_kernel<kY, 32, 128, 1, 4>), grid, dim3(256), 0, st, a);
+  constexpr bool kWide = kY == GPTQ_F32;
+  const bool exact = kWide || a.M <= kF8Exact;
+  if (p.bm == 256) hipLaunchKernelGGL((fp8_tile_kernel<kY, kWide, 256, 256, 4, 2>), grid, dim3(512), 0, st, a);
+  else if (p.bm == 128 && exact) hipLaunchKernelGGL((fp8_tile_kernel<kY, true, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else if (p.bm == 128) hipLaunchKernelGGL((fp8_tile_kernel<kY, kWide, 128, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else if (p.bm == 64 && exact) hipLaunchKernelGGL((fp8_tile_kernel<kY, true, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else if (p.bm == 64) hipLaunchKernelGGL((fp8_tile_kernel<kY, kWide, 64, 128, 2, 2>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((fp8_tile_kernel<kY, true, 32, 128, 1, 4>), grid, dim3(256), 0, st, a);
   if (a.splits > 1)
     hipLaunchKernelGGL((fp8_join_kernel<kY>), dim3((unsigned)cdiv(a.d_out, 1024), (unsigned)a.M), dim3(256), 0, st, a);
 }
