@@ -552,14 +552,17 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(F8MmArgs a) {
   f8_store4<kY>(a.Y, m * a.ld_y + n, left, v);
 }
 
-// Up to 16 tokens on up to 8192 rows take one launch, whose every workgroup quantizes all
-// tokens; more rows make that the larger part.  bf16 in one launch, or quantized apart
-// and in tiles of 32 tokens, us:
-//   4096 -> 4096     1 to 8 tokens 8 and 13,   16 tokens 9 and 14,   32 (by the codes) 18 and 14
-//   11008 -> 4096    2 tokens 13 and 20,       16 tokens 20 and 21,  32 37 and 22
-//   8192 -> 28672    2 tokens 57 and 44,       16 tokens 102 and 45, 48 70 and 50
+// Up to 16 tokens take one launch, whose every workgroup quantizes all tokens, where a CU
+// has one workgroup (4096 rows of weights), or two with few values to quantize.  bf16 in
+// one launch, or quantized apart and in tiles of 32 tokens, us:
+//   4096 -> 4096     1 token 8 and 14,    16 tokens 9 and 15,    32 (by the codes) 18 and 14
+//   28672 -> 4096    1 token 32 and 38,   16 tokens 42 and 41
+//   4096 -> 8192     1 token 13 and 17,   16 tokens 17 and 19
+//   8192 -> 8192     1 token 22 and 24,   8 tokens 24 and 26,    12 tokens 30 and 26
+//   28672 -> 8192    1 token 63 and 62,   8 tokens 69 and 65,    16 tokens 82 and 66
+//   4096 -> 11008    1 token 18 and 18,   8 tokens 21 and 20,    16 tokens 24 and 21
 constexpr int kF8Few = 16;
-constexpr int64_t kF8FewRows = 8192;
+constexpr int64_t kF8FewRows = 4096, kF8FewValues = 1 << 16;
 // Tiles of 256 by 256 if every CU gets one and they are more than half full: 4096 ->
 // 131072, bf16 (and fp32) in tiles of 256 and in the smaller ones, us: 16 tokens 153 (221)
 // and 126 (129), 100 tokens 183 (231) and 146 (165), 200 tokens 185 (247) and 221 (284).
@@ -580,7 +583,7 @@ struct F8Plan {
 static F8Plan f8_plan(int64_t M, int64_t d_in, int64_t d_out, bool codes) {
   F8Plan p{};
   const int64_t nb = cdiv(d_in, kF8Block);
-  p.few = M <= kF8Few && d_out <= kF8FewRows;
+  p.few = M <= kF8Few && (d_out <= kF8FewRows || (d_out <= 2 * kF8FewRows && M * d_in <= kF8FewValues));
   if (!codes && !p.few) {
     p.off_scales = align_up((size_t)M * nb * kF8Block, 256);
     p.total = align_up(p.off_scales + (size_t)M * nb, 256);
