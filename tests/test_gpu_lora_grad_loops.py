@@ -24,6 +24,8 @@ def mix(M, n, kind, gen):
     import torch
     if kind == "one":
         return torch.zeros(M, dtype=torch.int32, device="cuda")
+    if kind == "turns":                                   # a wave's 32 tokens have one adapter, a workgroup's several
+        return ((torch.arange(M, device="cuda") + 16) // 32 % (n + 1) - 1).int()
     if kind == "any":
         return torch.randint(-1, n + 1, (M,), generator=gen, device="cuda").int()
     cut = torch.sort(torch.randint(0, M, (2 * n,), generator=gen, device="cuda")).values
@@ -48,6 +50,8 @@ CASES = [
     (2048, 9000, 9001, 8, 1, "bf16", "bf16", "bf16", "one", "f32"),
     (1200, 5762, 286, 48, 3, "f16", "f16", "f32", "runs", None),
     (20000, 700, 520, 4, 7, "f16", "e4m3", "f32", "runs", "f16"),
+    (3000, 3000, 2500, 64, 6, "bf16", "e4m3", "f32", "turns", "bf16"),
+    (2048, 4100, 4001, 16, 3, "f16", "f16", "f16", "turns", None),
     (40, 28672, 14336, 16, 2, "bf16", "bf16", "f32", "any", "bf16"),
 ]
 
