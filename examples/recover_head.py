@@ -5,10 +5,11 @@ fine-tuned versions of it, W + D_0 and W + D_1.  Their answers are kept as the
 top lists of token_logprobs; low-rank adapters beside the quantized head are
 trained on them with distill_topk (lora_add makes the student's logits and
 distill_topk turns them into their gradient in place, which lora_grad takes to
-the adapters with the hidden states kept in 8 bits); then tokens that want the
-one or the other are served together by w4a16_lora_matmul and scored.
+the adapters, with the hidden states as they are or, to save memory, kept in
+8 bits); then tokens that want the one or the other are served together by
+w4a16_lora_matmul and scored.
 
-    python examples/recover_head.py [--steps 60]
+    python examples/recover_head.py [--steps 60] [--keep-8-bit]
 """
 import argparse
 import os
@@ -32,12 +33,14 @@ def quantize_head(W, X, group_size=128):
 
 
 def gradients(kept, A, B, adapter, scale, dlogits, out=None, ws=None):
-    """Gradients of every adapter's factors from the logits' and the hidden states as fp8_quantize keeps them."""
-    g = P.lora_grad(kept["codes"], dlogits, A, B, adapter, scale, x_scales=kept["scales"], out=out, ws=ws)
+    """Gradients of every adapter's factors from the logits' and the hidden states: as they are, or fp8_quantize's."""
+    x, x_scales = (kept["codes"], kept["scales"]) if isinstance(kept, dict) else (kept, None)
+    g = P.lora_grad(x, dlogits, A, B, adapter, scale, x_scales=x_scales, out=out, ws=ws)
     return g["dA"], g["dB"]
 
 
-def run(steps=60, hidden=512, vocab=8192, tokens=2048, rank=16, k=32, temperature=1.0, seed=0, show=print):
+def run(steps=60, hidden=512, vocab=8192, tokens=2048, rank=16, k=32, temperature=1.0, seed=0, show=print,
+        keep_8_bit=False):
     gen = torch.Generator(device="cuda").manual_seed(seed)
 
     def randn(*shape, scale=1.0):
@@ -70,7 +73,7 @@ def run(steps=60, hidden=512, vocab=8192, tokens=2048, rank=16, k=32, temperatur
     loss, ws = P.distill_topk_buffers(logits, k, want_grad=False)
     loss["grad"] = logits                                                    # the gradient replaces the logits
     weight = torch.full((tokens,), 1.0 / tokens, device="cuda")
-    kept = P.fp8_quantize(X)
+    kept = P.fp8_quantize(X) if keep_8_bit else X
     grads, ws_grad = P.lora_grad_buffers(X, logits, A, B)
     history = []
     for step in range(steps + 1):
@@ -109,4 +112,6 @@ def run(steps=60, hidden=512, vocab=8192, tokens=2048, rank=16, k=32, temperatur
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
-    run(ap.parse_args().steps)
+    ap.add_argument("--keep-8-bit", action="store_true")
+    args = ap.parse_args()
+    run(args.steps, keep_8_bit=args.keep_8_bit)
