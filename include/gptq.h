@@ -621,9 +621,10 @@ gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_sca
  *             be dX itself (ld_b == ld_dx).
  *   workspace gptq_lora_grad_workspace_size bytes, 256-byte aligned; calls sharing one
  *             workspace must be stream-ordered.
- * fp32 accumulation.  U and T, and values of fp32 dY, enter the sums with 24 bits;
- * everything else enters exactly.  A NaN or an infinity in a token
- * reaches its adapter's gradients as NaN or infinity, and no other adapter's.  Results
+ * fp32 accumulation.  U and T, and values of fp32 dY, enter the sums with 24 bits
+ * (magnitudes below 2^-109 with fewer, from 2^128 - 2^119 on as infinite); everything
+ * else enters exactly.  A NaN or an infinity in a token reaches its adapter's gradients
+ * as NaN or infinity, and no other adapter's.  Results
  * are bitwise reproducible for given inputs.  M = 0 writes zeros to dA and dB. */
 gptq_status gptq_lora_grad(const void* X, int32_t x_dtype, const uint8_t* x_scales, int64_t M, int64_t d_in,
                            int64_t ld_x, const void* dY, int32_t dy_dtype, int64_t d_out, int64_t ld_dy, const void* A,
