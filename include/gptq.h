@@ -622,7 +622,7 @@ gptq_status gptq_fp8_matmul(const void* X, int32_t x_dtype, const uint8_t* x_sca
  *   workspace gptq_lora_grad_workspace_size bytes, 256-byte aligned; calls sharing one
  *             workspace must be stream-ordered.
  * fp32 accumulation.  U and T, and values of fp32 dY, enter the sums with 24 bits
- * (magnitudes below 2^-109 with fewer, from 2^128 - 2^119 on as infinite); everything
+ * (magnitudes below 2^-102 with fewer, from 2^128 - 2^119 on as infinite); everything
  * else enters exactly.  A NaN or an infinity in a token reaches its adapter's gradients
  * as NaN or infinity, and no other adapter's.  Results
  * are bitwise reproducible for given inputs.  M = 0 writes zeros to dA and dB. */

@@ -565,7 +565,7 @@ constexpr int kF8Few = 16;
 constexpr int64_t kF8FewRows = 4096, kF8FewValues = 1 << 16;
 // Tiles of 256 by 256 if every CU gets one and they are more than half full: 4096 ->
 // 131072, bf16 (and fp32) in tiles of 256 and in the smaller ones, us: 16 tokens 153 (221)
-// and 126 (129), 100 tokens 183 (231) and 146 (165), 200 tokens 185 (247) and 221 (284).
+// and 126 (129), 100 tokens 183 (231) and 155 (165), 200 tokens 185 (247) and 221 (284).
 // Tiles of 128 tokens if two of them for every CU remain, else 64 (or 32), bf16, us:
 // 300 x 4096 -> 14336 56 and 50, 2048 x 4096 -> 4096 61 and 69.  The sum is split until
 // every CU has a workgroup, into parts of four blocks or more: 65 x 4096 -> 4096 in 1, 4

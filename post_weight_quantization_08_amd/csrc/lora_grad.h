@@ -94,7 +94,9 @@ struct Eight {
       __builtin_memcpy(w, __builtin_assume_aligned(static_cast<const uint16_t*>(row) + k, 2), 16);
     }
   }
-  // zero behind the row's end
+  // zero behind the row's end.  Where a row ends inside eight its last numbers are loaded one by
+  // one, and the compiler waits for each: 8192 x 11001 -> 4093, codes, 64 ranks 401 us, 11008 ->
+  // 4096 236.
   __device__ __forceinline__ void load_end(const void* row, int k, int n) {
     if (k + 8 <= n) {
       load(row, k);
